@@ -8,6 +8,7 @@ missing, every call raises.  The helpers at the end (``pack``, ``unpack``,
 ``quantize``, ``linear``) allocate their outputs with torch and then call the same
 entry points.
 """
+import collections
 import ctypes
 import os
 
@@ -78,6 +79,21 @@ def lib():
         L.tri_probe_rows.restype = i32
         L.tri_probe_stream.argtypes = [p, i64, i32, i32, p, p]
         L.tri_probe_stream.restype = i32
+        L.tri_int4_bytes.argtypes = [i64, i64, i32, i32]
+        L.tri_int4_bytes.restype = i64
+        L.tri_int4_pack.argtypes = [p, p, p, i64, i64, i32, p, p]
+        L.tri_int4_unpack.argtypes = [p, i64, i64, i32, i32, p, p, p, p]
+        L.tri_int4_quantize.argtypes = [p, i64, i64, i32, i32, p, p]
+        L.tri_int4_linear.argtypes = [p, p, i64, i64, i64, i32, i32, p, p, p]
+        L.tri_experts_route_workspace_bytes.argtypes = [i64, i32, i32]
+        L.tri_experts_route_workspace_bytes.restype = i64
+        L.tri_experts_route.argtypes = [p, i32, i64, i32, i32, i32, p, p, p, p, p, p, i64, p]
+        L.tri_experts_linear.argtypes = [p, i64, p, p, i64, p, p, i32, i64, i64, i32, p, p]
+        L.tri_experts_pair.argtypes = [p, i64, p, p, i64, p, p, p, p, i32, i64, i64, i32, p, p]
+        L.tri_experts_combine.argtypes = [p, i64, p, p, p, i64, i32, i64, p, p]
+        for name in ("tri_int4_pack", "tri_int4_unpack", "tri_int4_quantize", "tri_int4_linear", "tri_experts_route",
+                     "tri_experts_linear", "tri_experts_pair", "tri_experts_combine"):
+            getattr(L, name).restype = i32
         _lib = L
     return _lib
 
@@ -183,6 +199,62 @@ def tri_linear_fused(X, Wps, scales, M, Ns, K, fmt, Ys, norm=False, gain=None, e
                                          ctypes.byref(glue), _stream(stream)), "tri_linear_fused")
 
 
+TRI_MAX_EXPERTS, TRI_MAX_TOPK = 256, 16
+TRI_F16, TRI_F32 = 0, 1
+
+
+def tri_int4_bytes(N, K, group, zeros):
+    return int(lib().tri_int4_bytes(int(N), int(K), int(group), 1 if zeros else 0))
+
+
+def tri_int4_pack(Q, S, Z, N, K, group, Wp, stream=None):
+    return _check(lib().tri_int4_pack(_ptr(Q), _ptr(S), _ptr(Z), int(N), int(K), int(group), _ptr(Wp),
+                                      _stream(stream)), "tri_int4_pack")
+
+
+def tri_int4_unpack(Wp, N, K, group, zeros, Q, S, Z, stream=None):
+    return _check(lib().tri_int4_unpack(_ptr(Wp), int(N), int(K), int(group), 1 if zeros else 0, _ptr(Q), _ptr(S),
+                                        _ptr(Z), _stream(stream)), "tri_int4_unpack")
+
+
+def tri_int4_quantize(W, N, K, group, zeros, Wp, stream=None):
+    return _check(lib().tri_int4_quantize(_ptr(W), int(N), int(K), int(group), 1 if zeros else 0, _ptr(Wp),
+                                          _stream(stream)), "tri_int4_quantize")
+
+
+def tri_int4_linear(X, Wp, M, N, K, group, zeros, residual, Y, stream=None):
+    return _check(lib().tri_int4_linear(_ptr(X), _ptr(Wp), int(M), int(N), int(K), int(group), 1 if zeros else 0,
+                                        _ptr(residual), _ptr(Y), _stream(stream)), "tri_int4_linear")
+
+
+def tri_experts_route_workspace_bytes(T, E, topk):
+    return int(lib().tri_experts_route_workspace_bytes(int(T), int(E), int(topk)))
+
+
+def tri_experts_route(logits, dtype, T, E, topk, renorm, ids, weights, offsets, rows, pos, workspace, workspace_bytes,
+                      stream=None):
+    return _check(lib().tri_experts_route(_ptr(logits), int(dtype), int(T), int(E), int(topk), 1 if renorm else 0,
+                                          _ptr(ids), _ptr(weights), _ptr(offsets), _ptr(rows), _ptr(pos),
+                                          _ptr(workspace), int(workspace_bytes), _stream(stream)), "tri_experts_route")
+
+
+def tri_experts_linear(X, T, offsets, rows, R, Wp, scale, E, N, K, fmt, Y, stream=None):
+    return _check(lib().tri_experts_linear(_ptr(X), int(T), _ptr(offsets), _ptr(rows), int(R), _ptr(Wp), _ptr(scale),
+                                           int(E), int(N), int(K), int(fmt), _ptr(Y), _stream(stream)),
+                  "tri_experts_linear")
+
+
+def tri_experts_pair(X, T, offsets, rows, R, Wp, scale, Wp_up, scale_up, E, N, K, fmt, Y, stream=None):
+    return _check(lib().tri_experts_pair(_ptr(X), int(T), _ptr(offsets), _ptr(rows), int(R), _ptr(Wp), _ptr(scale),
+                                         _ptr(Wp_up), _ptr(scale_up), int(E), int(N), int(K), int(fmt), _ptr(Y),
+                                         _stream(stream)), "tri_experts_pair")
+
+
+def tri_experts_combine(Z, R, pos, weights, residual, T, topk, N, Y, stream=None):
+    return _check(lib().tri_experts_combine(_ptr(Z), int(R), _ptr(pos), _ptr(weights), _ptr(residual), int(T),
+                                            int(topk), int(N), _ptr(Y), _stream(stream)), "tri_experts_combine")
+
+
 def tri_select_algo(M, N, K, fmt):
     return int(lib().tri_select_algo(int(M), int(N), int(K), int(fmt)))
 
@@ -262,4 +334,215 @@ def linear(X, Wp, scale, K, fmt, algo=TRI_ALGO_AUTO, out=None, stream=None):
         tri_linear(X, Wp, scale, M, N, K, fmt, Y, stream)
     else:
         tri_linear_algo(X, Wp, scale, M, N, K, fmt, Y, algo, stream)
+    return Y
+
+
+# The helpers below take the tensors' device (whichever device is current) and its current stream, or `stream`; they
+# raise ValueError for tensors of another type, shape, device or layout than they name.
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _launch(name, device, stream, *args):
+    """The entry point `name` on `device` (an ordinal) with the stream appended."""
+    import torch
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(name, device, stream, *args)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    rc = getattr(lib(), name)(*args, handle)
+    if rc != TRI_OK:
+        raise TriError(rc, name)
+
+
+def _tensors(device, dtype, **named):
+    """Every named tensor (None is left out) is of `dtype`, contiguous and on `device`."""
+    for name, t in named.items():
+        if t is not None and not (t.dtype == dtype and t.get_device() == device and t.is_contiguous()):
+            raise ValueError("%s must be a contiguous %s tensor on device %d" % (name, dtype, device))
+
+
+def _keep(t, stream):
+    """Tell torch's allocator that temporary `t` is used on a stream that the caller named."""
+    import torch
+    if stream is not None:
+        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        t.record_stream(torch.cuda.ExternalStream(h, device=t.device))
+
+
+def int4_pack(Q, S, group, Z=None, stream=None):
+    """Lay out 4-bit codes Q (N, K) uint8 with group scales S (N, ceil(K/group)) float16 and, optionally, zero points
+    Z of S's shape uint8 (8 everywhere without); returns a new uint8 tensor for int4_linear."""
+    import torch
+    _need(Q.is_cuda and Q.dim() == 2 and Q.numel() > 0, "Q must be an (N, K) tensor on the GPU")
+    (N, K), dev = Q.shape, Q.get_device()
+    _tensors(dev, torch.uint8, Q=Q, Z=Z)
+    _tensors(dev, torch.float16, S=S)
+    nbytes = tri_int4_bytes(N, K, group, Z is not None)
+    _need(nbytes > 0, "group must be 32, 64 or 128 (and the matrix below 2^22 tiles)")
+    shape = (N, -(-K // group))
+    _need(S.shape == shape and (Z is None or Z.shape == shape), "S and Z must be (N, ceil(K/group))")
+    Wp = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+    _launch("tri_int4_pack", dev, stream, Q.data_ptr(), S.data_ptr(), None if Z is None else Z.data_ptr(), N, K, group,
+            Wp.data_ptr())
+    return Wp
+
+
+def int4_unpack(Wp, N, K, group, zeros=False, stream=None):
+    """The codes, scales and zero points (None where zeros is false) of a packed 4-bit matrix."""
+    import torch
+    _need(Wp.is_cuda, "Wp must be on the GPU")
+    dev = Wp.get_device()
+    _tensors(dev, torch.uint8, Wp=Wp)
+    nbytes = tri_int4_bytes(N, K, group, zeros)
+    _need(nbytes > 0 and Wp.numel() == nbytes, "Wp does not hold tri_int4_bytes(N, K, group, zeros) bytes")
+    shape = (N, -(-K // group))
+    Q = torch.empty((N, K), dtype=torch.uint8, device=Wp.device)
+    S = torch.empty(shape, dtype=torch.float16, device=Wp.device)
+    Z = torch.empty(shape, dtype=torch.uint8, device=Wp.device) if zeros else None
+    _launch("tri_int4_unpack", dev, stream, Wp.data_ptr(), N, K, group, 1 if zeros else 0, Q.data_ptr(), S.data_ptr(),
+            None if Z is None else Z.data_ptr())
+    return Q, S, Z
+
+
+def int4_quantize(W, group, zeros=False, stream=None):
+    """Quantise an (N, K) float32 tensor to 4-bit codes with group scales (and zero points), laid out for int4_linear."""
+    import torch
+    _need(W.is_cuda and W.dim() == 2 and W.numel() > 0, "W must be an (N, K) tensor on the GPU")
+    (N, K), dev = W.shape, W.get_device()
+    _tensors(dev, torch.float32, W=W)
+    nbytes = tri_int4_bytes(N, K, group, zeros)
+    _need(nbytes > 0, "group must be 32, 64 or 128 (and the matrix below 2^22 tiles)")
+    Wp = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+    _launch("tri_int4_quantize", dev, stream, W.data_ptr(), N, K, group, 1 if zeros else 0, Wp.data_ptr())
+    return Wp
+
+
+def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=None):
+    """Y = fp16(residual + X @ W.T) for an (M, K) fp16 tensor X and a packed 4-bit matrix of N rows.  `residual` may be
+    `out` itself."""
+    import torch
+    _need(X.is_cuda and X.dim() == 2 and X.numel() > 0, "X must be an (M, K) tensor on the GPU")
+    (M, K), dev = X.shape, X.get_device()
+    Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=X.device)
+    _tensors(dev, torch.float16, X=X, out=Y, residual=residual)
+    _tensors(dev, torch.uint8, Wp=Wp)
+    _need(Wp.numel() == tri_int4_bytes(N, K, group, zeros),
+          "Wp does not hold tri_int4_bytes(N, K, group, zeros) bytes for X's width")
+    _need(Y.shape == (M, N) and (residual is None or residual.shape == (M, N)), "out and residual must be (M, N)")
+    _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0,
+            None if residual is None else residual.data_ptr(), Y.data_ptr())
+    return Y
+
+
+class Routing(collections.namedtuple("Routing", "ids weights offsets rows pos")):
+    """What experts_route gives: ids, weights and pos (T, topk), offsets (E + 1), rows (T * topk)."""
+
+
+def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=None):
+    """The top-k experts of every row of (T, E) float16 or float32 logits, their weights, and the order of the (token,
+    expert) pairs by expert, as a Routing (the tensors of `out`, if it is given).  `workspace`: a uint8 tensor of at
+    least tri_experts_route_workspace_bytes(T, E, topk) bytes; allocated where it is None."""
+    import torch
+    _need(logits.is_cuda and logits.dim() == 2 and logits.is_contiguous() and
+          logits.dtype in (torch.float16, torch.float32), "logits must be a contiguous (T, E) float16 or float32 tensor on the GPU")
+    (T, E), dev = logits.shape, logits.get_device()
+    need = tri_experts_route_workspace_bytes(T, E, topk)
+    _need(need >= 0, "1 <= E <= %d, 1 <= topk <= min(E, %d) and T * topk < 2^31 are taken" % (TRI_MAX_EXPERTS, TRI_MAX_TOPK))
+    if out is None:
+        i32 = dict(dtype=torch.int32, device=logits.device)
+        out = Routing(torch.empty((T, topk), **i32), torch.empty((T, topk), dtype=torch.float32, device=logits.device),
+                      torch.empty(E + 1, **i32), torch.empty(T * topk, **i32), torch.empty((T, topk), **i32))
+    else:
+        _tensors(dev, torch.int32, ids=out.ids, offsets=out.offsets, rows=out.rows, pos=out.pos)
+        _tensors(dev, torch.float32, weights=out.weights)
+        _need(out.ids.shape == out.weights.shape == out.pos.shape == (T, topk) and out.offsets.shape == (E + 1,) and
+              out.rows.shape == (T * topk,), "out: ids, weights, pos (T, topk), offsets (E + 1), rows (T * topk)")
+    temporary = workspace is None and need > 0
+    if temporary:
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    if workspace is not None:
+        _tensors(dev, torch.uint8, workspace=workspace)
+    _launch("tri_experts_route", dev, stream, logits.data_ptr(), TRI_F16 if logits.dtype == torch.float16 else TRI_F32, T, E,
+            topk, 1 if renorm else 0, out.ids.data_ptr(), out.weights.data_ptr(), out.offsets.data_ptr(),
+            out.rows.data_ptr(), out.pos.data_ptr(), None if workspace is None else workspace.data_ptr(),
+            0 if workspace is None else workspace.numel())
+    if temporary:
+        _keep(workspace, stream)
+    return out
+
+
+def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
+    import torch
+    _need(X.is_cuda and X.dim() == 2 and X.numel() > 0 and X.shape[1] == K, "X must be a (T, K) tensor on the GPU")
+    T, dev = X.shape[0], X.get_device()
+    Wp = mats[0][0]
+    _need(Wp.dim() == 3, "packed weights must be (E, N, row_bytes)")
+    E, N = Wp.shape[0], Wp.shape[1]
+    R = T if rows is None else rows.shape[0]
+    Y = out if out is not None else torch.empty((R, N), dtype=torch.float16, device=X.device)
+    _tensors(dev, torch.float16, X=X, out=Y)
+    _tensors(dev, torch.int32, offsets=offsets, rows=rows)
+    _need(offsets.shape == (E + 1,) and (rows is None or rows.dim() == 1), "offsets must be (E + 1), rows one-dimensional")
+    _need(Y.dim() == 2 and Y.shape[0] >= R and Y.shape[1] == N, "out must be (R, N)")
+    args = []
+    for W, scale in mats:
+        _tensors(dev, torch.uint8, weights=W)
+        _tensors(dev, torch.float32, scale=scale)
+        _need(W.shape == (E, N, tri_row_bytes(K, fmt)) and scale.numel() == E,
+              "weights must be (E, N, tri_row_bytes(K, fmt)), scales (E)")
+        args += [W.data_ptr(), scale.data_ptr()]
+    _launch(name, dev, stream, X.data_ptr(), T, offsets.data_ptr(), None if rows is None else rows.data_ptr(), R, *args, E,
+            N, K, fmt, Y.data_ptr())
+    return Y
+
+
+def experts_linear(X, offsets, rows, Wp, scale, K, fmt, out=None, stream=None):
+    """Y[r] = fp16(scale[e] * X[rows[r]] @ W_e.T) for the places r of expert e, offsets[e] <= r < offsets[e + 1] (rows
+    None: X[r]).  Wp: (E, N, row_bytes) uint8, scale: (E) float32 on the device, offsets, rows: as experts_route gives
+    them.  Rows of a new Y behind offsets[E] are not written; those of `out` stay as they are."""
+    return _experts("tri_experts_linear", X, offsets, rows, ((Wp, scale),), K, fmt, out, stream)
+
+
+def experts_pair(X, offsets, rows, Wp_gate, scale_gate, Wp_up, scale_up, K, fmt, out=None, stream=None):
+    """experts_linear with two matrices per expert: Y[r] = fp16(silu(gate) * up)."""
+    return _experts("tri_experts_pair", X, offsets, rows, ((Wp_gate, scale_gate), (Wp_up, scale_up)), K, fmt, out, stream)
+
+
+def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
+    """Y[t] = fp16(residual[t] + sum_j weights[t, j] * Z[pos[t, j]]); pairs with pos outside Z are left out.  `residual`
+    may be `out` itself."""
+    import torch
+    _need(Z.is_cuda and Z.dim() == 2 and Z.numel() > 0 and pos.dim() == 2, "Z must be an (R, N) tensor on the GPU, pos (T, topk)")
+    (R, N), (T, topk), dev = Z.shape, pos.shape, Z.get_device()
+    Y = out if out is not None else torch.empty((T, N), dtype=torch.float16, device=Z.device)
+    _tensors(dev, torch.float16, Z=Z, residual=residual, out=Y)
+    _tensors(dev, torch.int32, pos=pos)
+    _tensors(dev, torch.float32, weights=weights)
+    _need(weights.shape == (T, topk) and Y.shape == (T, N) and (residual is None or residual.shape == (T, N)),
+          "weights must be (T, topk), out and residual (T, N)")
+    _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(),
+            None if residual is None else residual.data_ptr(), T, topk, N, Y.data_ptr())
+    return Y
+
+
+def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None, stream=None):
+    """A gated MLP of experts: for every row of X, the weighted sum over its top-k experts of
+    down(silu(gate(x)) * up(x)), plus `residual`.  gate, up and down are (packed weights, scales) as experts_pair and
+    experts_linear take them, logits (T, E) as experts_route takes them.  Four launches or a few more, no waiting."""
+    import torch
+    (T, hidden), inner = X.shape, gate[0].shape[1]
+    r = experts_route(logits, topk, renorm=renorm, stream=stream)
+    H = torch.empty((T * topk, inner), dtype=torch.float16, device=X.device)
+    Z = torch.empty((T * topk, down[0].shape[1]), dtype=torch.float16, device=X.device)
+    experts_pair(X, r.offsets, r.rows, *gate, *up, hidden, fmt, out=H, stream=stream)
+    experts_linear(H, r.offsets, None, *down, inner, fmt, out=Z, stream=stream)
+    Y = experts_combine(Z, r.pos, r.weights, residual=residual, stream=stream)
+    for t in r + (H, Z):
+        _keep(t, stream)
     return Y

@@ -8,6 +8,8 @@ static_assert(TRI_MAX_GROUPS == kMaxGroups, "group table size");
 namespace {
 
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool misaligned_to(const void *p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+bool known_group(int group) { return group == 32 || group == 64 || group == 128; }
 bool known_fmt(int fmt) { return fmt == TRI_FMT_2BIT || fmt == TRI_FMT_1P6BIT; }
 constexpr int64_t kMaxDim = (int64_t)1 << 31;   // K, N and one packed row are indexed with 32-bit ints
 
@@ -89,6 +91,35 @@ int run_linear(const _Float16 *X, const uint8_t *Wp, float scale, int64_t M, int
     default:
         return TRI_EINVAL;
     }
+}
+
+int run_experts(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R, const uint8_t *Wp,
+                const float *scale, const uint8_t *Wp_up, const float *scale_up, bool pair, int E, int64_t N, int64_t K,
+                int fmt, _Float16 *Y, hipStream_t s)
+{
+    if (!X || !offsets || !Wp || !scale || !Y || (pair && (!Wp_up || !scale_up)) || !known_fmt(fmt)) return TRI_EINVAL;
+    if (T < 1 || R < 1 || N < 1 || K < 1 || T >= kMaxDim || R >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+        return TRI_EINVAL;
+    if (E < 1 || E > TRI_MAX_EXPERTS || (!rows && T < R)) return TRI_EINVAL;
+    if (rows && T > (((int64_t)1 << 31) - 8) / K) return TRI_EINVAL;   // gathered rows: 32-bit buffer offsets
+    if (misaligned(X) || misaligned(Wp) || misaligned(Wp_up) || misaligned(Y)) return TRI_EALIGN;
+    if (misaligned_to(offsets, 4) || misaligned_to(rows, 4) || misaligned_to(scale, 4) || misaligned_to(scale_up, 4))
+        return TRI_EALIGN;
+    Experts ex{};
+    ex.X = reinterpret_cast<const uint16_t *>(X);
+    ex.offsets = offsets;
+    ex.rows = rows;
+    ex.Wp[0] = Wp;
+    ex.Wp[1] = Wp_up;
+    ex.scale[0] = scale;
+    ex.scale[1] = scale_up;
+    ex.Y = reinterpret_cast<uint16_t *>(Y);
+    ex.T = (int)T;
+    ex.R = (int)R;
+    ex.E = E;
+    ex.N = (int)N;
+    ex.K = (int)K;
+    return launch_experts(ex, fmt, s);
 }
 
 }  // namespace
@@ -260,6 +291,93 @@ int tri_linear_fused(const _Float16 *X, const uint8_t *const *Wp, const float *s
                      launch_mvm(x, gr, (int)M, (int)K, fmt, stream, &fu);
     if (!done) return TRI_EINVAL;                // a shape the glue variants do not serve
     return hipGetLastError() == hipSuccess ? TRI_OK : TRI_EHIP;
+}
+
+int64_t tri_int4_bytes(int64_t N, int64_t K, int group, int zeros)
+{
+    if (N < 1 || K < 1 || N >= kMaxDim || K >= kMaxDim || !known_group(group)) return -1;
+    return int4_bytes(N, K, group, zeros != 0);
+}
+
+int tri_int4_pack(const uint8_t *Q, const _Float16 *S, const uint8_t *Z, int64_t N, int64_t K, int group, uint8_t *Wp,
+                  hipStream_t stream)
+{
+    if (!Q || !S || !Wp || tri_int4_bytes(N, K, group, Z != nullptr) < 0) return TRI_EINVAL;
+    if (misaligned(Wp) || misaligned_to(S, 2)) return TRI_EALIGN;
+    return launch_int4_pack(Q, reinterpret_cast<const uint16_t *>(S), Z, (int)N, (int)K, group, Wp, stream);
+}
+
+int tri_int4_unpack(const uint8_t *Wp, int64_t N, int64_t K, int group, int zeros, uint8_t *Q, _Float16 *S, uint8_t *Z,
+                    hipStream_t stream)
+{
+    if (!Wp || !Q || !S || (zeros && !Z) || tri_int4_bytes(N, K, group, zeros) < 0) return TRI_EINVAL;
+    if (misaligned(Wp) || misaligned_to(S, 2)) return TRI_EALIGN;
+    return launch_int4_unpack(Wp, (int)N, (int)K, group, zeros != 0, Q, reinterpret_cast<uint16_t *>(S), Z, stream);
+}
+
+int tri_int4_quantize(const float *W, int64_t N, int64_t K, int group, int zeros, uint8_t *Wp, hipStream_t stream)
+{
+    if (!W || !Wp || tri_int4_bytes(N, K, group, zeros) < 0) return TRI_EINVAL;
+    if (misaligned(Wp) || misaligned_to(W, 4)) return TRI_EALIGN;
+    return launch_int4_quantize(W, (int)N, (int)K, group, zeros != 0, Wp, stream);
+}
+
+int tri_int4_linear(const _Float16 *X, const uint8_t *Wp, int64_t M, int64_t N, int64_t K, int group, int zeros,
+                    const _Float16 *residual, _Float16 *Y, hipStream_t stream)
+{
+    if (!X || !Wp || !Y || M < 1 || M >= kMaxDim || tri_int4_bytes(N, K, group, zeros) < 0) return TRI_EINVAL;
+    if (misaligned(X) || misaligned(Wp) || misaligned(residual) || misaligned(Y)) return TRI_EALIGN;
+    return launch_int4_linear(reinterpret_cast<const uint16_t *>(X), Wp, (int)M, (int)N, (int)K, group, zeros != 0,
+                              reinterpret_cast<const uint16_t *>(residual), reinterpret_cast<uint16_t *>(Y), stream);
+}
+
+int64_t tri_experts_route_workspace_bytes(int64_t T, int E, int topk)
+{
+    if (T < 1 || E < 1 || E > TRI_MAX_EXPERTS || topk < 1 || topk > E || topk > TRI_MAX_TOPK || T >= kMaxDim / 16 ||
+        T * topk >= kMaxDim)
+        return -1;
+    return route_workspace_bytes(T, E, topk);
+}
+
+int tri_experts_route(const void *logits, int dtype, int64_t T, int E, int topk, int renorm, int32_t *ids,
+                      float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                      int64_t workspace_bytes, hipStream_t stream)
+{
+    const int64_t need = tri_experts_route_workspace_bytes(T, E, topk);
+    if (need < 0 || (dtype != TRI_F16 && dtype != TRI_F32)) return TRI_EINVAL;
+    if (!logits || !ids || !weights || !offsets || !rows || !pos) return TRI_EINVAL;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return TRI_EINVAL;
+    if (misaligned_to(logits, dtype == TRI_F16 ? 2 : 4) || misaligned_to(ids, 4) || misaligned_to(weights, 4) ||
+        misaligned_to(offsets, 4) || misaligned_to(rows, 4) || misaligned_to(pos, 4) || misaligned(workspace))
+        return TRI_EALIGN;
+    return launch_route(logits, dtype == TRI_F16, (int)T, E, topk, renorm != 0, ids, weights, offsets, rows, pos,
+                        workspace, stream);
+}
+
+int tri_experts_linear(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,
+                       const uint8_t *Wp, const float *scale, int E, int64_t N, int64_t K, int fmt, _Float16 *Y,
+                       hipStream_t stream)
+{
+    return run_experts(X, T, offsets, rows, R, Wp, scale, nullptr, nullptr, false, E, N, K, fmt, Y, stream);
+}
+
+int tri_experts_pair(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,
+                     const uint8_t *Wp, const float *scale, const uint8_t *Wp_up, const float *scale_up, int E,
+                     int64_t N, int64_t K, int fmt, _Float16 *Y, hipStream_t stream)
+{
+    return run_experts(X, T, offsets, rows, R, Wp, scale, Wp_up, scale_up, true, E, N, K, fmt, Y, stream);
+}
+
+int tri_experts_combine(const _Float16 *Z, int64_t R, const int32_t *pos, const float *weights,
+                        const _Float16 *residual, int64_t T, int topk, int64_t N, _Float16 *Y, hipStream_t stream)
+{
+    if (!Z || !pos || !weights || !Y || R < 1 || T < 1 || N < 1 || topk < 1 || topk > TRI_MAX_TOPK) return TRI_EINVAL;
+    if (R >= kMaxDim || T >= kMaxDim || N >= kMaxDim) return TRI_EINVAL;
+    if (misaligned(Z) || misaligned(residual) || misaligned(Y) || misaligned_to(pos, 4) || misaligned_to(weights, 4))
+        return TRI_EALIGN;
+    return launch_combine(reinterpret_cast<const uint16_t *>(Z), R, pos, weights,
+                          reinterpret_cast<const uint16_t *>(residual), (int)T, topk, (int)N,
+                          reinterpret_cast<uint16_t *>(Y), stream);
 }
 
 const char *tri_status_string(int code)

@@ -178,6 +178,30 @@ bool launch_decode(const uint16_t *X, const uint8_t *Wp, float scale, int M, int
                    hipStream_t s);
 int launch_gemm(const uint16_t *X, const uint8_t *Wp, float scale, int64_t M, int N, int K, int fmt, uint16_t *Y,
                 hipStream_t s);
+// 4-bit layers (tri_int4.hip).
+int64_t int4_bytes(int64_t N, int64_t K, int group, bool zeros);
+int launch_int4_pack(const uint8_t *Q, const uint16_t *S, const uint8_t *Z, int N, int K, int group, uint8_t *Wp,
+                     hipStream_t s);
+int launch_int4_unpack(const uint8_t *Wp, int N, int K, int group, bool zeros, uint8_t *Q, uint16_t *S, uint8_t *Z,
+                       hipStream_t s);
+int launch_int4_quantize(const float *W, int N, int K, int group, bool zeros, uint8_t *Wp, hipStream_t s);
+int launch_int4_linear(const uint16_t *X, const uint8_t *Wp, int M, int N, int K, int group, bool zeros,
+                       const uint16_t *R, uint16_t *Y, hipStream_t s);
+// Experts (tri_experts.hip).  An expert's product: one matrix per expert, or two (the gated pair).
+struct Experts {
+    const uint16_t *X;
+    const int32_t *offsets, *rows;               // rows null: X is in the order of the places
+    const uint8_t *Wp[2];                        // [1] null: one matrix
+    const float *scale[2];
+    uint16_t *Y;
+    int T, R, E, N, K;
+};
+int64_t route_workspace_bytes(int64_t T, int E, int topk);
+int launch_route(const void *logits, bool half, int T, int E, int topk, bool renorm, int32_t *ids, float *weights,
+                 int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace, hipStream_t s);
+int launch_experts(const Experts &ex, int fmt, hipStream_t s);
+int launch_combine(const uint16_t *Z, int64_t R, const int32_t *pos, const float *weights, const uint16_t *res, int T,
+                   int topk, int N, uint16_t *Y, hipStream_t s);
 int launch_probe_read(const void *src, int64_t bytes, uint32_t *sink, hipStream_t s);
 int launch_probe_copy(const void *src, void *dst, int64_t bytes, hipStream_t s);
 int launch_probe_empty(int64_t workgroups, int threads, uint32_t *sink, hipStream_t s);

@@ -202,6 +202,119 @@ int tri_linear_fused(const _Float16 *X, const uint8_t *const *Wp, const float *s
                      const int64_t *N, int64_t K, int fmt, _Float16 *const *Y, int G,
                      const tri_glue *glue, hipStream_t stream);
 
+/* ---- 4-bit layers with group scales ---------------------------------------
+ * For the layers of a mixed-precision model that ternary weights do not serve: 4-bit codes
+ * with one fp16 scale, and optionally one zero point, per group of `group` consecutive
+ * weights of a row,
+ *
+ *     W[n][k] = S[n][k / group] * (Q[n][k] - Z[n][k / group]),   Q, Z in 0..15,
+ *
+ * Z = 8 everywhere where a matrix is stored without zero points (zeros == 0).  group is 32,
+ * 64 or 128.
+ *
+ * Layout of a packed matrix (tri_int4_bytes bytes), with NB = ceil(N/16) blocks of 16 rows,
+ * KS = ceil(K/128) steps of 128 values and gps = 128/group groups per step:
+ *   codes   32-bit word ((b*KS + s)*64 + 16*g + j)*4 + p holds the eight values
+ *           k = 128 s + 32 p + 8 g + i (i < 8) of row 16 b + j, value i in the four bits from
+ *           bit 4*(i/2) + 16*(i%2): the tile of a block and a step is 1 KB in a row, and the
+ *           word that lane 16 g + j of a wave feeds to a matrix instruction is whole;
+ *   scales  fp16 ((b*KS + s)*16 + j)*gps + i: row 16 b + j, group i of step s;
+ *   zeros   (only if zeros != 0) bytes 0..15, indexed like the scales.
+ * Rows past N and values past K hold code 8, scale 0 and zero point 8; groups that begin past K
+ * likewise. */
+
+/* Bytes of a packed N x K matrix; -1 if a size is < 1 or >= 2^31, the group is unknown or the
+ * matrix has 2^22 tiles or more (8.6e9 weights; every call here rejects such a matrix). */
+int64_t tri_int4_bytes(int64_t N, int64_t K, int group, int zeros);
+
+/* Lay out codes that are given.  Q: N*K bytes (their low four bits count); S: N * ceil(K/group)
+ * fp16; Z: N * ceil(K/group) bytes (low four bits), or NULL for a matrix without zero points;
+ * all row-major.  Wp: tri_int4_bytes(N, K, group, Z != NULL) bytes, 16-byte aligned.
+ * Errors: TRI_EINVAL, TRI_EALIGN (Wp; S not 2-byte aligned), TRI_EHIP. */
+int tri_int4_pack(const uint8_t *Q, const _Float16 *S, const uint8_t *Z, int64_t N, int64_t K, int group,
+                  uint8_t *Wp, hipStream_t stream);
+
+/* The inverse of tri_int4_pack: writes Q, S and, if zeros != 0, Z (else Z is not used). */
+int tri_int4_unpack(const uint8_t *Wp, int64_t N, int64_t K, int group, int zeros, uint8_t *Q, _Float16 *S,
+                    uint8_t *Z, hipStream_t stream);
+
+/* Quantise full-precision weights to nearest, group by group, and lay them out.  W: N*K float32
+ * row-major, 4-byte aligned, finite.  In fp32, with m the group's largest |w| (zeros == 0):
+ *     S = fp16_rne(m / 7) (at most 65504),  Q = clip(round_half_even(w / S), -8, 7) + 8;
+ * with lo, hi the group's smallest and largest value, 0 included (zeros != 0):
+ *     S = fp16_rne((hi - lo) / 15) (at most 65504),  Z = clip(round_half_even(-lo / S), 0, 15),
+ *     Q = clip(round_half_even(w / S) + Z, 0, 15);
+ * a group whose S is 0 has Q = Z = 8.  Errors as tri_int4_pack. */
+int tri_int4_quantize(const float *W, int64_t N, int64_t K, int group, int zeros, uint8_t *Wp, hipStream_t stream);
+
+/* The 4-bit layer:  Y[m][n] = fp16_rne( residual[m][n] + sum_k W[n][k] X[m][k] ), accumulated in
+ * fp32 (codes minus zero points are exact in fp16; a group's sum is scaled in fp32).
+ * X: M*K fp16 row-major; Wp: as packed for this N, K, group and zeros; residual: M*N fp16 or
+ * NULL (it may be Y itself); Y: M*N fp16.  X, Wp, residual and Y must be 16-byte aligned; any M
+ * and K.  X is expected finite.
+ * Errors: TRI_EINVAL (a size < 1 or >= 2^31, null, unknown group), TRI_EALIGN, TRI_EHIP. */
+int tri_int4_linear(const _Float16 *X, const uint8_t *Wp, int64_t M, int64_t N, int64_t K, int group, int zeros,
+                    const _Float16 *residual, _Float16 *Y, hipStream_t stream);
+
+/* ---- Experts: ternary layers of which every row takes a few ----------------
+ * A router gives every token a logit per expert; the token takes the top-k of them.  The
+ * (token, expert) pairs are ordered by expert (tri_experts_route), the experts' products run
+ * over that order, whose ragged sizes stay on the device (tri_experts_linear,
+ * tri_experts_pair), and each token's results are weighted and added (tri_experts_combine).
+ * No call waits for the device, allocates, or reads anything back. */
+enum { TRI_MAX_EXPERTS = 256, TRI_MAX_TOPK = 16 };
+enum { TRI_F16 = 0, TRI_F32 = 1 };                /* types of logits */
+
+/* Workspace (device bytes) of tri_experts_route; -1 for sizes it does not take. */
+int64_t tri_experts_route_workspace_bytes(int64_t T, int E, int topk);
+
+/* logits: T*E row-major, fp16 (TRI_F16, 2-byte aligned) or fp32 (TRI_F32, 4-byte aligned).
+ * Token t takes its topk largest logits, the lower expert first among equal ones; a logit of
+ * -inf or NaN is never taken (a masked expert; a row of them is a token of padding).  Outputs:
+ *   ids      T*topk: the experts, largest logit first; -1 where fewer than topk can be taken;
+ *   weights  T*topk fp32: exp(x_j - max) / D, D the sum of exp(x - max) over the taken logits
+ *            (renorm != 0) or over all of the row (renorm == 0); 0 where ids is -1.  Logits of
+ *            +inf share the weight among themselves;
+ *   offsets  E+1: expert e owns the places offsets[e] .. offsets[e+1]-1 of the order by expert
+ *            (within one expert by token);
+ *   rows     T*topk: the token at each place; -1 behind offsets[E];
+ *   pos      T*topk: the place of pair (t, j); -1 where ids is -1.
+ * All are int32 but the weights, 4-byte aligned.  1 <= E <= TRI_MAX_EXPERTS,
+ * 1 <= topk <= min(E, TRI_MAX_TOPK), T < 2^27, T*topk < 2^31.  workspace: 16-byte aligned, at least
+ * tri_experts_route_workspace_bytes bytes, overwritten; NULL where that is 0.  Calls that share
+ * one must be ordered.  Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
+int tri_experts_route(const void *logits, int dtype, int64_t T, int E, int topk, int renorm, int32_t *ids,
+                      float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace,
+                      int64_t workspace_bytes, hipStream_t stream);
+
+/* For every place r of expert e:  Y[r][n] = fp16_rne( scale[e] * sum_k t_e[n][k] X[x(r)][k] ),
+ * x(r) = rows[r], or r itself where rows is NULL.  X: T*K fp16 (T >= R where rows is NULL); Wp: E
+ * packed N x K matrices one after another, as tri_pack2 / tri_pack16 give them (for one matrix
+ * of E*N rows, too); scale: E fp32 on the DEVICE (as tri_quantize writes them); offsets: E+1
+ * int32, not decreasing, at most R (values outside are clamped); rows: R int32; Y: R*N fp16.
+ * Rows of Y behind offsets[E] stay as they are, so do rows whose x(r) lies outside 0..T-1.  X,
+ * Wp and Y must be 16-byte aligned, the rest 4-byte.  1 <= E <= TRI_MAX_EXPERTS; with rows, X
+ * of at most 4 GiB - 16.  Y must not alias an input.  X is expected finite.
+ * Errors: TRI_EINVAL (a size < 1 or >= 2^31, null, unknown fmt), TRI_EALIGN, TRI_EHIP. */
+int tri_experts_linear(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,
+                       const uint8_t *Wp, const float *scale, int E, int64_t N, int64_t K, int fmt, _Float16 *Y,
+                       hipStream_t stream);
+
+/* tri_experts_linear's product with two matrices per expert, the gate and up projections of a
+ * gated MLP:  Y[r] = fp16_rne( silu(g) * u ),  g and u the fp32 results of the two (never rounded
+ * on their own), silu(z) = z / (1 + e^-z).  Wp_up and scale_up: as Wp and scale. */
+int tri_experts_pair(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,
+                     const uint8_t *Wp, const float *scale, const uint8_t *Wp_up, const float *scale_up, int E,
+                     int64_t N, int64_t K, int fmt, _Float16 *Y, hipStream_t stream);
+
+/* Y[t][n] = fp16_rne( residual[t][n] + sum_j weights[t][j] * Z[pos[t][j]][n] ), added in fp32, j
+ * rising; pairs whose pos lies outside 0..R-1 are left out (nothing is read for them).  Z: R*N
+ * fp16; pos, weights: T*topk; residual: T*N fp16 or NULL (it may be Y itself); Y: T*N fp16.  Z,
+ * residual and Y must be 16-byte aligned, pos and weights 4-byte.  1 <= topk <= TRI_MAX_TOPK.
+ * Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
+int tri_experts_combine(const _Float16 *Z, int64_t R, const int32_t *pos, const float *weights,
+                        const _Float16 *residual, int64_t T, int topk, int64_t N, _Float16 *Y, hipStream_t stream);
+
 /* The algorithm tri_linear would pick for (M, N, K, fmt); TRI_EINVAL if invalid.  Up to
  * M = 16 it is TRI_ALGO_SMALLM; above, whichever of TRI_ALGO_SMALLM and TRI_ALGO_GEMM a cost
  * model fitted to MI355X timings says is faster (the small-M kernels' time grows with the

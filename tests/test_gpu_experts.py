@@ -1,0 +1,431 @@
+"""Experts on the GPU: routing, ragged ternary products and their combination, against their definitions in float64.
+
+Tolerance of a product.  The stored digits t + 1 are exact, sum_k t x is sum_k (t+1) x - sum_k x (at most 3 sum |x| in
+magnitude); a term passes at most 32 additions inside a matrix instruction, one per later instruction on the same
+accumulator (K/16 at most) and 48 of partial sums, each off by at most 2^-23 (a truncating adder); one rounding to fp16:
+    d = (80 + K/16) 2^-23 3 |scale| sum_k |x|,   |Y - Y_ref| <= d + 2^-11 |Y_ref| + 2^-25.
+The gated pair: silu'(z) <= 1.1, exp and the division within 2^-18:
+    1.1 d_g |u| + |silu(g)| d_u + 1.1 d_g d_u + (2^-18 + 2^-11) |Y_ref| + 2^-25.
+Combination: topk + 1 additions of fp32 products, each within 2^-24 of the terms' magnitudes, and one rounding.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import bit_mixed_precision_tri_amd as tri
+from bit_mixed_precision_tri_amd import synth
+from tests.gpu_helpers import say, cuda, host
+
+pytestmark = pytest.mark.gpu
+F2, F16 = tri.TRI_FMT_2BIT, tri.TRI_FMT_1P6BIT
+INF = np.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    tri.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- routing
+
+def route_ref(x, topk, renorm):
+    x = x.astype(np.float64)
+    x = np.where(np.isnan(x), -INF, x)
+    T, E = x.shape
+    order = np.argsort(-x, axis=1, kind="stable")[:, :topk]
+    top = np.take_along_axis(x, order, 1)
+    ids = np.where(top > -INF, order, -1)
+    mx = x.max(1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        mass = lambda v: np.where(v == -INF, 0.0, np.where(v == mx, 1.0, np.exp(v - mx)))
+        den = (mass(top) if renorm else mass(x)).sum(1, keepdims=True)
+        weights = np.where(ids >= 0, mass(top) / np.where(den > 0, den, 1.0), 0.0)
+    flat = np.where(ids >= 0, ids, E).reshape(-1)
+    by = np.argsort(flat, kind="stable")
+    offsets = np.searchsorted(flat[by], np.arange(E + 1))
+    rows = np.where(flat[by] < E, by // topk, -1)
+    pos = np.empty(T * topk, dtype=np.int64)
+    pos[by] = np.arange(T * topk)
+    return ids, weights, offsets, rows, np.where(ids >= 0, pos.reshape(T, topk), -1)
+
+
+def check_route(x, topk, renorm):
+    import torch
+    T, E = x.shape
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = tri.Routing(torch.full((T, topk), 77, **i32), torch.full((T, topk), 7.0, device="cuda"),
+                      torch.full((E + 1,), 77, **i32), torch.full((T * topk,), 77, **i32), torch.full((T, topk), 77, **i32))
+    got = tri.experts_route(cuda(x), topk, renorm=renorm, out=out)
+    assert got is out
+    ids, weights, offsets, rows, pos = (host(t) for t in got)
+    rids, rweights, roffsets, rrows, rpos = route_ref(x, topk, renorm)
+    np.testing.assert_array_equal(ids, rids)
+    np.testing.assert_array_equal(offsets, roffsets)
+    np.testing.assert_array_equal(rows, rrows)
+    np.testing.assert_array_equal(pos, rpos)
+    # x - max exact to 2^-24 of its size (<= 120 where exp does not vanish), exp to a few steps, E additions, a division
+    assert np.all(np.abs(weights - rweights) <= (E + 140) * 2.0 ** -23 * rweights + 1e-38)
+
+
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 100, 129, 700])
+@pytest.mark.parametrize("E,topk", [(1, 1), (4, 2), (8, 8), (64, 6), (65, 3), (100, 16), (256, 8), (256, 16)])
+def test_route(T, E, topk):
+    rng = np.random.default_rng([51, T, E, topk])
+    x = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    say("route T=%d E=%d k=%d" % (T, E, topk))
+    for renorm in (True, False):
+        check_route(x, topk, renorm)
+        check_route((np.round(2 * x) / 2).astype(np.float16), topk, renorm)   # many equal logits
+
+
+def test_route_long():
+    """More workgroups than one adds up by itself; all tokens at one expert; a padded end."""
+    rng = np.random.default_rng(52)
+    x = rng.standard_normal((9001, 5)).astype(np.float32)
+    check_route(x, 2, True)
+    check_route(rng.standard_normal((20011, 256)).astype(np.float16), 3, False)
+    x[:] = [0, 0, 9, 0, 0]
+    check_route(x, 1, True)
+    x[8000:] = -INF
+    check_route(x, 2, False)
+
+
+def test_route_masks_and_extremes():
+    rng = np.random.default_rng(53)
+    x = rng.standard_normal((40, 8)).astype(np.float32)
+    x[0] = -INF                                  # a row without an expert
+    x[1, :7] = -INF                              # fewer experts than topk
+    x[2, 3] = np.nan
+    x[3] = np.nan
+    x[4, 5] = INF
+    x[5, [1, 6]] = INF                           # two infinities share the weight
+    x[6] = np.finfo(np.float32).min              # the lowest finite value is a logit like others
+    x[7] = -INF
+    x[7, 2] = np.finfo(np.float32).min
+    x[8] = 0.0
+    x[8, ::2] = -0.0                             # zeros of both signs are equal
+    x[9, 4] = np.finfo(np.float32).max
+    x[10] = [88, -88, 0, 1, 2, 3, 4, 5]
+    x[39] = -INF
+    for topk in (1, 2, 3, 8):
+        for renorm in (True, False):
+            check_route(x, topk, renorm)
+    check_route(np.full((70, 8), -INF, dtype=np.float32), 2, True)   # padding only: no pair at all
+    check_route(np.full((200, 8), -INF, dtype=np.float16), 4, False)
+
+
+# ---------------------------------------------------------------- products
+
+def places(sizes, first=0):
+    return (first + np.concatenate([[0], np.cumsum(sizes)])).astype(np.int32)
+
+
+def sum_bound(K, scale, X):
+    return (80 + K / 16) * 2.0 ** -23 * 3.0 * abs(float(scale)) * np.abs(X).sum(1, keepdims=True)
+
+
+def check_experts(rng, T, E, N, K, fmt, sizes, gather, pair, R=None, first=0, rows=None, what=""):
+    import torch
+    off = places(sizes, first)
+    R = int(off[-1]) if R is None else R
+    X = rng.standard_normal((T, K)).astype(np.float16)
+    if gather and rows is None:
+        rows = rng.integers(0, T, R).astype(np.int32)
+    Ws = [synth.trits(rng, E * N, K).reshape(E, N, K) for _ in range(2 if pair else 1)]
+    # scales of products around 1, so that a gate's exponential is exercised
+    ss = [(rng.uniform(0.5, 1.5, E) / np.sqrt(0.6 * K)).astype(np.float32) for _ in Ws]
+    mats = [(tri.pack(cuda(W.reshape(E * N, K)), fmt).view(E, N, -1), cuda(s)) for W, s in zip(Ws, ss)]
+    Y = torch.full((R + 3, N), 7.0, dtype=torch.float16, device="cuda")
+    say("experts %s T=%d E=%d N=%d K=%d fmt=%d R=%d gather=%d pair=%d" % (what, T, E, N, K, fmt, R, gather, pair))
+    rd = cuda(rows) if gather else None
+    Xd, od = cuda(X), cuda(off)
+    if pair:
+        tri.tri_experts_pair(Xd, T, od, rd, R, *mats[0], *mats[1], E, N, K, fmt, Y)
+    else:
+        tri.tri_experts_linear(Xd, T, od, rd, R, *mats[0], E, N, K, fmt, Y)
+    got, X = host(Y).astype(np.float64), X.astype(np.float64)
+    seen = np.zeros(R + 3, dtype=bool)
+    for e in range(E):
+        a, b = min(int(off[e]), R), min(int(off[e + 1]), R)
+        r = np.arange(a, b)
+        src = rows[a:b] if gather else r
+        live = (src >= 0) & (src < T)
+        r, x = r[live], X[src[live]]
+        if not len(r):
+            continue
+        seen[r] = True
+        ys = [float(s[e]) * (x @ W[e].astype(np.float64).T) for W, s in zip(Ws, ss)]
+        ds = [sum_bound(K, s[e], x) for s in ss]
+        if pair:
+            sil = ys[0] / (1 + np.exp(-ys[0]))
+            ref = sil * ys[1]
+            tol = 1.1 * ds[0] * np.abs(ys[1]) + np.abs(sil) * ds[1] + 1.1 * ds[0] * ds[1] + 2.0 ** -18 * np.abs(ref)
+        else:
+            ref, tol = ys[0], ds[0]
+        tol = tol + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+        err = np.abs(got[r] - ref)
+        assert np.all(err <= tol), "%s expert %d: worst %.3g of the tolerance" % (what, e, np.max(err / tol))
+    assert np.all(got[~seen] == 7.0), "a row that no expert owns was written"
+
+
+RAGGED = {"one": [1], "few": [1, 0, 2, 1], "hole": [0, 0, 5, 0], "mixed": [3, 17, 0, 1, 16, 64, 33, 5],
+          "single": [0, 130, 0], "many": [2, 0, 1, 3, 0, 0, 4, 1] * 8, "long": [200, 0, 70, 129], "empty": [0, 0]}
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("name", list(RAGGED))
+def test_products_of_ragged_experts(name, pair, fmt):
+    rng = np.random.default_rng([54, list(RAGGED).index(name), pair, fmt])
+    sizes = RAGGED[name]
+    for (N, K) in [(48, 256), (100, 648), (513, 1000), (130, 333)]:
+        if len(sizes) > 32 and N > 200:
+            continue
+        for gather in (False, True):
+            R = max(1, sum(sizes))
+            check_experts(rng, R + 2 if not gather else 9, len(sizes), N, K, fmt, sizes, gather, pair, R=R, what=name)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("M", [1, 2, 4, 5, 8, 9, 16, 40])
+@pytest.mark.parametrize("K", [4096, 11008, 28672])
+def test_products_of_long_rows(K, M, fmt):
+    """One expert of M rows, and two that share them unevenly."""
+    rng = np.random.default_rng([55, M, fmt, K])
+    N = 40 if K > 4096 else 80
+    check_experts(rng, M, 1, N, K, fmt, [M], False, False)
+    check_experts(rng, 7, 3, N, K, fmt, [M // 3, 0, M - M // 3], True, K < 28672)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+def test_products_of_whole_tiles(fmt):
+    """Sizes at the edges of the large tiles, in rows and in columns."""
+    rng = np.random.default_rng([56, fmt])
+    for pair in (False, True):
+        check_experts(rng, 640, 2, 1024, 512, fmt, [128, 512], False, pair)
+        check_experts(rng, 300, 3, 511, 520, fmt, [127, 129, 1], True, pair)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("big", [False, True])
+def test_places_that_no_expert_owns(fmt, big):
+    """Places before the first offset and behind the last, and rows that name no row of X."""
+    rng = np.random.default_rng([57, fmt, big])
+    sizes = [150, 0, 200, 33] if big else [2, 0, 3, 1]
+    n = sum(sizes)
+    for pair in (False, True):
+        check_experts(rng, n + 20, 4, 96, 264, fmt, sizes, False, pair, R=n + 15, first=6)
+        rows = rng.integers(0, 11, n + 15).astype(np.int32)
+        rows[[0, 7, n + 3]] = [-1, 11, -(1 << 31)]
+        rows[8] = (1 << 31) - 1
+        check_experts(rng, 11, 4, 96, 264, fmt, sizes, True, pair, R=n + 15, first=6, rows=rows)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+def test_offsets_past_the_places_are_clamped(fmt):
+    rng = np.random.default_rng([58, fmt])
+    for R in (5, 100):
+        check_experts(rng, R, 3, 64, 256, fmt, [2, R, 40], False, False, R=R)
+
+
+def test_one_expert_equals_the_layer():
+    """Against tri_linear on the same matrix, within both tolerances, and the packed rows of one tri_pack2 call for all
+    experts are those of one call each."""
+    import torch
+    rng = np.random.default_rng(59)
+    W = synth.trits(rng, 96, 512)
+    X = rng.standard_normal((20, 512)).astype(np.float16)
+    for fmt in (F2, F16):
+        whole = tri.pack(cuda(W), fmt)
+        each = torch.cat([tri.pack(cuda(W[48 * e:48 * e + 48]), fmt) for e in range(2)])
+        assert torch.equal(whole, each)
+        s = torch.full((1,), 0.05, device="cuda")
+        Y = tri.experts_linear(cuda(X), cuda(places([20])), None, whole.view(1, 96, -1), s, 512, fmt)
+        L = host(tri.linear(cuda(X), whole, float(s[0]), 512, fmt)).astype(np.float64)
+        ref = oracle.linear_f64(X, W, float(np.float32(0.05)))
+        assert np.all(np.abs(host(Y) - L) <= 2 * oracle.tolerance(X, 0.05, ref))
+
+
+# ---------------------------------------------------------------- combination
+
+def check_combine(Y, Z, pos, weights, residual):
+    Z = Z.astype(np.float64)
+    ok = (pos >= 0) & (pos < len(Z))
+    terms = np.where(ok[..., None], weights.astype(np.float64)[..., None] * Z[np.where(ok, pos, 0)], 0.0)
+    ref, mag = terms.sum(1), np.abs(terms).sum(1)
+    if residual is not None:
+        ref, mag = ref + residual.astype(np.float64), mag + np.abs(residual.astype(np.float64))
+    tol = (pos.shape[1] + 2) * 2.0 ** -24 * mag + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+    assert np.all(np.abs(Y.astype(np.float64) - ref) <= tol)
+
+
+@pytest.mark.parametrize("T,topk,N", [(1, 1, 8), (1, 2, 4096), (3, 5, 100), (17, 8, 257), (300, 6, 1024), (5, 16, 33),
+                                      (2, 3, 1)])
+def test_combine(T, topk, N):
+    rng = np.random.default_rng([60, T, topk, N])
+    R = T * topk
+    Z = rng.standard_normal((R, N)).astype(np.float16)
+    w = rng.uniform(-1, 1, (T, topk)).astype(np.float32)
+    pos = rng.permutation(R).reshape(T, topk).astype(np.int32)
+    res = rng.standard_normal((T, N)).astype(np.float16)
+    for r in (None, res):
+        check_combine(host(tri.experts_combine(cuda(Z), cuda(pos), cuda(w), residual=None if r is None else cuda(r))), Z,
+                      pos, w, r)
+    # left out: places outside Z, with whatever lies at their weights; the rows that nobody names may hold anything
+    bad = pos.copy()
+    bad[0, 0], bad[-1, -1] = -1, R
+    bad[0, topk // 2] = -(1 << 31)
+    Z[pos[bad != pos]] = np.nan
+    w[bad != pos] = np.nan
+    Rd = cuda(res)
+    out = tri.experts_combine(cuda(Z), cuda(bad), cuda(w), residual=Rd, out=Rd)   # in place
+    w[bad != pos] = 0.0
+    check_combine(host(out), np.nan_to_num(Z), bad, w, res)
+
+
+# ---------------------------------------------------------------- together
+
+def mixed_block(rng, T, E, topk, hidden, inner, fmt):
+    """A 4-bit layer that gives the router's logits, and an MLP of ternary experts."""
+    Wr = tri.int4_quantize(cuda((0.05 * rng.standard_normal((E, hidden))).astype(np.float32)), 64)
+    mats = []
+    for (n, k) in ((inner, hidden), (inner, hidden), (hidden, inner)):
+        W, s = [], []
+        for _ in range(E):                       # experts from latent weights, the scales as the quantiser leaves them
+            p, sc = tri.quantize(cuda(synth.latent_weights(rng, n, k)), fmt)
+            W.append(p)
+            s.append(sc)
+        import torch
+        mats.append((torch.stack(W), torch.cat(s)))
+    return Wr, mats
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("T,E,topk,hidden,inner", [(1, 8, 2, 512, 768), (9, 4, 2, 256, 344), (150, 16, 4, 256, 200)])
+def test_a_block_of_experts(T, E, topk, hidden, inner, fmt):
+    """All four operators as a block uses them; each step is checked on what the step before gave."""
+    rng = np.random.default_rng([61, T, E, fmt])
+    Wr, (gate, up, down) = mixed_block(rng, T, E, topk, hidden, inner, fmt)
+    X = rng.standard_normal((T, hidden)).astype(np.float16)
+    Xd = cuda(X)
+    logits = tri.int4_linear(Xd, Wr, E, 64)
+    Y = tri.experts_mlp(Xd, logits, topk, gate, up, down, fmt, residual=Xd)
+    r = tri.experts_route(logits, topk)
+    H = tri.experts_pair(Xd, r.offsets, r.rows, *gate, *up, hidden, fmt)
+    Z = tri.experts_linear(H, r.offsets, None, *down, inner, fmt)
+    assert np.array_equal(host(tri.experts_combine(Z, r.pos, r.weights, residual=Xd)).view(np.uint16),
+                          host(Y).view(np.uint16))
+    ids, weights, offsets, rows, pos = route_ref(host(logits), topk, True)
+    np.testing.assert_array_equal(host(r.ids), ids)
+    np.testing.assert_array_equal(host(r.pos), pos)
+    dense = [[oracle.unpack(host(W[e]), k, fmt).astype(np.float64) * float(s[e]) for e in range(E)]
+             for (W, s), k in zip((gate, up, down), (hidden, hidden, inner))]
+    H, Z = host(H).astype(np.float64), host(Z).astype(np.float64)
+    for e in range(E):
+        a, b = offsets[e], offsets[e + 1]
+        x = X[rows[a:b]].astype(np.float64)
+        g, u = x @ dense[0][e].T, x @ dense[1][e].T
+        h = g / (1 + np.exp(-g)) * u
+        dg, du = (sum_bound(hidden, float(m[1][e]), x) for m in (gate, up))
+        tol = 1.1 * dg * np.abs(u) + np.abs(g) * du + 1.1 * dg * du + (2.0 ** -18 + 2.0 ** -11) * np.abs(h) + 2.0 ** -25
+        assert np.all(np.abs(H[a:b] - h) <= tol)
+        z = H[a:b] @ dense[2][e].T
+        assert np.all(np.abs(Z[a:b] - z) <= sum_bound(inner, float(down[1][e]), H[a:b]) + 2.0 ** -11 * np.abs(z) + 2.0 ** -25)
+    check_combine(host(Y), Z, pos, host(r.weights), X)
+
+
+def test_graph_replays_equal_eager_calls():
+    """The block captured once and replayed on new inputs, with eager work between the replays."""
+    import torch
+    rng = np.random.default_rng(62)
+    T, E, topk, hidden, inner = 100, 8, 2, 256, 384
+    Wr, (gate, up, down) = mixed_block(rng, T, E, topk, hidden, inner, F2)
+    X = torch.empty((T, hidden), dtype=torch.float16, device="cuda")
+    ws = torch.empty(tri.tri_experts_route_workspace_bytes(T, E, topk), dtype=torch.uint8, device="cuda")
+    mk = lambda *s, d=torch.float16: torch.zeros(s, dtype=d, device="cuda")
+    logits, H, Z, Y = mk(T, E), mk(T * topk, inner), mk(T * topk, hidden), mk(T, hidden)
+    r = tri.Routing(mk(T, topk, d=torch.int32), mk(T, topk, d=torch.float32), mk(E + 1, d=torch.int32),
+                    mk(T * topk, d=torch.int32), mk(T, topk, d=torch.int32))
+
+    def step():
+        tri.int4_linear(X, Wr, E, 64, out=logits)
+        tri.experts_route(logits, topk, workspace=ws, out=r)
+        tri.experts_pair(X, r.offsets, r.rows, *gate, *up, hidden, F2, out=H)
+        tri.experts_linear(H, r.offsets, None, *down, inner, F2, out=Z)
+        tri.experts_combine(Z, r.pos, r.weights, residual=X, out=Y)
+
+    def inputs(seed):
+        X.copy_(torch.randn(X.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)).half())
+
+    inputs(0)
+    step()
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    torch.cuda.synchronize()
+    outs = lambda: [t.clone() for t in (logits, H, Z, Y) + tuple(r)]
+    for seed in (1, 2, 3):
+        inputs(seed)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = outs()
+        step()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, outs())):
+            assert torch.equal(a, b), "replay %d, output %d" % (seed, i)
+    del graph
+
+
+def test_two_streams_at_once():
+    """Two blocks on two streams, with the workspaces and intermediate results that the helpers allocate."""
+    import torch
+    rng = np.random.default_rng(63)
+    T, E, topk, hidden, inner = 200, 8, 2, 256, 384
+    Wr, (gate, up, down) = mixed_block(rng, T, E, topk, hidden, inner, F16)
+    Xs = [cuda(rng.standard_normal((T, hidden)).astype(np.float16)) for _ in range(2)]
+
+    def step(X, stream=None):
+        return tri.experts_mlp(X, tri.int4_linear(X, Wr, E, 64, stream=stream), topk, gate, up, down, F16, stream=stream)
+
+    want = [step(X).clone() for X in Xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Xs]
+    for _ in range(3):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        got = [step(X, s) for X, s in zip(Xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_refusals_of_the_helpers():
+    import torch
+    h, i, u, f = (dict(dtype=d, device="cuda") for d in (torch.float16, torch.int32, torch.uint8, torch.float32))
+    x, off, rows, s = torch.zeros((4, 64), **h), torch.zeros(3, **i), torch.zeros(5, **i), torch.zeros(2, **f)
+    W = torch.zeros((2, 16, 16), **u)
+    tri.experts_linear(x, off, rows, W, s, 64, F2)
+    for bad in [lambda: tri.experts_linear(x, off.long(), rows, W, s, 64, F2),
+                lambda: tri.experts_linear(x, off[:2], rows, W, s, 64, F2),
+                lambda: tri.experts_linear(x, off, rows.long(), W, s, 64, F2),
+                lambda: tri.experts_linear(x, off, rows, W, s.double(), 64, F2),
+                lambda: tri.experts_linear(x, off, rows, W, s[:1], 64, F2),
+                lambda: tri.experts_linear(x, off, rows, W, s, 128, F2),
+                lambda: tri.experts_linear(x, off, rows, W, s, 64, F2, out=torch.zeros((4, 16), **h)),
+                lambda: tri.experts_linear(x, off, rows, W.view(32, 16), s, 64, F2),
+                lambda: tri.experts_pair(x, off, rows, W, s, torch.zeros((2, 17, 16), **u), s, 64, F2),
+                lambda: tri.experts_route(x, 0), lambda: tri.experts_route(x, 17), lambda: tri.experts_route(x.double(), 2),
+                lambda: tri.experts_route(x.t(), 2), lambda: tri.experts_route(torch.zeros((4, 300), **h), 2),
+                lambda: tri.experts_combine(x, rows.view(1, 5), torch.zeros((1, 4), **f)),
+                lambda: tri.experts_combine(x, rows.view(1, 5), torch.zeros((1, 5), **h)),
+                lambda: tri.experts_combine(x, rows.view(1, 5), torch.zeros((1, 5), **f), out=torch.zeros((2, 64), **h))]:
+        with pytest.raises(ValueError):
+            bad()
