@@ -20,6 +20,8 @@ struct Int4Map {
 
 // Tiles of a matrix, at most (2^33 weights): keeps every launch's thread count below 2^32.
 constexpr int64_t kInt4MaxTiles = (int64_t)1 << 22;
+// Longest row: 32-bit buffer offsets over 16 activation rows and over four blocks of a row's tiles.
+constexpr int64_t kInt4MaxK = (int64_t)1 << 25;
 
 Int4Map int4_map(int64_t N, int64_t K, int group) { return {(N + 15) / 16, (K + 127) / 128, 128 / group}; }
 
@@ -125,39 +127,284 @@ __global__ __launch_bounds__(256) void k_int4_quantize(const float *__restrict__
     }
 }
 
-// The product, one wave per weight row and eight activation rows: lanes own pieces of eight values.
-__global__ __launch_bounds__(256) void k_int4_rows(const uint16_t *__restrict__ X, const uint32_t *__restrict__ codes,
-                                                   const uint16_t *__restrict__ scales,
-                                                   const uint8_t *__restrict__ zeros, int M, int N, int K, int KS,
-                                                   int gps, const uint16_t *R, uint16_t *Y)
+// ---------------------------------------------------------------- product, up to 16 rows per pass
+
+constexpr uint32_t kRsrcWord3 = 0x00020000u;     // raw buffer resource, gfx9 family
+constexpr uint32_t kOob = 0x80000000u;           // an offset past every buffer here: reads zero
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes)
 {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, (int)kRsrcWord3);
+}
+
+__device__ __forceinline__ float4_t mfma(const u32x4 a, const u32x4 b, float4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// Eight codes of a word as fp16 code - zero, exactly.  Codes at bits 0-3 of a half, OR-ed into 1024.0 (mantissa
+// step 1), read 1024 + q; at bits 4-7, OR-ed into 64.0 (step 1/16), 64 + q; one packed add takes 1024 + z or
+// 64 + z away.  lo, hi: the two fp16 pairs -(1024 + z) and -(64 + z); b10, b6: 1024.0 and 64.0 pairs held in
+// registers (an instruction takes one scalar operand: the mask).
+__device__ __forceinline__ u32x4 decode(uint32_t w, uint32_t b10, uint32_t b6, uint32_t lo, uint32_t hi)
+{
+    const uint32_t v = w >> 8;
+    u32x4 r;
+    r[0] = __builtin_bit_cast(uint32_t, as_h2((w & 0x000F000Fu) | b10) + as_h2(lo));
+    r[1] = __builtin_bit_cast(uint32_t, as_h2((w & 0x00F000F0u) | b6) + as_h2(hi));
+    r[2] = __builtin_bit_cast(uint32_t, as_h2((v & 0x000F000Fu) | b10) + as_h2(lo));
+    r[3] = __builtin_bit_cast(uint32_t, as_h2((v & 0x00F000F0u) | b6) + as_h2(hi));
+    return r;
+}
+
+// MA (1, 2, 4, 8, 16) activation rows times RB blocks of 16 weight rows per workgroup of NW waves.
+//
+// v_mfma_f32_16x16x32_f16 takes 16 A rows.  With fewer activation rows than that, the A rows that one product does
+// not need carry the activations of the next ones: A row i = MA c + a holds activation row a at the c-th of
+// 16/MA consecutive pieces of 32 values.  One 16-byte load per lane then fetches the A operand of 16/MA products
+// (for one activation row, of four whole steps), with nothing to permute or stage; of product c's result only
+// the rows MA c .. MA c + MA-1 are taken.  B operands are whole words of the layout, lane for lane.
+//
+// A unit is U steps (the span of one A load, at least one step); wave w takes units w, w + NW, ..., the loads of two
+// units in flight.  Each step's partial sums are scaled in fp32 by their group's scale where they lie: lane (g, j)
+// of the result holds row j's products of step tl(g), so it loads the scales of that row and step.  Zero points
+// shift the codes as they are decoded (U == 1), or are taken off by sum_k x, formed by one more product with
+// ones per A load (U > 1, where a lane decodes other steps than it scales).
+template <int MA, int RB, int GPS, bool ZP, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict__ X, const uint8_t *__restrict__ codes,
+                                                     const uint16_t *__restrict__ scales,
+                                                     const uint8_t *__restrict__ zeros, int M, int N, int K, int KS,
+                                                     const uint16_t *R, uint16_t *Y)
+{
+    constexpr int CL = 16 / MA;                  // pieces of 32 values per A load
+    constexpr int U = CL > 4 ? CL / 4 : 1;       // steps per unit
+    constexpr int AL = CL < 4 ? 4 / CL : 1;      // A loads per unit
+    constexpr bool ZSUM = ZP && U > 1, ZDEC = ZP && U == 1;
+    constexpr int TE = MA < 4 ? MA : 4;          // results per lane and block
+    __shared__ float red[NW][MA][16 * RB];
+
     const int lane = threadIdx.x & 63;
-    const int64_t n = 4 * (int64_t)blockIdx.x + (threadIdx.x >> 6);
-    if (n >= N) return;
-    const int64_t b = n / 16, j = n % 16;
-    for (int64_t m0 = 8 * (int64_t)blockIdx.y; m0 < M; m0 += 8 * (int64_t)gridDim.y) {
-        float acc[8] = {};
-        for (int64_t q = lane; q < 16 * (int64_t)KS; q += 64) {
-            const int64_t tile = b * KS + q / 16;
-            const int qq = (int)(q % 16);
-            const uint32_t w = codes[tile * 256 + (16 * (qq & 3) + j) * 4 + (qq >> 2)];
-            const int64_t o = (tile * 16 + j) * gps + qq * gps / 16;
-            const float sc = h2f(scales[o]);
-            const int z = zeros ? zeros[o] : 8;
-            for (int i = 0; i < 8; ++i) {
-                const int64_t k = 8 * q + i;
-                if (k >= K) break;
-                const float wv = sc * (float)((int)((w >> nibble_at(i)) & 15u) - z);
-                for (int r = 0; r < 8; ++r)
-                    if (m0 + r < M) acc[r] += wv * h2f(X[(m0 + r) * K + k]);
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    const int m0 = MA * (int)blockIdx.y;
+    const int64_t b0 = (int64_t)blockIdx.x * RB; // first block of 16 weight rows
+    const int nb = min(RB, (N + 15) / 16 - (int)b0);
+
+    const __amdgpu_buffer_rsrc_t wr = rsrc(codes + b0 * KS * 1024, __builtin_amdgcn_readfirstlane((uint32_t)nb * KS * 1024u));
+    const __amdgpu_buffer_rsrc_t sr =
+        rsrc(scales + b0 * KS * (16 * GPS), __builtin_amdgcn_readfirstlane((uint32_t)nb * KS * (32u * GPS)));
+    const __amdgpu_buffer_rsrc_t zr =
+        rsrc(ZP ? zeros + b0 * KS * (16 * GPS) : nullptr, __builtin_amdgcn_readfirstlane(ZP ? (uint32_t)nb * KS * (16u * GPS) : 0u));
+    const int mm = min(MA, M - m0);
+    const __amdgpu_buffer_rsrc_t xr =
+        rsrc(X + (int64_t)m0 * K, __builtin_amdgcn_readfirstlane((uint32_t)mm * (uint32_t)K * 2u));
+
+    const int ac = j / MA, aa = j % MA;          // this lane's A row: piece ac of the load, activation row aa
+    const uint32_t xrow = aa < mm ? (uint32_t)aa * (uint32_t)K * 2u : kOob;
+    const int tl = U == 4 ? g : U == 2 ? g >> 1 : 0;   // the step of a unit that this lane scales
+
+    struct Unit {
+        u32x4 w[RB][U];
+        u32x4 a[AL];
+        uint32_t s[RB][GPS == 4 ? 2 : 1];        // GPS scales
+        uint32_t z[RB];                          // GPS zero points
+    };
+    auto load = [&](int u, Unit &t) __attribute__((always_inline)) {
+        const int s0 = u * U;
+#pragma unroll
+        for (int q = 0; q < AL; ++q) {
+            const int k = 128 * s0 + 32 * (CL * q + ac) + 8 * g;
+            if constexpr (VEC) {
+                t.a[q] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(k < K ? xrow + 2u * (uint32_t)k : kOob), 0, 0);
+            } else {                             // rows that are no whole pieces: value by value
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
+                        xr, (int)(k + 2 * e < K ? xrow + 2u * (uint32_t)(k + 2 * e) : kOob), 0, 0);
+                    const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
+                        xr, (int)(k + 2 * e + 1 < K ? xrow + 2u * (uint32_t)(k + 2 * e + 1) : kOob), 0, 0);
+                    t.a[q][e] = (lo & 0xFFFFu) | hi << 16;
+                }
             }
         }
-        const float t = wave_reduce_rows<8>(acc, lane);
-        const int64_t m = m0 + (lane >> 3);
-        if ((lane & 7) == 0 && m < M) {
-            float y = t;
-            if (R) y += h2f(R[m * N + n]);
-            Y[m * N + n] = __builtin_bit_cast(uint16_t, (_Float16)y);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int st = s0 + tl;
+            const uint32_t so = st < KS ? ((uint32_t)(r * KS + st) * 16u + (uint32_t)j) * GPS : kOob >> 1;
+            if constexpr (GPS == 4) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(sr, (int)(so * 2u), 0, 0);
+                t.s[r][0] = v[0];
+                t.s[r][1] = v[1];
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b32(zr, (int)so, 0, 0);
+            } else if constexpr (GPS == 2) {
+                t.s[r][0] = __builtin_amdgcn_raw_buffer_load_b32(sr, (int)(so * 2u), 0, 0);
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b16(zr, (int)so, 0, 0);
+            } else {
+                t.s[r][0] = __builtin_amdgcn_raw_buffer_load_b16(sr, (int)(so * 2u), 0, 0);
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b8(zr, (int)so, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const uint32_t o = s0 + i < KS ? (uint32_t)(r * KS + s0 + i) * 1024u + 16u * (uint32_t)lane : kOob;
+                t.w[r][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)o, 0, 0);
+            }
+        }
+    };
+    uint32_t b10, b6;
+    asm volatile("v_mov_b32 %0, 0x64006400" : "=v"(b10));
+    asm volatile("v_mov_b32 %0, 0x54005400" : "=v"(b6));
+    const float4_t zero4 = {0.f, 0.f, 0.f, 0.f};
+    float tot[RB][TE];
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int e = 0; e < TE; ++e) tot[r][e] = 0.f;
+
+    auto scale_of = [](const Unit &t, int r, int i) {
+        return h2f((uint16_t)(t.s[r][GPS == 4 ? i / 2 : 0] >> (GPS == 1 ? 0 : 16 * (i % 2))));
+    };
+    auto run = [&](const Unit &t) __attribute__((always_inline)) {
+        float4_t xs = zero4;                     // ZSUM: sums of the A rows
+        if constexpr (ZSUM) {
+            const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+            xs = mfma(t.a[0], ones, zero4);
+        }
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            float sc[GPS];
+#pragma unroll
+            for (int i = 0; i < GPS; ++i) sc[i] = scale_of(t, r, i);
+            if constexpr (U > 1) {
+                // products of step i, piece p: A row 4 i + p (MA = 1), 2 (4 i + p) + a (MA = 2)
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float4_t d[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) d[p] = mfma(t.a[0], decode(t.w[r][i][p], b10, b6, 0xE408E408u, 0xD480D480u), zero4);
+                    if constexpr (MA == 1) {     // lane group i, element p
+                        float v = 0.f;
+                        if constexpr (ZP) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+                                d[p][p] = fmaf(xs[p], 8.f - (float)((t.z[r] >> (8 * (p * GPS / 4))) & 15u), d[p][p]);
+                        }
+                        if constexpr (GPS == 4) v = (d[0][0] * sc[0] + d[1][1] * sc[1]) + (d[2][2] * sc[2] + d[3][3] * sc[3]);
+                        if constexpr (GPS == 2) v = (d[0][0] + d[1][1]) * sc[0] + (d[2][2] + d[3][3]) * sc[1];
+                        if constexpr (GPS == 1) v = ((d[0][0] + d[1][1]) + (d[2][2] + d[3][3])) * sc[0];
+                        tot[r][0] += g == i ? v : 0.f;
+                    } else {                     // lane group 2 i + p / 2, elements 2 (p % 2) + a
+                        const bool odd = g & 1;
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            float v0 = odd ? d[2][a] : d[0][a], v1 = odd ? d[3][2 + a] : d[1][2 + a];
+                            if constexpr (ZP) {
+                                const uint32_t zz = GPS == 4 ? (odd ? t.z[r] >> 16 : t.z[r])
+                                                             : GPS == 2 ? (odd ? t.z[r] >> 8 : t.z[r]) : t.z[r];
+                                v0 = fmaf(xs[a], 8.f - (float)(zz & 15u), v0);
+                                v1 = fmaf(xs[2 + a], 8.f - (float)((GPS == 4 ? zz >> 8 : zz) & 15u), v1);
+                            }
+                            float v;
+                            if constexpr (GPS == 4) v = v0 * (odd ? sc[2] : sc[0]) + v1 * (odd ? sc[3] : sc[1]);
+                            else v = (v0 + v1) * (GPS == 2 && odd ? sc[GPS - 1] : sc[0]);
+                            tot[r][a] += (g >> 1) == i ? v : 0.f;
+                        }
+                    }
+                }
+            } else {
+                u32x4 bop[4];
+                uint32_t lo = 0xE408E408u, hi = 0xD480D480u;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if constexpr (ZDEC) {
+                        if (p % (4 / GPS) == 0) {
+                            const uint32_t z = (t.z[r] >> (8 * (p * GPS / 4))) & 15u, zz = z | z << 16;
+                            lo = 0xE400E400u + zz;
+                            hi = 0xD400D400u + (zz << 4);
+                        }
+                    }
+                    bop[p] = decode(t.w[r][0][p], b10, b6, lo, hi);
+                }
+                if constexpr (MA == 4) {         // piece p in lane group p, elements the rows
+                    float4_t d[4];
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) d[p] = mfma(t.a[0], bop[p], zero4);
+                    const float s01 = g & 1 ? sc[1 * GPS / 4] : sc[0], s23 = g & 1 ? sc[3 * GPS / 4] : sc[2 * GPS / 4];
+                    const float sg = g & 2 ? s23 : s01;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float v01 = g & 1 ? d[1][e] : d[0][e], v23 = g & 1 ? d[3][e] : d[2][e];
+                        tot[r][e] = fmaf(g & 2 ? v23 : v01, sg, tot[r][e]);
+                    }
+                } else if constexpr (MA == 8) {  // pieces 2 q + c, c = g / 2
+                    const bool up = g & 2;
+                    float4_t d0 = zero4, d1 = zero4;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        d0 = mfma(t.a[q], bop[2 * q], GPS == 1 && q ? d0 : zero4);
+                        d1 = mfma(t.a[q], bop[2 * q + 1], GPS == 1 && q ? d1 : zero4);
+                        if (GPS == 1 && q == 0) continue;
+                        const float sq = GPS == 4 ? (up ? sc[GPS == 4 ? 2 * q + 1 : 0] : sc[GPS == 4 ? 2 * q : 0])
+                                                  : sc[GPS == 2 ? q : 0];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tot[r][e] = fmaf(up ? d1[e] : d0[e], sq, tot[r][e]);
+                    }
+                } else {                         // every lane its four rows
+                    float4_t d = zero4;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        d = mfma(t.a[p], bop[p], p % (4 / GPS) ? d : zero4);
+                        if ((p + 1) % (4 / GPS) == 0) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) tot[r][e] = fmaf(d[e], sc[p * GPS / 4], tot[r][e]);
+                        }
+                    }
+                }
+            }
+        }
+    };
+
+    // (an even number of turns keeps one code path; units past the end read zeros)
+    const int nu = (KS + U - 1) / U, turns = (nu + NW - 1) / NW;
+    Unit t0, t1;
+    load(wv, t0);
+    load(wv + NW, t1);
+    for (int i = 0; i < turns; i += 2) {
+        run(t0);
+        load(wv + (i + 2) * NW, t0);
+        if (i + 1 < turns) run(t1);
+        load(wv + (i + 3) * NW, t1);
+    }
+
+    // sum over the lane groups that hold the same activation row, then over the waves in a fixed order
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int e = 0; e < TE; ++e) {
+            float v = tot[r][e];
+            if constexpr (MA <= 4) {
+                v = sum_over_rows(v);
+                if (g == 0) red[wv][e][16 * r + j] = v;
+            } else if constexpr (MA == 8) {
+                float a = v, b = v;
+                swap32(a, b);
+                v = a + b;
+                if (g < 2) red[wv][4 * g + e][16 * r + j] = v;
+            } else {
+                red[wv][4 * g + e][16 * r + j] = v;
+            }
+        }
+    __syncthreads();
+    for (int o = threadIdx.x; o < MA * 16 * RB; o += 64 * NW) {
+        const int m = o / (16 * RB), c = o % (16 * RB);
+        const int64_t n = 16 * b0 + c;
+        if (m < mm && n < N) {
+            float y = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) y += red[w][m][c];
+            const int64_t at = (int64_t)(m0 + m) * N + n;
+            if (R) y += h2f(R[at]);
+            Y[at] = __builtin_bit_cast(uint16_t, (_Float16)y);
         }
     }
 }
@@ -172,7 +419,7 @@ int launched() { return hipGetLastError() == hipSuccess ? TRI_OK : TRI_EHIP; }
 int64_t int4_bytes(int64_t N, int64_t K, int group, bool zeros)
 {
     const Int4Map m = int4_map(N, K, group);
-    if (m.tiles() >= kInt4MaxTiles) return -1;
+    if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return -1;
     return m.tiles() * 1024 + m.scales() * (zeros ? 3 : 2);
 }
 
@@ -180,7 +427,7 @@ int launch_int4_pack(const uint8_t *Q, const uint16_t *S, const uint8_t *Z, int 
                      hipStream_t s)
 {
     const Int4Map m = int4_map(N, K, group);
-    if (m.tiles() >= kInt4MaxTiles) return TRI_EINVAL;
+    if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return TRI_EINVAL;
     hipLaunchKernelGGL(k_int4_pack, dim3((unsigned)m.tiles()), dim3(256), 0, s, Q, S, Z, N, K, (int)m.KS, m.gps,
                        reinterpret_cast<uint32_t *>(Wp), scales_of(Wp, m), Z ? zeros_of(Wp, m) : nullptr);
     return launched();
@@ -190,7 +437,7 @@ int launch_int4_unpack(const uint8_t *Wp, int N, int K, int group, bool zeros, u
                        hipStream_t s)
 {
     const Int4Map m = int4_map(N, K, group);
-    if (m.tiles() >= kInt4MaxTiles) return TRI_EINVAL;
+    if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return TRI_EINVAL;
     uint8_t *p = const_cast<uint8_t *>(Wp);      // (read only)
     hipLaunchKernelGGL(k_int4_unpack, dim3((unsigned)m.tiles()), dim3(256), 0, s, reinterpret_cast<const uint32_t *>(Wp),
                        scales_of(p, m), zeros ? zeros_of(p, m) : nullptr, N, K, (int)m.KS, m.gps, Q, S, Z);
@@ -200,22 +447,76 @@ int launch_int4_unpack(const uint8_t *Wp, int N, int K, int group, bool zeros, u
 int launch_int4_quantize(const float *W, int N, int K, int group, bool zeros, uint8_t *Wp, hipStream_t s)
 {
     const Int4Map m = int4_map(N, K, group);
-    if (m.tiles() >= kInt4MaxTiles) return TRI_EINVAL;
+    if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return TRI_EINVAL;
     hipLaunchKernelGGL(k_int4_quantize, dim3((unsigned)m.tiles()), dim3(256), 0, s, W, N, K, (int)m.KS, m.gps,
                        reinterpret_cast<uint32_t *>(Wp), scales_of(Wp, m), zeros ? zeros_of(Wp, m) : nullptr);
     return launched();
 }
 
+namespace {
+
+struct Int4Args {
+    const uint16_t *X;
+    const uint8_t *codes;
+    const uint16_t *scales;
+    const uint8_t *zeros;
+    int M, N, K, KS;
+    const uint16_t *R;
+    uint16_t *Y;
+};
+
+template <int MA, int RB, int GPS, bool ZP, bool VEC>
+void mv_go(const Int4Args &a, hipStream_t s)
+{
+    constexpr int NW = 8;
+    const int blocks = (a.N + 15) / 16;
+    hipLaunchKernelGGL((k_int4_mv<MA, RB, GPS, ZP, NW, VEC>), dim3((blocks + RB - 1) / RB, (a.M + MA - 1) / MA), dim3(64 * NW),
+                       0, s, a.X, a.codes, a.scales, a.zeros, a.M, a.N, a.K, a.KS, a.R, a.Y);
+}
+
+template <int MA, int RB, bool VEC>
+void mv_fmt(const Int4Args &a, int gps, hipStream_t s)
+{
+    if (a.zeros) {
+        if (gps == 1) mv_go<MA, RB, 1, true, VEC>(a, s);
+        else if (gps == 2) mv_go<MA, RB, 2, true, VEC>(a, s);
+        else mv_go<MA, RB, 4, true, VEC>(a, s);
+    } else {
+        if (gps == 1) mv_go<MA, RB, 1, false, VEC>(a, s);
+        else if (gps == 2) mv_go<MA, RB, 2, false, VEC>(a, s);
+        else mv_go<MA, RB, 4, false, VEC>(a, s);
+    }
+}
+
+void mv_rows(const Int4Args &a, int gps, hipStream_t s)
+{
+    if (a.K % 8) {
+        if (a.M <= 4) mv_fmt<4, 1, false>(a, gps, s);
+        else mv_fmt<16, 1, false>(a, gps, s);
+        return;
+    }
+    if (a.M <= 1) mv_fmt<1, 1, true>(a, gps, s);
+    else if (a.M <= 2) mv_fmt<2, 1, true>(a, gps, s);
+    else if (a.M <= 4) mv_fmt<4, 1, true>(a, gps, s);
+    else if (a.M <= 8) mv_fmt<8, 2, true>(a, gps, s);
+    else mv_fmt<16, 2, true>(a, gps, s);
+}
+
+}  // namespace
+
 int launch_int4_linear(const uint16_t *X, const uint8_t *Wp, int M, int N, int K, int group, bool zeros,
                        const uint16_t *R, uint16_t *Y, hipStream_t s)
 {
     const Int4Map m = int4_map(N, K, group);
-    if (m.tiles() >= kInt4MaxTiles) return TRI_EINVAL;
+    if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return TRI_EINVAL;
     uint8_t *p = const_cast<uint8_t *>(Wp);      // (read only)
-    const int64_t rows = ((int64_t)M + 7) / 8;
-    hipLaunchKernelGGL(k_int4_rows, dim3((unsigned)((N + 3) / 4), (unsigned)(rows < 32768 ? rows : 32768)), dim3(256), 0,
-                       s, X, reinterpret_cast<const uint32_t *>(Wp), scales_of(p, m), zeros ? zeros_of(p, m) : nullptr, M,
-                       N, K, (int)m.KS, m.gps, R, Y);
+    // 16-row slices go to the second grid dimension, at most 65535 of them per launch
+    for (int64_t m0 = 0; m0 < M; m0 += 16 * 65535) {
+        const int rows = (int)(M - m0 < 16 * 65535 ? M - m0 : 16 * 65535);
+        const Int4Args a{X + m0 * K, Wp, scales_of(p, m), zeros ? zeros_of(p, m) : nullptr, rows, N, K, (int)m.KS,
+                         R ? R + m0 * N : nullptr, Y + m0 * N};
+        mv_rows(a, m.gps, s);
+    }
     return launched();
 }
 

@@ -223,8 +223,8 @@ int tri_linear_fused(const _Float16 *X, const uint8_t *const *Wp, const float *s
  * Rows past N and values past K hold code 8, scale 0 and zero point 8; groups that begin past K
  * likewise. */
 
-/* Bytes of a packed N x K matrix; -1 if a size is < 1 or >= 2^31, the group is unknown or the
- * matrix has 2^22 tiles or more (8.6e9 weights; every call here rejects such a matrix). */
+/* Bytes of a packed N x K matrix; -1 if a size is < 1, N >= 2^31, K >= 2^25, the group is unknown
+ * or the matrix has 2^22 tiles or more (8.6e9 weights): every call here rejects such a matrix. */
 int64_t tri_int4_bytes(int64_t N, int64_t K, int group, int zeros);
 
 /* Lay out codes that are given.  Q: N*K bytes (their low four bits count); S: N * ceil(K/group)
