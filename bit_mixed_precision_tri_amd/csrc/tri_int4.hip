@@ -364,16 +364,16 @@ __global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict_
         }
     };
 
-    // (an even number of turns keeps one code path; units past the end read zeros)
-    const int nu = (KS + U - 1) / U, turns = (nu + NW - 1) / NW;
+    // units u < nu are this wave's (wave-uniform)
+    const int nu = (KS + U - 1) / U;
     Unit t0, t1;
-    load(wv, t0);
-    load(wv + NW, t1);
-    for (int i = 0; i < turns; i += 2) {
+    int u = wv;
+    if (u < nu) load(u, t0);
+    for (; u < nu; u += 2 * NW) {
+        if (u + NW < nu) load(u + NW, t1);
         run(t0);
-        load(wv + (i + 2) * NW, t0);
-        if (i + 1 < turns) run(t1);
-        load(wv + (i + 3) * NW, t1);
+        if (u + 2 * NW < nu) load(u + 2 * NW, t0);
+        if (u + NW < nu) run(t1);
     }
 
     // sum over the lane groups that hold the same activation row, then over the waves in a fixed order
@@ -470,8 +470,8 @@ void mv_go(const Int4Args &a, hipStream_t s)
 {
     constexpr int NW = 8;
     const int blocks = (a.N + 15) / 16;
-    hipLaunchKernelGGL((k_int4_mv<MA, RB, GPS, ZP, NW, VEC>), dim3((blocks + RB - 1) / RB, (a.M + MA - 1) / MA), dim3(64 * NW),
-                       0, s, a.X, a.codes, a.scales, a.zeros, a.M, a.N, a.K, a.KS, a.R, a.Y);
+    hipLaunchKernelGGL((k_int4_mv<MA, RB, GPS, ZP, NW, VEC>), dim3((blocks + RB - 1) / RB, (a.M + MA - 1) / MA),
+                       dim3(64 * NW), 0, s, a.X, a.codes, a.scales, a.zeros, a.M, a.N, a.K, a.KS, a.R, a.Y);
 }
 
 template <int MA, int RB, bool VEC>
@@ -488,6 +488,37 @@ void mv_fmt(const Int4Args &a, int gps, hipStream_t s)
     }
 }
 
+// Blocks per workgroup: the busiest CU's rounds times (1 + RB), a workgroup costing about one block's work on top of
+// its blocks (the activations it loads), at most four; the larger on a tie.  Measured at 8 rows, group 128: 688 blocks
+// (4096 -> 11008) 9.0 / 8.5 / 7.4 / 7.9 us with RB = 1 .. 4 (3 taken), 256 blocks (11008 -> 4096) 8.4 / 10.0 / 12.3 /
+// 14.3 (1), 1792 blocks (8192 -> 28672) 38.4 / 29.5 / 29.3 / 29.1 (4); 64 rows in four slices 43 / 25 / - / 17.8 on 256
+// blocks (4).
+int blocks_per_workgroup(int64_t blocks, int64_t slices)
+{
+    const int64_t cus = cu_count();
+    int best = 1;
+    int64_t least = -1;
+    for (int rb = 4; rb >= 1; --rb) {
+        const int64_t cost = ((blocks + rb - 1) / rb * slices + cus - 1) / cus * (1 + rb);
+        if (least < 0 || cost < least) {
+            best = rb;
+            least = cost;
+        }
+    }
+    return best;
+}
+
+template <int MA>
+void mv_rb(const Int4Args &a, int gps, hipStream_t s)
+{
+    switch (blocks_per_workgroup((a.N + 15) / 16, (a.M + MA - 1) / MA)) {
+    case 1: mv_fmt<MA, 1, true>(a, gps, s); break;
+    case 2: mv_fmt<MA, 2, true>(a, gps, s); break;
+    case 3: mv_fmt<MA, 3, true>(a, gps, s); break;
+    default: mv_fmt<MA, 4, true>(a, gps, s); break;
+    }
+}
+
 void mv_rows(const Int4Args &a, int gps, hipStream_t s)
 {
     if (a.K % 8) {
@@ -495,11 +526,13 @@ void mv_rows(const Int4Args &a, int gps, hipStream_t s)
         else mv_fmt<16, 1, false>(a, gps, s);
         return;
     }
+    // up to four rows one block per workgroup: the activations are few (more blocks lost 10 - 90% at 256 and 688 blocks,
+    // and at most 5% was won at 1792)
     if (a.M <= 1) mv_fmt<1, 1, true>(a, gps, s);
     else if (a.M <= 2) mv_fmt<2, 1, true>(a, gps, s);
     else if (a.M <= 4) mv_fmt<4, 1, true>(a, gps, s);
-    else if (a.M <= 8) mv_fmt<8, 2, true>(a, gps, s);
-    else mv_fmt<16, 2, true>(a, gps, s);
+    else if (a.M <= 8) mv_rb<8>(a, gps, s);
+    else mv_rb<16>(a, gps, s);
 }
 
 }  // namespace
