@@ -3,8 +3,7 @@
 //   route    top-k of every token's logits and the stable order of the (token, expert) pairs by expert
 //   product  Y[r] = scale[e] X[rows[r]] W_e^T for the places r of expert e, one matrix or a gated pair
 //   combine  Y[t] = residual[t] + sum_j weights[t][j] Z[pos[t][j]]
-#include "tri_device.h"
-#include "tri_internal.h"
+#include "tri_experts.h"
 
 namespace tri {
 
@@ -269,35 +268,298 @@ constexpr int kRouteScanBlocks = 256;
 
 // ---------------------------------------------------------------- product
 
-// Simple form: one wave per place and output.
-template <int FMT>
-__global__ __launch_bounds__(256) void k_experts_rows(const Experts ex, int S)
+constexpr uint32_t kRsrcWord3 = 0x00020000u;     // raw buffer resource, gfx9 family
+constexpr uint32_t kOob = 0xFFFFFFF0u;           // an offset past every buffer here: reads zero
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *base, uint32_t bytes)
 {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, (int)kRsrcWord3);
+}
+
+__device__ __forceinline__ float4_t mfma(const u32x4 a, const u32x4 b, float4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, a), __builtin_bit_cast(half8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// A few rows per expert (tiles of MA = 1, 4 or 16 places): workgroup (x, y) computes RB blocks of 16 outputs of tile y.
+//
+// The eight waves split the row; wave w takes the chunk-steps w, w + 8, ..., where lane (g = lane/16, j = lane%16) reads
+// 16-byte chunk 4 s + g of weight row j of every block and decodes it to digits d = t + 1 in place, as exact fp16 values
+// d * 2^-24 (2-bit: masked, d * 4^p * 2^-24 at position p of a 16-bit half; 1.6-bit: multiply-shift quotients).  One
+// v_mfma_f32_16x16x32_f16 per position p contracts them; sum_k x, from products with ones, is taken off at the end.
+//
+// A operands.  A product's 8 values per lane are strided over the chunk (2-bit: 16 v + p and 16 v + 8 + p; 1.6-bit:
+// 5 q + p and 5 q + 40 + p), so the wave puts the step's activations in LDS, rows as they are, and gathers.  With fewer
+// rows than 16, A row MA c + a holds row a in the order of the c-th of 16/MA products: eight 2-byte reads per lane then
+// serve 16/MA products, and of product c's result the rows MA c .. MA c + MA-1 are taken.  With 16 rows every lane
+// reads its row's pieces whole and pairs the values in registers.
+//
+// Loads of the next step's activations and of the next kAhead steps' weights are in flight in registers.
+template <int FMT, int MA, int RB, bool PAIR, bool VEC>
+__global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int slot0)
+{
+    constexpr int NW = 8;
+    constexpr bool TWO = FMT == TRI_FMT_2BIT;
+    constexpr int XH = TWO ? 64 : 80;            // values per chunk
+    constexpr int NOP = TWO ? 8 : 10;            // products per chunk
+    constexpr int CL = MA == 1 ? NOP : 16 / MA;  // products per gathered A operand
+    constexpr int NSET = (NOP + CL - 1) / CL;
+    constexpr int NM = PAIR ? 2 : 1;             // matrices
+    constexpr int PR = 4 * XH / 8;               // 16-byte pieces of a row per step
+    constexpr int NLD = (MA * PR + 63) / 64;
+    constexpr int ROW = 4 * XH + 8;              // values of a row's place in LDS (16 bytes more than a step: banks)
+    constexpr int kAhead = 2;
+    // accumulators: one per product of an A operand and scale of its digits
+    constexpr int NACC = MA == 16 ? (TWO ? 6 : 2) : (TWO ? 8 : CL);
+    __shared__ __attribute__((aligned(16))) uint16_t xs[NW][MA][ROW];
+    __shared__ float red[NW][MA][16 * RB * NM + 1];
+
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int r = (int)(w / ex.N), n = (int)(w % ex.N);
-    if (r >= ex.R) return;
-    int e = -1;
-    for (int q = 0; q < ex.E; ++q)
-        if (r >= ex.offsets[q] && r < ex.offsets[q + 1]) e = q;
-    if (e < 0) return;
-    const int x = ex.rows ? ex.rows[r] : r;
-    if (x < 0 || x >= ex.T) return;
-    constexpr int PER = FMT == TRI_FMT_2BIT ? 4 : 5, BASE = FMT == TRI_FMT_2BIT ? 4 : 3;
-    float y[2] = {0.f, 0.f};
-    for (int q = 0; q < 2; ++q) {
-        if (!ex.Wp[q]) break;
-        const uint8_t *row = ex.Wp[q] + ((int64_t)e * ex.N + n) * S;
-        float acc[1] = {0.f};
-        for (int b = lane; b < S; b += 64) {
-            int v = row[b];
-            for (int i = 0; i < PER; ++i, v /= BASE)
-                if (PER * b + i < ex.K) acc[0] += (float)(v % BASE - 1) * h2f(ex.X[(int64_t)x * ex.K + PER * b + i]);
-        }
-        y[q] = wave_reduce_rows<1>(acc, lane) * ex.scale[q][e];
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    const ExpertTile et = expert_tile(ex.offsets, ex.E, ex.R, slot0 + (int)blockIdx.y, MA);
+    if (et.e < 0) return;                        // (the whole workgroup)
+    const int K = ex.K, N = ex.N;
+    const int64_t S = (int64_t)C * 16;
+    const int n0 = (int)blockIdx.x * 16 * RB;
+
+    // source rows of the tile, -1 where there is none: lane l holds row l's
+    int src = -1;
+    if (lane < et.rows) {
+        src = ex.rows ? ex.rows[et.r0 + lane] : et.r0 + lane;
+        if (src < 0 || src >= ex.T) src = -1;
     }
-    const float o = ex.Wp[1] ? y[0] / (1.f + __expf(-y[0])) * y[1] : y[0];
-    if (lane == 0) ex.Y[(int64_t)r * ex.N + n] = __builtin_bit_cast(uint16_t, (_Float16)o);
+    const int wrows = min(16 * RB, N - n0);
+    __amdgpu_buffer_rsrc_t wr[NM];
+#pragma unroll
+    for (int q = 0; q < NM; ++q)
+        wr[q] = rsrc(ex.Wp[q] + ((int64_t)et.e * N + n0) * S, __builtin_amdgcn_readfirstlane((uint32_t)(wrows * S)));
+    u32x4 w[kAhead][NM][RB];
+    auto load_w = [&](int s, u32x4 (&t)[NM][RB]) __attribute__((always_inline)) {
+        const int c = 4 * s + g;
+#pragma unroll
+        for (int q = 0; q < NM; ++q)
+#pragma unroll
+            for (int r = 0; r < RB; ++r)
+                t[q][r] = __builtin_amdgcn_raw_buffer_load_b128(
+                    wr[q], (int)(c < C ? (uint32_t)((16 * r + j) * S + 16 * c) : kOob), 0, 0);
+    };
+    const int ns = (C + 3) / 4;                  // steps of the row
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (wv + NW * i < ns) load_w(wv + NW * i, w[i]);
+
+    // activations of a step: piece P = 64 i + lane is piece P % PR of row P / PR
+    const uint16_t *xrow[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+        const int P = 64 * i + lane, row = P / PR;
+        const int r = row < MA ? __shfl(src, row < MA ? row : 0, 64) : -1;
+        xrow[i] = r >= 0 ? ex.X + (int64_t)r * K : nullptr;
+    }
+    u32x4 xv[NLD];
+    auto load_x = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < NLD; ++i) {
+            const int k = 4 * XH * s + 8 * ((64 * i + lane) % PR);
+            xv[i] = u32x4{0u, 0u, 0u, 0u};
+            if constexpr (VEC) {
+                if (xrow[i] && k < K) xv[i] = *reinterpret_cast<const u32x4 *>(xrow[i] + k);
+            } else if (xrow[i]) {                // rows that are no whole pieces: value by value
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = k + 2 * e < K ? xrow[i][k + 2 * e] : 0u;
+                    const uint32_t hi = k + 2 * e + 1 < K ? xrow[i][k + 2 * e + 1] : 0u;
+                    xv[i][e] = lo | hi << 16;
+                }
+            }
+        }
+    };
+    if (wv < ns) load_x(wv);
+
+    const float4_t zero4 = {0.f, 0.f, 0.f, 0.f};
+    float4_t acc[NM][RB][NACC], accx = zero4;
+#pragma unroll
+    for (int q = 0; q < NM; ++q)
+#pragma unroll
+        for (int r = 0; r < RB; ++r)
+#pragma unroll
+            for (int c = 0; c < NACC; ++c) acc[q][r][c] = zero4;
+    const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+
+    // digits of a chunk for product p (and, 1.6-bit, half hh: products 2 p + hh)
+    auto contract = [&](const u32x4 (&a)[MA == 16 ? NOP : NSET], const u32x4 v, float4_t (&ac)[NACC]) __attribute__((always_inline)) {
+        auto A = [&](int op) -> const u32x4 & { return a[MA == 16 ? op : op / CL]; };
+        if constexpr (TWO) {
+            const u32x4 u = v >> 12u;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const u32x4 b = p < 6 ? v & (0x00030003u << (2 * p)) : u & (0x00030003u << (2 * (p - 6)));
+                const int c = MA == 16 && p >= 6 ? p - 6 : p;
+                ac[c] = mfma(A(p), b, ac[c]);
+            }
+        } else {
+            uint32_t d[8][5];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) base3_digits_u16x2(byte_pair(v, q), d[q]);
+#pragma unroll
+            for (int op = 0; op < 10; ++op) {
+                const int p = op / 2, q = 4 * (op % 2), c = MA == 16 ? op % 2 : op % CL;
+                ac[c] = mfma(A(op), u32x4{d[q][p], d[q + 1][p], d[q + 2][p], d[q + 3][p]}, ac[c]);
+            }
+        }
+    };
+    auto step = [&](int s, u32x4 (&wc)[NM][RB]) __attribute__((always_inline)) {
+        // this step's activations into LDS, the next step's on the way
+#pragma unroll
+        for (int i = 0; i < NLD; ++i) {
+            const int P = 64 * i + lane, row = P / PR;
+            if (row < MA) *reinterpret_cast<u32x4 *>(&xs[wv][row][8 * (P % PR)]) = xv[i];
+        }
+        if (s + NW < ns) load_x(s + NW);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if constexpr (MA == 16) {
+            const u32x4 *row = reinterpret_cast<const u32x4 *>(&xs[wv][j][XH * g]);
+            uint32_t x32[XH / 2];
+#pragma unroll
+            for (int q = 0; q < XH / 8; ++q) {
+                const u32x4 v = row[q];
+                x32[4 * q] = v[0]; x32[4 * q + 1] = v[1]; x32[4 * q + 2] = v[2]; x32[4 * q + 3] = v[3];
+            }
+            u32x4 a[NOP];
+            if constexpr (TWO) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        a[p][v] = (p & 1) ? pair_halves<1>(x32[8 * v + 4 + p / 2], x32[8 * v + p / 2])
+                                          : pair_halves<0>(x32[8 * v + 4 + p / 2], x32[8 * v + p / 2]);
+            } else {
+#pragma unroll
+                for (int op = 0; op < 10; ++op)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int e = 5 * (4 * (op % 2) + q) + op / 2;   // value; its partner is e + 40
+                        a[op][q] = (e & 1) ? pair_halves<1>(x32[(e >> 1) + 20], x32[e >> 1])
+                                           : pair_halves<0>(x32[(e >> 1) + 20], x32[e >> 1]);
+                    }
+            }
+#pragma unroll
+            for (int p = 0; p < NOP; ++p) accx = mfma(a[p], ones, accx);
+#pragma unroll
+            for (int q = 0; q < NM; ++q)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) contract(a, wc[q][r], acc[q][r]);
+        } else {
+            u32x4 a[NSET];
+            const int aa = j % MA, c = j / MA;   // (MA = 1: A rows past the products repeat the last one's, unused)
+#pragma unroll
+            for (int t = 0; t < NSET; ++t) {
+                const int op = min(CL * t + (MA == 1 ? min(c, CL - 1) : c), NOP - 1);
+                const uint16_t *x = &xs[wv][aa][XH * g + (TWO ? op : 5 * 4 * (op & 1) + (op >> 1))];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint32_t lo = x[TWO ? 16 * v : 5 * v], hi = x[TWO ? 16 * v + 8 : 5 * v + 40];
+                    a[t][v] = lo | hi << 16;
+                }
+                if (NOP % CL && t == NSET - 1 && CL * t + c >= NOP) a[t] = u32x4{0u, 0u, 0u, 0u};   // no product left
+                accx = mfma(a[t], ones, accx);
+            }
+#pragma unroll
+            for (int q = 0; q < NM; ++q)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) contract(a, wc[q][r], acc[q][r]);
+        }
+    };
+    for (int s = wv; s < ns; s += NW * kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s + NW * i < ns) {
+                step(s + NW * i, w[i]);
+                if (s + NW * (i + kAhead) < ns) load_w(s + NW * (i + kAhead), w[i]);
+            }
+        }
+    }
+
+    // Merge: product op's rows of result r lie in A rows MA c + a, c = op % CL: lane group (MA c + a) / 4, element
+    // (MA c + a) % 4.  Lanes take what is theirs, and the lane groups that hold the same row are added.
+    auto unit = [&](int p) { return TWO ? 1.f / (float)(1 << (2 * (p < 6 ? p : p - 6))) : 1.f; };
+    auto put = [&](int col, float (&v)[4]) __attribute__((always_inline)) {   // v[e]: this lane's rows
+        if constexpr (MA == 16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[wv][4 * g + e][col] = v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < MA; ++e) {
+                const float t = sum_over_rows(v[e]);
+                if (g == 0) red[wv][e][col] = t;
+            }
+        }
+    };
+#pragma unroll
+    for (int q = 0; q < NM; ++q)
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (MA == 16) {
+#pragma unroll
+                for (int c = 0; c < NACC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += acc[q][r][c][e] * unit(c);
+            } else if constexpr (MA == 4) {      // class c in lane group c
+#pragma unroll
+                for (int c = 0; c < NACC; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] += g == c % 4 ? acc[q][r][c][e] * unit(c) : 0.f;
+            } else {                             // product c: lane group c / 4, element c % 4
+#pragma unroll
+                for (int c = 0; c < NACC; ++c) v[0] += g == c / 4 ? acc[q][r][c][c % 4] * unit(c) : 0.f;
+            }
+            put(16 * (RB * q + r) + j, v);
+        }
+    // sum_k x: every product of an A operand counts once
+    {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (MA == 1) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[0] += 4 * g + c < CL ? accx[c] : 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = accx[e];
+        }
+        if constexpr (MA == 16) {
+            if (j == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) red[wv][4 * g + e][16 * RB * NM] = v[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < MA; ++e) {
+                const float t = sum_over_rows(v[e]);
+                if (lane == 0) red[wv][e][16 * RB * NM] = t;
+            }
+        }
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < MA * 16 * RB; o += 64 * NW) {
+        const int m = o / (16 * RB), c = o % (16 * RB);
+        if (m >= et.rows || n0 + c >= N) continue;
+        const int row = ex.rows ? ex.rows[et.r0 + m] : et.r0 + m;
+        if (row < 0 || row >= ex.T) continue;
+        float sx = 0.f, sd[NM] = {};
+#pragma unroll
+        for (int q = 0; q < NW; ++q) {
+            sx += red[q][m][16 * RB * NM];
+#pragma unroll
+            for (int p = 0; p < NM; ++p) sd[p] += red[q][m][16 * RB * p + c];
+        }
+        float y = (sd[0] * 16777216.0f - sx) * ex.scale[0][et.e];
+        if constexpr (PAIR) y = y / (1.f + __expf(-y)) * ((sd[NM - 1] * 16777216.0f - sx) * ex.scale[1][et.e]);
+        ex.Y[(int64_t)(et.r0 + m) * N + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)y);
+    }
 }
 
 // ---------------------------------------------------------------- combination
@@ -400,14 +662,41 @@ int launch_route(const void *logits, bool half, int T, int E, int topk, bool ren
     return launched();
 }
 
+namespace {
+
+template <int FMT, int MA, int RB, bool PAIR, bool VEC>
+void experts_go(const Experts &ex, hipStream_t s)
+{
+    const int C = (int)(row_bytes(ex.K, FMT) / 16);
+    const int64_t slots = expert_slots(ex.R, ex.E, MA);
+    for (int64_t s0 = 0; s0 < slots; s0 += 65535) {   // (the second grid dimension's limit)
+        const dim3 grid((ex.N + 16 * RB - 1) / (16 * RB), (unsigned)(slots - s0 < 65535 ? slots - s0 : 65535));
+        hipLaunchKernelGGL((k_experts_mv<FMT, MA, RB, PAIR, VEC>), grid, dim3(512), 0, s, ex, C, (int)s0);
+    }
+}
+
+template <int FMT, bool PAIR, bool VEC>
+int experts_ma(const Experts &ex, hipStream_t s)
+{
+    if (ex.R <= ex.E / 2) experts_go<FMT, 1, 1, PAIR, VEC>(ex, s);
+    else if (ex.R / 2 <= ex.E) experts_go<FMT, 4, 1, PAIR, VEC>(ex, s);
+    else experts_go<FMT, 16, 1, PAIR, VEC>(ex, s);
+    return launched();
+}
+
+template <int FMT>
+int experts_fmt(const Experts &ex, hipStream_t s)
+{
+    const bool vec = ex.K % 8 == 0;
+    if (ex.Wp[1]) return vec ? experts_ma<FMT, true, true>(ex, s) : experts_ma<FMT, true, false>(ex, s);
+    return vec ? experts_ma<FMT, false, true>(ex, s) : experts_ma<FMT, false, false>(ex, s);
+}
+
+}  // namespace
+
 int launch_experts(const Experts &ex, int fmt, hipStream_t s)
 {
-    const int S = (int)row_bytes(ex.K, fmt);
-    const int64_t wgs = ((int64_t)ex.R * ex.N + 3) / 4;
-    if (wgs >= ((int64_t)1 << 24)) return TRI_EINVAL;
-    if (fmt == TRI_FMT_2BIT) hipLaunchKernelGGL(k_experts_rows<TRI_FMT_2BIT>, dim3((unsigned)wgs), dim3(256), 0, s, ex, S);
-    else hipLaunchKernelGGL(k_experts_rows<TRI_FMT_1P6BIT>, dim3((unsigned)wgs), dim3(256), 0, s, ex, S);
-    return launched();
+    return fmt == TRI_FMT_2BIT ? experts_fmt<TRI_FMT_2BIT>(ex, s) : experts_fmt<TRI_FMT_1P6BIT>(ex, s);
 }
 
 int launch_combine(const uint16_t *Z, int64_t R, const int32_t *pos, const float *weights, const uint16_t *res, int T,
