@@ -696,6 +696,7 @@ int experts_fmt(const Experts &ex, hipStream_t s)
 
 int launch_experts(const Experts &ex, int fmt, hipStream_t s)
 {
+    if (ex.R / 2 >= ex.E && experts_gemm_fits(ex, fmt)) return launch_experts_gemm(ex, fmt, s);
     return fmt == TRI_FMT_2BIT ? experts_fmt<TRI_FMT_2BIT>(ex, s) : experts_fmt<TRI_FMT_1P6BIT>(ex, s);
 }
 

@@ -38,10 +38,15 @@
 // Workgroups are mapped to tiles XCD by XCD: consecutive workgroups of one XCD take
 // consecutive row tiles of the same column tiles, so they share weights and activations in
 // that XCD's L2.
+//
+// Experts (MODE kExperts, kPair).  The row tiles are those of a list that cuts every expert's places into tiles of BM
+// (expert_tile: the sizes are on the device, the grid is their upper bound and tiles past the list end at once); the
+// tile's rows of X are gathered by the load offsets, its weights and scale are its expert's.  kPair: half of a wave's
+// column tiles are those of the second matrix, for the same output columns, and silu(gate) * up is formed from the two
+// accumulators.
 #include <type_traits>
 
-#include "tri_device.h"
-#include "tri_internal.h"
+#include "tri_experts.h"
 
 namespace tri {
 
@@ -101,11 +106,16 @@ constexpr int kBN = 512;             // columns of Y per tile (4 waves side by s
 // A workgroup computes one BM x 512 tile of Y (NT = 4), one half of it, BM x 256 (NT = 2), or one
 // quarter, BM x 128 (NT = 1): part blockIdx.x % (4/NT) of tile tile_base + blockIdx.x / (4/NT) in
 // the tile order.  BM is 128, or 64 for a middling M (each wave then covers 64 rows).
-template <int FMT, int NT, int BM>
-__global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, const uint8_t *__restrict__ Wp,
-                                              float scale, int M, int N, int K, int C, int tiles_m, int tiles_n,
-                                              int tile_base, uint16_t *__restrict__ Y)
+enum { kLayer = 0, kExperts = 1, kPair = 2 };
+
+template <int FMT, int NT, int BM, int MODE>
+__device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const uint8_t *__restrict__ Wp, float scale,
+                                          int M, int N, int K, int C, int tiles_m, int tiles_n, int tile_base,
+                                          uint16_t *__restrict__ Y, const Experts &ex)
 {
+    constexpr bool EXP = MODE != kLayer, PAIR = MODE == kPair;
+    constexpr int NB = PAIR ? NT / 2 : NT;       // column tiles of one matrix
+    static_assert(!PAIR || NT % 2 == 0, "a pair takes column tiles of both matrices");
     constexpr int kNT = NT;                      // 32-column MFMA tiles per wave
     constexpr int kBMt = BM;                     // rows of Y per workgroup (128, or 64 for few rows)
     constexpr int kMTt = BM / 32;                // 32-row MFMA tiles per wave
@@ -154,22 +164,47 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
     const int tm = first_m + in_band % band_m;
     const int tn = in_band / band_m;
     const int m0 = tm * kBMt;
-    const int n0 = tn * kBN + (bid % kParts) * (kBN / kParts) + 32 * kNT * wv;   // this wave's first column
+    constexpr int kCols = PAIR ? kBN / 2 : kBN;  // output columns of a tile
+    const int n0 = tn * kCols + (bid % kParts) * (kCols / kParts) + 32 * NB * wv;   // this wave's first column
+
+    // experts: the tile's expert, rows and their sources
+    __shared__ int source[EXP ? BM : 1];
+    ExpertTile et{0, 0, 0};
+    if constexpr (EXP) {
+        et = expert_tile(ex.offsets, ex.E, ex.R, tm, BM);
+        if (et.e < 0) return;                    // (the whole workgroup)
+        if (tid < BM) {
+            int src = -1;
+            if (tid < et.rows) {
+                src = ex.rows ? ex.rows[et.r0 + tid] : et.r0 + tid;
+                if (src < 0 || src >= ex.T) src = -1;
+            }
+            source[tid] = src;
+        }
+        __syncthreads();
+        Y += (int64_t)et.r0 * N;
+        M = m0 + et.rows;
+        scale = ex.scale[0][et.e];
+    }
 
     if constexpr (!TWO) {
         lut[tid] = base3_digits_2bit((uint32_t)tid);   // 256 threads, one entry each
     }
 
-    const uint32_t xbytes = __builtin_amdgcn_readfirstlane((uint32_t)((int64_t)min(kBMt, M - m0) * K * 2));
-    const __amdgpu_buffer_rsrc_t xr = rsrc(X + (int64_t)m0 * K, xbytes);
+    // (experts: rows in order are addressed from the tile's first, gathered ones from X's)
+    const uint32_t xbytes = __builtin_amdgcn_readfirstlane(
+        EXP && ex.rows ? (uint32_t)((int64_t)ex.T * K * 2) : (uint32_t)((int64_t)min(kBMt, M - m0) * K * 2));
+    const __amdgpu_buffer_rsrc_t xr = rsrc(EXP ? (ex.rows ? X : X + (int64_t)et.r0 * K) : X + (int64_t)m0 * K, xbytes);
     // weights: lane (h, c) of column tile nt reads row n0 + 32nt + c, bytes 16h.. of each slice
     const int64_t S = (int64_t)C * 16;
-    const int rows_here = min(32 * kNT, N - n0); // may be <= 0 for the last workgroup's high waves
+    const int rows_here = min(32 * NB, N - n0);  // may be <= 0 for the last workgroup's high waves
     // (readfirstlane keeps the descriptor fields in scalar registers: a descriptor the compiler
     // believes divergent turns every buffer load into a loop)
     const uint32_t wbytes = __builtin_amdgcn_readfirstlane((uint32_t)((rows_here > 0 ? rows_here : 0) * S));
     const int wrow = __builtin_amdgcn_readfirstlane(min(n0, N - 1));
-    const __amdgpu_buffer_rsrc_t wr = rsrc(Wp + (int64_t)wrow * S, wbytes);
+    const int64_t first_row = EXP ? (int64_t)et.e * N + wrow : (int64_t)wrow;
+    const __amdgpu_buffer_rsrc_t wr = rsrc((EXP ? ex.Wp[0] : Wp) + first_row * S, wbytes);
+    const __amdgpu_buffer_rsrc_t wr2 = rsrc(PAIR ? ex.Wp[1] + first_row * S : nullptr, PAIR ? wbytes : 0u);
     const int KT = (C + 1) / 2;                  // K tiles (two 16-byte chunks each)
     const int KTe = (KT + 1) & ~1;               // padded to an even count (see the tile loop)
 
@@ -178,8 +213,10 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
     // offset past the buffer.  (The out-of-range offset is held in a register: as a literal it
     // would be rebuilt before every select.)  Instruction I of a tile (the wave's i-th) fills
     // rows 16 (I / (PR/4)) + lane / 4, pieces 4 (I % (PR/4)) + ((lane % 4) ^ (lane / 16)).
+    // (Gathered rows may lie past 2 GiB of X, at most at 4 GiB - 16.)
     uint32_t oob;
-    asm volatile("v_mov_b32 %0, 0x80000000" : "=v"(oob));
+    if constexpr (EXP) asm volatile("v_mov_b32 %0, 0xFFFFFFF0" : "=v"(oob));
+    else asm volatile("v_mov_b32 %0, 0x80000000" : "=v"(oob));
     auto piece_of = [&](int i) { return 4 * ((wv * NI + i) % (PR / 4)) + ((lane & 3) ^ (lane >> 4)); };
     auto row_of = [&](int i) { return 16 * ((wv * NI + i) / (PR / 4)) + (lane >> 2); };
     uint32_t xoff[NI];
@@ -187,8 +224,14 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int row = row_of(i);
-        xoff[i] = (uint32_t)(row * K + 8 * piece_of(i)) * 2u;
-        klim[i] = K - 8 * piece_of(i);
+        if constexpr (EXP) {
+            const int src = source[row];
+            xoff[i] = ((uint32_t)(ex.rows ? src : row) * (uint32_t)K + 8u * (uint32_t)piece_of(i)) * 2u;
+            klim[i] = src >= 0 ? K - 8 * piece_of(i) : -1;
+        } else {
+            xoff[i] = (uint32_t)(row * K + 8 * piece_of(i)) * 2u;
+            klim[i] = K - 8 * piece_of(i);
+        }
     }
     // Activations of K tile kt into buffer `buf` (tiles past the end read zeros).  The K test
     // is a per-lane select, not a branch: a branch would split the tile body into blocks, and
@@ -206,8 +249,8 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
     auto load_b = [&](int kt, u32x4 (&wb)[kNT]) {
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-            const uint32_t off = (uint32_t)((32 * nt + c) * S + kt * 32 + 16 * h);
-            wb[nt] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)off, 0, 0);
+            const uint32_t off = (uint32_t)((32 * (nt % NB) + c) * S + kt * 32 + 16 * h);
+            wb[nt] = __builtin_amdgcn_raw_buffer_load_b128(nt < NB ? wr : wr2, (int)off, 0, 0);
         }
     };
 
@@ -354,6 +397,27 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
     wait_vm<0>();                                // (the last tile's loads to LDS, past the end, are in)
 
     // epilogue: lane (h, c) holds rows 32mt + 8i + 4h + v of column 32nt + c
+    if constexpr (EXP) {
+        float scale2 = 0.f;
+        if constexpr (PAIR) scale2 = ex.scale[1][et.e];
+#pragma unroll
+        for (int mt = 0; mt < kMTt; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int m = 32 * mt + 8 * i + 4 * h + v;
+                    if (source[m] < 0) continue;
+#pragma unroll
+                    for (int nt = 0; nt < NB; ++nt) {
+                        const int n = n0 + 32 * nt + c;
+                        float y = acc[mt][nt][4 * i + v] * scale;
+                        if constexpr (PAIR) y = y / (1.f + __expf(-y)) * (acc[mt][nt + NB][4 * i + v] * scale2);
+                        if (n < N) Y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (_Float16)y);
+                    }
+                }
+        return;
+    }
 #pragma unroll
     for (int mt = 0; mt < kMTt; ++mt)
 #pragma unroll
@@ -368,6 +432,20 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
                         Y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (_Float16)(acc[mt][nt][4 * i + v] * scale));
                 }
         }
+}
+
+template <int FMT, int NT, int BM>
+__global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, const uint8_t *__restrict__ Wp,
+                                              float scale, int M, int N, int K, int C, int tiles_m, int tiles_n,
+                                              int tile_base, uint16_t *__restrict__ Y)
+{
+    gemm_tile<FMT, NT, BM, kLayer>(X, Wp, scale, M, N, K, C, tiles_m, tiles_n, tile_base, Y, Experts{});
+}
+
+template <int FMT, int NT, int BM, int MODE>
+__global__ __launch_bounds__(256) void k_gemm_experts(const Experts ex, int C, int tiles_m, int tiles_n, int tile_base)
+{
+    gemm_tile<FMT, NT, BM, MODE>(ex.X, nullptr, 0.f, 0, ex.N, ex.K, C, tiles_m, tiles_n, tile_base, ex.Y, ex);
 }
 
 template <int FMT>
@@ -428,6 +506,49 @@ int launch_gemm(const uint16_t *X, const uint8_t *Wp, float scale, int64_t M, in
         if (rc != TRI_OK) return rc;
     }
     return TRI_OK;
+}
+
+template <int FMT, int NT, int BM, int MODE>
+static int launch_experts_tiles(const Experts &ex, int C, hipStream_t s)
+{
+    const int cols = MODE == kPair ? kBN / 2 : kBN;
+    const int64_t tiles_m = expert_slots(ex.R, ex.E, BM), tiles_n = (ex.N + cols - 1) / cols;
+    const int64_t wgs = tiles_m * tiles_n * (4 / NT);
+    constexpr int64_t most = (int64_t)1 << 22;   // workgroups of a launch
+    for (int64_t w0 = 0; w0 < wgs; w0 += most)
+        hipLaunchKernelGGL((k_gemm_experts<FMT, NT, BM, MODE>), dim3((unsigned)(wgs - w0 < most ? wgs - w0 : most)),
+                           dim3(256), 0, s, ex, C, (int)tiles_m, (int)tiles_n, (int)(w0 / (4 / NT)));
+    return hipGetLastError() == hipSuccess ? TRI_OK : TRI_EHIP;
+}
+
+bool experts_gemm_fits(const Experts &ex, int fmt)
+{
+    // 32-bit offsets as in launch_gemm: a 128-row block of activations in order, and of weights; pieces of 8 values
+    // (and the tile count of a launch in int range)
+    const int64_t tiles = expert_slots(ex.R, ex.E, 64) * ((ex.N + 255) / 256);
+    return tiles < ((int64_t)1 << 30) && ex.K % 8 == 0 && 128 * (int64_t)ex.K * 2 < ((int64_t)1 << 31) && 128 * row_bytes(ex.K, fmt) < ((int64_t)1 << 31);
+}
+
+// Tiles of 64 places, whatever the sizes: several such workgroups share a CU, the last tile of an expert wastes little,
+// and 128-place tiles lost at every measured size (pair, 2-bit, 4096 -> 11008, eight experts, two per token: 256 tokens
+// 150 against 202 us, 2048 tokens 655 against 654 (256 columns) and 727 us (512); 1.6-bit 798 against 828 - 1029).  Two
+// column tiles per wave for a pair; for one matrix one, or two for 2-bit digits where those still make two rounds
+// (11008 -> 4096, 2048 tokens 369 -> 332 us, 256 tokens 82 -> 85 us; 1.6-bit 421 -> 422 us, 256 tokens 101 -> 122 us).
+template <int FMT>
+static int launch_experts_fmt(const Experts &ex, hipStream_t s)
+{
+    const int C = (int)(row_bytes(ex.K, FMT) / 16);
+    if (ex.Wp[1]) return launch_experts_tiles<FMT, 2, 64, kPair>(ex, C, s);
+    if constexpr (FMT == TRI_FMT_2BIT) {
+        if (expert_slots(ex.R, ex.E, 64) * ((ex.N + 255) / 256) >= 2 * (int64_t)cu_count())
+            return launch_experts_tiles<FMT, 2, 64, kExperts>(ex, C, s);
+    }
+    return launch_experts_tiles<FMT, 1, 64, kExperts>(ex, C, s);
+}
+
+int launch_experts_gemm(const Experts &ex, int fmt, hipStream_t s)
+{
+    return fmt == TRI_FMT_2BIT ? launch_experts_fmt<TRI_FMT_2BIT>(ex, s) : launch_experts_fmt<TRI_FMT_1P6BIT>(ex, s);
 }
 
 }  // namespace tri

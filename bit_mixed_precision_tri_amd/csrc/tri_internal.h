@@ -200,6 +200,9 @@ int64_t route_workspace_bytes(int64_t T, int E, int topk);
 int launch_route(const void *logits, bool half, int T, int E, int topk, bool renorm, int32_t *ids, float *weights,
                  int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace, hipStream_t s);
 int launch_experts(const Experts &ex, int fmt, hipStream_t s);
+// tri_gemm.hip: row tiles of 64 places, for shapes that fit its 32-bit offsets.
+bool experts_gemm_fits(const Experts &ex, int fmt);
+int launch_experts_gemm(const Experts &ex, int fmt, hipStream_t s);
 int launch_combine(const uint16_t *Z, int64_t R, const int32_t *pos, const float *weights, const uint16_t *res, int T,
                    int topk, int N, uint16_t *Y, hipStream_t s);
 int launch_probe_read(const void *src, int64_t bytes, uint32_t *sink, hipStream_t s);
