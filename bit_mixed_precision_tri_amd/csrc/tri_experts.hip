@@ -318,7 +318,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, j = lane & 15;
-    const ExpertTile et = expert_tile(ex.offsets, ex.E, ex.R, slot0 + (int)blockIdx.y, MA);
+    const ExpertTile et = expert_tile(ex.offsets, ex.E, ex.R, MA, [&](int) { return slot0 + (int)blockIdx.y; });
     if (et.e < 0) return;                        // (the whole workgroup)
     const int K = ex.K, N = ex.N;
     const int64_t S = (int64_t)C * 16;
@@ -562,6 +562,302 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     }
 }
 
+// The same product with the activations kept: rows short enough that a wave's A operands of all its CST steps stay in
+// registers (gathered once, as above; tiles of MA = 1, 4, 8 or 16 places).  The workgroup then runs through blocks of 16
+// outputs, blockIdx.x, + gridDim.x, ...: only weights are read, the next block's chunks in flight while one is
+// contracted; the waves' partial sums meet in one of two LDS buffers in turn, so a block costs one barrier.
+constexpr int kHeld = 16;                        // blocks whose results wait in LDS
+// Whether the loop's registers for A operands and for D blocks' chunks leave the rest of its code enough of 128 registers
+// (two workgroups per CU) that the compiler spills nothing, or next to nothing; limits as found by compiling.
+constexpr bool loop_fits(int fmt, int ma, int cst, bool pair, int d)
+{
+    const int nop = fmt == TRI_FMT_2BIT ? 8 : 10, cl = ma == 1 ? nop : 16 / ma, na = (nop + cl - 1) / cl;
+    return 4 * cst * (na + (pair ? 2 : 1) * d) <= (fmt == TRI_FMT_2BIT ? 80 : ma == 1 ? 40 : 64);
+}
+// Waves per SIMD to compile for, and blocks in registers: three workgroups per CU with one block each where the registers
+// are very few (a pair of one row: 12.3 us against 13.8 with two of two blocks); else two per CU where they fit, with the
+// next block's chunks in flight (D = 2) or, failing that, one workgroup's loads under the other's products (D = 1); else
+// one.
+constexpr bool loop_light(int fmt, int ma, int cst, bool pair) { return ma == 1 && fmt == TRI_FMT_2BIT && pair && cst <= 2; }
+constexpr int loop_waves(int fmt, int ma, int cst, bool pair)
+{
+    return loop_light(fmt, ma, cst, pair) ? 6 : loop_fits(fmt, ma, cst, pair, 1) ? 4 : 2;
+}
+constexpr int loop_depth(int fmt, int ma, int cst, bool pair)
+{
+    if (loop_light(fmt, ma, cst, pair)) return 1;
+    return loop_fits(fmt, ma, cst, pair, 2) || !loop_fits(fmt, ma, cst, pair, 1) ? 2 : 1;
+}
+
+template <int FMT, int MA, int CST, bool PAIR, int D, int EU>
+__global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int C)
+{
+    constexpr int NW = 8;
+    constexpr bool TWO = FMT == TRI_FMT_2BIT;
+    constexpr int XH = TWO ? 64 : 80;            // values per chunk
+    constexpr int NOP = TWO ? 8 : 10;            // products per chunk
+    constexpr int CL = MA == 1 ? NOP : 16 / MA;  // products per gathered A operand
+    constexpr int NA = MA == 16 ? NOP : (NOP + CL - 1) / CL;   // A operands per step
+    constexpr int NM = PAIR ? 2 : 1;             // matrices
+    constexpr int PR = 4 * XH / 8;               // 16-byte pieces of a row per step
+    constexpr int NLD = (MA * PR + 63) / 64;
+    constexpr int ROW = 4 * XH + 8;              // values of a row's place in LDS (16 bytes more than a step: banks)
+    // accumulators by (product's place in the A operand, scale of its digits)
+    constexpr int NACC = TWO ? (MA >= 8 ? 6 : 8) : (MA == 16 ? 2 : CL);
+    // (the activations' passage and, after it, the partial sums use the same LDS)
+    constexpr int XS = NW * MA * ROW * 2, RED = 2 * NW * MA * (16 * NM + 1) * 4;
+    __shared__ u32x4 smem[((XS > RED ? XS : RED) + 15) / 16];
+    auto xs = reinterpret_cast<uint16_t (*)[MA][ROW]>(smem);
+    auto red = reinterpret_cast<float (*)[NW][MA][16 * NM + 1]>(smem);
+    __shared__ float sxw[NW][MA], sxt[MA];
+    __shared__ uint16_t done[kHeld][MA][16];     // results not yet written
+    __shared__ int source[MA];
+
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = lane >> 4, j = lane & 15;
+    const int K = ex.K, N = ex.N;
+    const int64_t S = (int64_t)C * 16;
+    const int nblk = (N + 15) / 16;
+    // The tiles share the workgroups evenly (there are at least as many): tile t has workgroups t G .. t G + G - 1, of
+    // which the q-th takes blocks q, q + G, ...
+    int G = 1;
+    const ExpertTile et = expert_tile(ex.offsets, ex.E, ex.R, MA, [&](int tiles) {
+        G = min((int)gridDim.x / max(tiles, 1), nblk);
+        return (int)blockIdx.x / G;
+    });
+    if (et.e < 0) return;                        // (the whole workgroup)
+    int src = -1;                                // source rows of the tile: lane l holds row l's
+    if (lane < et.rows) {
+        src = ex.rows ? ex.rows[et.r0 + lane] : et.r0 + lane;
+        if (src < 0 || src >= ex.T) src = -1;
+    }
+    if (wv == 0 && lane < MA) source[lane] = src;
+
+    const uint8_t *W[NM];
+#pragma unroll
+    for (int q = 0; q < NM; ++q) W[q] = ex.Wp[q] + (int64_t)et.e * N * S;
+    auto load_w = [&](int b, u32x4 (&t)[NM][CST]) __attribute__((always_inline)) {
+        const int rows = min(16, N - 16 * b);
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            const __amdgpu_buffer_rsrc_t wr =
+                rsrc(W[q] + 16 * (int64_t)b * S, __builtin_amdgcn_readfirstlane((uint32_t)(rows * S)));
+#pragma unroll
+            for (int i = 0; i < CST; ++i) {
+                const int c = 4 * (wv + NW * i) + g;
+                t[q][i] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)(c < C ? (uint32_t)(j * S + 16 * c) : kOob), 0, 0);
+            }
+        }
+    };
+    u32x4 w[D][NM][CST];
+    int b = (int)blockIdx.x % G;
+#pragma unroll
+    for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i)
+        if (b + i * G < nblk) load_w(b + i * G, w[i]);
+
+    // activations: piece P = 64 i + lane of a step is piece P % PR of row P / PR
+    const float4_t zero4 = {0.f, 0.f, 0.f, 0.f};
+    const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+    u32x4 a[CST][NA];
+    {
+        const uint16_t *xrow[NLD];
+#pragma unroll
+        for (int i = 0; i < NLD; ++i) {
+            const int row = (64 * i + lane) / PR;
+            const int r = row < MA ? __shfl(src, row < MA ? row : 0, 64) : -1;
+            xrow[i] = r >= 0 ? ex.X + (int64_t)r * K : nullptr;
+        }
+        u32x4 xv[CST][NLD];
+#pragma unroll
+        for (int t = 0; t < CST; ++t)
+#pragma unroll
+            for (int i = 0; i < NLD; ++i) {
+                const int k = 4 * XH * (wv + NW * t) + 8 * ((64 * i + lane) % PR);
+                xv[t][i] = u32x4{0u, 0u, 0u, 0u};
+                if (xrow[i] && k < K) xv[t][i] = *reinterpret_cast<const u32x4 *>(xrow[i] + k);
+            }
+        float4_t accx = zero4;
+#pragma unroll
+        for (int t = 0; t < CST; ++t) {
+#pragma unroll
+            for (int i = 0; i < NLD; ++i) {
+                const int P = 64 * i + lane, row = P / PR;
+                if (row < MA) *reinterpret_cast<u32x4 *>(&xs[wv][row][8 * (P % PR)]) = xv[t][i];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if constexpr (MA == 16) {
+                const u32x4 *row = reinterpret_cast<const u32x4 *>(&xs[wv][j][XH * g]);
+                uint32_t x32[XH / 2];
+#pragma unroll
+                for (int q = 0; q < XH / 8; ++q) {
+                    const u32x4 v = row[q];
+                    x32[4 * q] = v[0]; x32[4 * q + 1] = v[1]; x32[4 * q + 2] = v[2]; x32[4 * q + 3] = v[3];
+                }
+#pragma unroll
+                for (int op = 0; op < NOP; ++op)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        // 2-bit: values 16 q + op and its partner 8 on; 1.6-bit: 5 (4 (op % 2) + q) + op / 2 and 40 on
+                        const int e = TWO ? 16 * q + op : 5 * (4 * (op % 2) + q) + op / 2, f = e + (TWO ? 8 : 40);
+                        a[t][op][q] = (e & 1) ? pair_halves<1>(x32[f >> 1], x32[e >> 1]) : pair_halves<0>(x32[f >> 1], x32[e >> 1]);
+                    }
+            } else {
+                const int aa = j % MA, c = MA == 1 ? min(j, CL - 1) : j / MA;
+#pragma unroll
+                for (int q = 0; q < NA; ++q) {
+                    const int op = CL * q + c;
+                    const uint16_t *x = &xs[wv][aa][XH * g + (TWO ? op : 20 * (op & 1) + (op >> 1))];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const uint32_t lo = x[TWO ? 16 * v : 5 * v], hi = x[TWO ? 16 * v + 8 : 5 * v + 40];
+                        a[t][q][v] = lo | hi << 16;
+                    }
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+            for (int q = 0; q < NA; ++q) accx = mfma(a[t][q], ones, accx);
+        }
+        // sum_k x of every row: each product of an A operand counts once
+        if constexpr (MA == 16) {
+            if (j == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sxw[wv][4 * g + e] = accx[e];
+            }
+        } else if constexpr (MA == 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float p = accx[e], q = accx[e];
+                swap32(p, q);
+                if (j == 0 && g < 2) sxw[wv][4 * g + e] = p + q;
+            }
+        } else {
+            float v = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v += 4 * g + c < CL ? accx[c] : 0.f;
+            v = sum_over_rows(v);
+            if (lane == 0) sxw[wv][0] = v;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < MA) {
+        float t = 0.f;
+#pragma unroll
+        for (int q = 0; q < NW; ++q) t += sxw[q][threadIdx.x];
+        sxt[threadIdx.x] = t;                    // (read after the first block's barrier)
+    }
+    float scale[NM];
+#pragma unroll
+    for (int q = 0; q < NM; ++q) scale[q] = ex.scale[q][et.e];
+
+    auto contract = [&](const u32x4 (&x)[NA], const u32x4 v, float4_t (&ac)[NACC]) __attribute__((always_inline)) {
+        auto A = [&](int op) -> const u32x4 & { return x[MA == 16 ? op : op / CL]; };
+        if constexpr (TWO) {
+            const u32x4 u = v >> 12u;
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const u32x4 d = p < 6 ? v & (0x00030003u << (2 * p)) : u & (0x00030003u << (2 * (p - 6)));
+                const int c = NACC == 6 && p >= 6 ? p - 6 : p;
+                ac[c] = mfma(A(p), d, ac[c]);
+            }
+        } else {
+            uint32_t d[8][5];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) base3_digits_u16x2(byte_pair(v, q), d[q]);
+#pragma unroll
+            for (int op = 0; op < 10; ++op) {
+                const int p = op / 2, q = 4 * (op % 2), c = MA == 16 ? op % 2 : op % CL;
+                ac[c] = mfma(A(op), u32x4{d[q][p], d[q + 1][p], d[q + 2][p], d[q + 3][p]}, ac[c]);
+            }
+        }
+    };
+    // scale of accumulator c's digits
+    auto unit = [&](int c) { return TWO ? 1.f / (float)(1 << (2 * (c < 6 ? c : c - 6))) : 1.f; };
+    auto run = [&](const u32x4 (&wc)[NM][CST], int buf, int held) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            float4_t acc[NACC];
+#pragma unroll
+            for (int c = 0; c < NACC; ++c) acc[c] = zero4;
+#pragma unroll
+            for (int i = 0; i < CST; ++i) contract(a[i], wc[q][i], acc);
+            // product op's rows of the result lie in A rows MA c + a, c = op % CL: lane group (MA c + a) / 4
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < NACC; ++c) {
+                if constexpr (MA == 1) {
+                    v[0] += g == c / 4 ? acc[c][c % 4] * unit(c) : 0.f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float t = acc[c][e] * unit(c);
+                        v[e] += MA == 16 || (g >> 1) == c % 2 ? t : 0.f;
+                    }
+                }
+            }
+            const int col = 16 * q + j;
+            if constexpr (MA == 16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) red[buf][wv][4 * g + e][col] = v[e];
+            } else if constexpr (MA == 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float x = v[e], y = v[e];
+                    swap32(x, y);
+                    if (g < 2) red[buf][wv][4 * g + e][col] = x + y;
+                }
+            } else {
+                const float t = sum_over_rows(v[0]);
+                if (g == 0) red[buf][wv][0][col] = t;
+            }
+        }
+        __syncthreads();
+        for (int o = threadIdx.x; o < 16 * MA; o += 64 * NW) {
+            const int m = o / 16, c = o % 16;
+            float sd[NM] = {};
+#pragma unroll
+            for (int q = 0; q < NW; ++q)
+#pragma unroll
+                for (int p = 0; p < NM; ++p) sd[p] += red[buf][q][m][16 * p + c];
+            float y = (sd[0] * 16777216.0f - sxt[m]) * scale[0];
+            if constexpr (PAIR) y = y / (1.f + __expf(-y)) * ((sd[NM - 1] * 16777216.0f - sxt[m]) * scale[NM - 1]);
+            done[held][m][c] = __builtin_bit_cast(uint16_t, (_Float16)y);
+        }
+    };
+    // Results wait in LDS and are written kHeld blocks at a time: a store between the loads would be waited for with
+    // them, by every wave at the next barrier.
+    int first = b, held = 0;                     // results of blocks first, + G, ... (held of them) wait
+    auto flush = [&]() __attribute__((always_inline)) {
+        __syncthreads();
+        for (int o = (int)threadIdx.x; o < held * MA * 16; o += 64 * NW) {
+            const int i = o / (MA * 16), m = o / 16 % MA, n = 16 * (first + i * G) + o % 16;
+            if (n < N && source[m] >= 0) ex.Y[(int64_t)(et.r0 + m) * N + n] = done[i][m][o % 16];
+        }
+        __syncthreads();
+        first += held * G;
+        held = 0;
+    };
+    int buf = 0;
+    for (; b < nblk; b += D * G) {
+#pragma unroll
+        for (int i = 0; i < D; ++i) {
+            if (b + i * G < nblk) {
+                if (D > 1 && b + (i + D - 1) * G < nblk) load_w(b + (i + D - 1) * G, w[(i + D - 1) % D]);
+                run(w[i], buf, held++);
+                if (D == 1 && b + G < nblk) load_w(b + G, w[0]);
+                buf ^= 1;
+            }
+        }
+        if (held > kHeld - D) flush();
+    }
+    flush();
+}
+
 // ---------------------------------------------------------------- combination
 
 // Thread p of the grid's stride loop owns VEC values (one 16-byte piece, or one value where rows are not whole
@@ -675,11 +971,59 @@ void experts_go(const Experts &ex, hipStream_t s)
     }
 }
 
+template <int FMT, int MA, int CST, bool PAIR>
+bool loop_go(const Experts &ex, hipStream_t s)
+{
+    constexpr int D = loop_depth(FMT, MA, CST, PAIR), EU = loop_waves(FMT, MA, CST, PAIR);
+    constexpr auto kernel = k_experts_loop<FMT, MA, CST, PAIR, D, EU>;
+    const int C = (int)(row_bytes(ex.K, FMT) / 16);
+    const int64_t slots = expert_slots(ex.R, ex.E, MA), most = slots * ((ex.N + 15) / 16);
+    const int64_t resident = (int64_t)cu_count() * resident_per_cu<kernel>(512), least = resident > slots ? resident : slots;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(most < least ? most : least)), dim3(512), 0, s, ex, C);
+    return true;
+}
+
+// The fewest steps per wave that cover the row; false where the A operands would not stay in registers.
+template <int FMT, int MA, bool PAIR>
+bool loop_cst(const Experts &ex, hipStream_t s)
+{
+    constexpr int kLong = FMT == TRI_FMT_2BIT ? 6 : 5;
+    const int cst = (int)((row_bytes(ex.K, FMT) / 16 + 31) / 32);
+    if (cst <= 1) return loop_go<FMT, MA, 1, PAIR>(ex, s);
+    if (cst <= 2) return loop_go<FMT, MA, 2, PAIR>(ex, s);
+    if constexpr (MA <= 8) {
+        if (cst <= 4) return loop_go<FMT, MA, 4, PAIR>(ex, s);
+        if (cst <= kLong) return loop_go<FMT, MA, kLong, PAIR>(ex, s);
+    }
+    return false;
+}
+
+// The tile height by the mean number of places per expert, R / E; false: the tiled GEMM.  Measured on eight experts, two
+// per token (us; MA = 1 / 8 / 16 / GEMM, 2-bit):
+//   gate and up, 4096 -> 11008   R/E = 1/4: 12.3 / 16.5 / 16.6 / 29.7,  1: 38.0 / 32.9 / 34.2 / 63.7,
+//                                4: - / 45.5 / 43.4 / 69.8,  16: - / 96.4 / 60.1 / 74.3,  32: - / 156 / 87 / 118
+//   down, 11008 -> 4096          R/E = 1: 19.4 / 23.0 / - / 45.3,  4: - / 29.5 / - / 53.8,  16: - / 58.7 / - / 66.3,
+//                                24: - / 77.0 / - / 67.5
+// (MA = 4 won nowhere by more than 3%.)
+template <int FMT, bool PAIR>
+bool loop_ma(const Experts &ex, hipStream_t s)
+{
+    const int one = FMT == TRI_FMT_2BIT && !PAIR ? ex.E : ex.E / 2;
+    if (ex.R <= one) return loop_cst<FMT, 1, PAIR>(ex, s);
+    if (ex.R / 2 > ex.E && ex.R / (FMT == TRI_FMT_2BIT ? 32 : 16) <= ex.E && loop_cst<FMT, 16, PAIR>(ex, s)) return true;
+    if (ex.R / 16 <= ex.E) return loop_cst<FMT, 8, PAIR>(ex, s);
+    return false;
+}
+
 template <int FMT, bool PAIR, bool VEC>
 int experts_ma(const Experts &ex, hipStream_t s)
 {
-    if (ex.R <= ex.E / 2) experts_go<FMT, 1, 1, PAIR, VEC>(ex, s);
-    else if (ex.R / 2 <= ex.E) experts_go<FMT, 4, 1, PAIR, VEC>(ex, s);
+    if constexpr (VEC) {
+        if (loop_ma<FMT, PAIR>(ex, s)) return launched();
+        if (ex.R / 2 > ex.E && experts_gemm_fits(ex, FMT)) return launch_experts_gemm(ex, FMT, s);
+    }
+    // rows too long for the loop, or no whole 16-byte pieces
+    if (ex.R <= ex.E) experts_go<FMT, 4, 1, PAIR, VEC>(ex, s);
     else experts_go<FMT, 16, 1, PAIR, VEC>(ex, s);
     return launched();
 }
@@ -696,7 +1040,6 @@ int experts_fmt(const Experts &ex, hipStream_t s)
 
 int launch_experts(const Experts &ex, int fmt, hipStream_t s)
 {
-    if (ex.R / 2 >= ex.E && experts_gemm_fits(ex, fmt)) return launch_experts_gemm(ex, fmt, s);
     return fmt == TRI_FMT_2BIT ? experts_fmt<TRI_FMT_2BIT>(ex, s) : experts_fmt<TRI_FMT_1P6BIT>(ex, s);
 }
 

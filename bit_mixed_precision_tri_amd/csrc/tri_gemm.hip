@@ -171,7 +171,7 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
     __shared__ int source[EXP ? BM : 1];
     ExpertTile et{0, 0, 0};
     if constexpr (EXP) {
-        et = expert_tile(ex.offsets, ex.E, ex.R, tm, BM);
+        et = expert_tile(ex.offsets, ex.E, ex.R, BM, [&](int) { return tm; });
         if (et.e < 0) return;                    // (the whole workgroup)
         if (tid < BM) {
             int src = -1;
