@@ -10,6 +10,7 @@ entry points.
 """
 import collections
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -355,15 +356,20 @@ def _launch(name, device, stream, *args):
         handle = torch._C._cuda_getCurrentRawStream(device)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    rc = getattr(lib(), name)(*args, handle)
+    rc = getattr(_lib or lib(), name)(*args, handle)
     if rc != TRI_OK:
         raise TriError(rc, name)
+
+
+def _plain(t, dtype, device):
+    """Whether tensor `t` is of `dtype`, contiguous and on `device`."""
+    return t.dtype is dtype and t.get_device() == device and t.is_contiguous()
 
 
 def _tensors(device, dtype, **named):
     """Every named tensor (None is left out) is of `dtype`, contiguous and on `device`."""
     for name, t in named.items():
-        if t is not None and not (t.dtype == dtype and t.get_device() == device and t.is_contiguous()):
+        if t is not None and not _plain(t, dtype, device):
             raise ValueError("%s must be a contiguous %s tensor on device %d" % (name, dtype, device))
 
 
@@ -373,6 +379,21 @@ def _keep(t, stream):
     if stream is not None:
         h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         t.record_stream(torch.cuda.ExternalStream(h, device=t.device))
+
+
+@functools.lru_cache(maxsize=4096)
+def _int4_nbytes(N, K, group, zeros):
+    return tri_int4_bytes(N, K, group, zeros)
+
+
+@functools.lru_cache(maxsize=4096)
+def _route_nbytes(T, E, topk):
+    return tri_experts_route_workspace_bytes(T, E, topk)
+
+
+@functools.lru_cache(maxsize=4096)
+def _row_nbytes(K, fmt):
+    return tri_row_bytes(K, fmt)
 
 
 def int4_pack(Q, S, group, Z=None, stream=None):
@@ -427,16 +448,20 @@ def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=No
     """Y = fp16(residual + X @ W.T) for an (M, K) fp16 tensor X and a packed 4-bit matrix of N rows.  `residual` may be
     `out` itself."""
     import torch
-    _need(X.is_cuda and X.dim() == 2 and X.numel() > 0, "X must be an (M, K) tensor on the GPU")
-    (M, K), dev = X.shape, X.get_device()
-    Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=X.device)
-    _tensors(dev, torch.float16, X=X, out=Y, residual=residual)
-    _tensors(dev, torch.uint8, Wp=Wp)
-    _need(Wp.numel() == tri_int4_bytes(N, K, group, zeros),
-          "Wp does not hold tri_int4_bytes(N, K, group, zeros) bytes for X's width")
-    _need(Y.shape == (M, N) and (residual is None or residual.shape == (M, N)), "out and residual must be (M, N)")
-    _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0,
-            None if residual is None else residual.data_ptr(), Y.data_ptr())
+    half, dev, shape = torch.float16, X.get_device(), X.shape
+    _need(dev >= 0 and len(shape) == 2 and _plain(X, half, dev), "X must be a contiguous (M, K) float16 tensor on the GPU")
+    M, K = shape
+    _need(_plain(Wp, torch.uint8, dev) and Wp.numel() == _int4_nbytes(N, K, group, bool(zeros)) and M > 0,
+          "Wp must be a uint8 tensor on X's device of tri_int4_bytes(N, K, group, zeros) bytes for X's width")
+    Y = out if out is not None else torch.empty((M, N), dtype=half, device=X.device)
+    _need(Y.shape == (M, N) and _plain(Y, half, dev), "out must be a contiguous (M, N) float16 tensor on X's device")
+    res = None
+    if residual is not None:
+        _need(residual.shape == (M, N) and _plain(residual, half, dev),
+              "residual must be a contiguous (M, N) float16 tensor on X's device")
+        res = residual.data_ptr()
+    _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0, res,
+            Y.data_ptr())
     return Y
 
 
@@ -449,29 +474,32 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     expert) pairs by expert, as a Routing (the tensors of `out`, if it is given).  `workspace`: a uint8 tensor of at
     least tri_experts_route_workspace_bytes(T, E, topk) bytes; allocated where it is None."""
     import torch
-    _need(logits.is_cuda and logits.dim() == 2 and logits.is_contiguous() and
-          logits.dtype in (torch.float16, torch.float32), "logits must be a contiguous (T, E) float16 or float32 tensor on the GPU")
-    (T, E), dev = logits.shape, logits.get_device()
-    need = tri_experts_route_workspace_bytes(T, E, topk)
+    dtype, dev, shape = logits.dtype, logits.get_device(), logits.shape
+    _need(dev >= 0 and len(shape) == 2 and (dtype is torch.float16 or dtype is torch.float32) and logits.is_contiguous(),
+          "logits must be a contiguous (T, E) float16 or float32 tensor on the GPU")
+    T, E = shape
+    need = _route_nbytes(T, E, topk)
     _need(need >= 0, "1 <= E <= %d, 1 <= topk <= min(E, %d) and T * topk < 2^31 are taken" % (TRI_MAX_EXPERTS, TRI_MAX_TOPK))
+    i32 = torch.int32
     if out is None:
-        i32 = dict(dtype=torch.int32, device=logits.device)
-        out = Routing(torch.empty((T, topk), **i32), torch.empty((T, topk), dtype=torch.float32, device=logits.device),
-                      torch.empty(E + 1, **i32), torch.empty(T * topk, **i32), torch.empty((T, topk), **i32))
-    else:
-        _tensors(dev, torch.int32, ids=out.ids, offsets=out.offsets, rows=out.rows, pos=out.pos)
-        _tensors(dev, torch.float32, weights=out.weights)
-        _need(out.ids.shape == out.weights.shape == out.pos.shape == (T, topk) and out.offsets.shape == (E + 1,) and
-              out.rows.shape == (T * topk,), "out: ids, weights, pos (T, topk), offsets (E + 1), rows (T * topk)")
+        kw = dict(dtype=i32, device=logits.device)
+        out = Routing(torch.empty((T, topk), **kw), torch.empty((T, topk), dtype=torch.float32, device=logits.device),
+                      torch.empty(E + 1, **kw), torch.empty(T * topk, **kw), torch.empty((T, topk), **kw))
+    ids, weights, offsets, rows, pos = out
+    _need(_plain(ids, i32, dev) and _plain(weights, torch.float32, dev) and _plain(offsets, i32, dev) and
+          _plain(rows, i32, dev) and _plain(pos, i32, dev) and ids.shape == weights.shape == pos.shape == (T, topk) and
+          offsets.shape == (E + 1,) and rows.shape == (T * topk,),
+          "out: ids, weights, pos (T, topk), offsets (E + 1), rows (T * topk); int32, the weights float32")
     temporary = workspace is None and need > 0
     if temporary:
         workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    ws, nbytes = None, 0
     if workspace is not None:
-        _tensors(dev, torch.uint8, workspace=workspace)
-    _launch("tri_experts_route", dev, stream, logits.data_ptr(), TRI_F16 if logits.dtype == torch.float16 else TRI_F32, T, E,
-            topk, 1 if renorm else 0, out.ids.data_ptr(), out.weights.data_ptr(), out.offsets.data_ptr(),
-            out.rows.data_ptr(), out.pos.data_ptr(), None if workspace is None else workspace.data_ptr(),
-            0 if workspace is None else workspace.numel())
+        _need(_plain(workspace, torch.uint8, dev), "workspace must be a contiguous uint8 tensor on the logits' device")
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    _launch("tri_experts_route", dev, stream, logits.data_ptr(), TRI_F16 if dtype is torch.float16 else TRI_F32, T, E, topk,
+            1 if renorm else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), ws,
+            nbytes)
     if temporary:
         _keep(workspace, stream)
     return out
@@ -479,26 +507,26 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
 
 def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
     import torch
-    _need(X.is_cuda and X.dim() == 2 and X.numel() > 0 and X.shape[1] == K, "X must be a (T, K) tensor on the GPU")
-    T, dev = X.shape[0], X.get_device()
-    Wp = mats[0][0]
-    _need(Wp.dim() == 3, "packed weights must be (E, N, row_bytes)")
-    E, N = Wp.shape[0], Wp.shape[1]
-    R = T if rows is None else rows.shape[0]
-    Y = out if out is not None else torch.empty((R, N), dtype=torch.float16, device=X.device)
-    _tensors(dev, torch.float16, X=X, out=Y)
-    _tensors(dev, torch.int32, offsets=offsets, rows=rows)
-    _need(offsets.shape == (E + 1,) and (rows is None or rows.dim() == 1), "offsets must be (E + 1), rows one-dimensional")
-    _need(Y.dim() == 2 and Y.shape[0] >= R and Y.shape[1] == N, "out must be (R, N)")
+    half, i32, dev, shape = torch.float16, torch.int32, X.get_device(), X.shape
+    _need(dev >= 0 and len(shape) == 2 and shape[1] == K and shape[0] > 0 and _plain(X, half, dev),
+          "X must be a contiguous (T, K) float16 tensor on the GPU")
+    T, wshape = shape[0], mats[0][0].shape
+    _need(len(wshape) == 3 and wshape[2] == _row_nbytes(K, fmt), "weights must be (E, N, tri_row_bytes(K, fmt))")
+    E, N = wshape[0], wshape[1]
+    _need(_plain(offsets, i32, dev) and offsets.shape == (E + 1,), "offsets must be a contiguous (E + 1) int32 tensor on X's device")
+    R, rp = T, None
+    if rows is not None:
+        _need(_plain(rows, i32, dev) and rows.dim() == 1, "rows must be a contiguous one-dimensional int32 tensor on X's device")
+        R, rp = rows.shape[0], rows.data_ptr()
+    Y = out if out is not None else torch.empty((R, N), dtype=half, device=X.device)
+    _need(_plain(Y, half, dev) and Y.dim() == 2 and Y.shape[0] >= R and Y.shape[1] == N,
+          "out must be a contiguous (R, N) float16 tensor on X's device")
     args = []
     for W, scale in mats:
-        _tensors(dev, torch.uint8, weights=W)
-        _tensors(dev, torch.float32, scale=scale)
-        _need(W.shape == (E, N, tri_row_bytes(K, fmt)) and scale.numel() == E,
-              "weights must be (E, N, tri_row_bytes(K, fmt)), scales (E)")
+        _need(_plain(W, torch.uint8, dev) and W.shape == wshape and _plain(scale, torch.float32, dev) and scale.numel() == E,
+              "weights must be contiguous (E, N, tri_row_bytes(K, fmt)) uint8 tensors, scales (E) float32, on X's device")
         args += [W.data_ptr(), scale.data_ptr()]
-    _launch(name, dev, stream, X.data_ptr(), T, offsets.data_ptr(), None if rows is None else rows.data_ptr(), R, *args, E,
-            N, K, fmt, Y.data_ptr())
+    _launch(name, dev, stream, X.data_ptr(), T, offsets.data_ptr(), rp, R, *args, E, N, K, fmt, Y.data_ptr())
     return Y
 
 
@@ -518,16 +546,21 @@ def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
     """Y[t] = fp16(residual[t] + sum_j weights[t, j] * Z[pos[t, j]]); pairs with pos outside Z are left out.  `residual`
     may be `out` itself."""
     import torch
-    _need(Z.is_cuda and Z.dim() == 2 and Z.numel() > 0 and pos.dim() == 2, "Z must be an (R, N) tensor on the GPU, pos (T, topk)")
-    (R, N), (T, topk), dev = Z.shape, pos.shape, Z.get_device()
-    Y = out if out is not None else torch.empty((T, N), dtype=torch.float16, device=Z.device)
-    _tensors(dev, torch.float16, Z=Z, residual=residual, out=Y)
-    _tensors(dev, torch.int32, pos=pos)
-    _tensors(dev, torch.float32, weights=weights)
-    _need(weights.shape == (T, topk) and Y.shape == (T, N) and (residual is None or residual.shape == (T, N)),
-          "weights must be (T, topk), out and residual (T, N)")
-    _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(),
-            None if residual is None else residual.data_ptr(), T, topk, N, Y.data_ptr())
+    half, dev, shape = torch.float16, Z.get_device(), Z.shape
+    _need(dev >= 0 and len(shape) == 2 and _plain(Z, half, dev) and Z.numel() > 0,
+          "Z must be a contiguous (R, N) float16 tensor on the GPU")
+    _need(_plain(pos, torch.int32, dev) and pos.dim() == 2 and _plain(weights, torch.float32, dev) and
+          weights.shape == pos.shape, "pos must be a contiguous (T, topk) int32 tensor on Z's device, weights float32 like it")
+    (R, N), (T, topk) = shape, pos.shape
+    Y = out if out is not None else torch.empty((T, N), dtype=half, device=Z.device)
+    _need(_plain(Y, half, dev) and Y.shape == (T, N), "out must be a contiguous (T, N) float16 tensor on Z's device")
+    res = None
+    if residual is not None:
+        _need(_plain(residual, half, dev) and residual.shape == (T, N),
+              "residual must be a contiguous (T, N) float16 tensor on Z's device")
+        res = residual.data_ptr()
+    _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), res, T, topk, N,
+            Y.data_ptr())
     return Y
 
 

@@ -3,6 +3,8 @@
 //   route    top-k of every token's logits and the stable order of the (token, expert) pairs by expert
 //   product  Y[r] = scale[e] X[rows[r]] W_e^T for the places r of expert e, one matrix or a gated pair
 //   combine  Y[t] = residual[t] + sum_j weights[t][j] Z[pos[t][j]]
+#include <type_traits>
+
 #include "tri_experts.h"
 
 namespace tri {
@@ -18,25 +20,18 @@ constexpr int kRouteWaves = kRouteThreads / 64;
 constexpr int kRouteTokens = 32;                 // tokens per workgroup where there are several (32 * 16 pairs at most)
 constexpr int kMaxCols = TRI_MAX_EXPERTS + 1;    // the last bucket holds the pairs that take no expert
 
-__device__ __forceinline__ float wave_max(float v)
+// Over the 16 lanes of a row, in every one of them.
+template <typename F>
+__device__ __forceinline__ float row_all(float v, F f)
 {
-    float a = v, b = v;
-    swap32(a, b);
-    v = fmaxf(a, b);
-    a = b = v;
-    swap16(a, b);
-    v = fmaxf(a, b);
-    v = fmaxf(v, dpp<0x140>(v));
-    v = fmaxf(v, dpp<0x141>(v));
-    v = fmaxf(v, dpp<0x4E>(v));
-    return fmaxf(v, dpp<0xB1>(v));
+    v = f(v, dpp<0x140>(v));                     // row_mirror: lane ^ 15
+    v = f(v, dpp<0x141>(v));                     // row_half_mirror: lane ^ 7
+    v = f(v, dpp<0x4E>(v));                      // lane ^ 2
+    return f(v, dpp<0xB1>(v));                   // lane ^ 1
 }
-
-__device__ __forceinline__ float wave_sum(float v)
-{
-    float a[1] = {v};
-    return wave_reduce_rows<1>(a, 0);
-}
+__device__ __forceinline__ float row_max(float v) { return row_all(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float row_min(float v) { return row_all(v, [](float a, float b) { return fminf(a, b); }); }
+__device__ __forceinline__ float row_sum(float v) { return row_all(v, [](float a, float b) { return a + b; }); }
 
 // Exclusive prefix sums of total[0 .. cols-1] into first[] (first wave; cols <= 64 * 5).
 __device__ __forceinline__ void scan_cols(const int *total, int *first, int cols, int lane)
@@ -61,11 +56,12 @@ __device__ __forceinline__ void scan_cols(const int *total, int *first, int cols
     }
 }
 
-// One workgroup per TB tokens.  A wave takes one token at a time: lane l holds logits EP l .. EP l + EP-1, so
-// the lowest lane among equals holds the lowest expert.  Then thread i ranks pair i of the workgroup among the
-// pairs before it with the same expert: lanes that agree in all nine bits of the bucket number (ballots), and
-// counts of the waves before.  With one workgroup (hist null) that finishes the order; otherwise the counts go
-// to hist[block][bucket], the ranks to pos, and k_route_place finishes.
+// One workgroup per TB tokens.  A row of 16 lanes takes a token, four a wave: lane l holds logits EP l .. EP l + EP-1.
+// Each round takes the row's largest value and, among the lanes that hold it, the lowest expert (as an exact small float:
+// the row reductions are those of floats).  Then thread i ranks pair i of the workgroup among the pairs before it with
+// the same expert: lanes that agree in all nine bits of the bucket number (ballots), and counts of the waves before.  With
+// one workgroup (hist null) that finishes the order; otherwise the counts go to hist[block][bucket], the ranks to pos, and
+// k_route_place finishes.
 template <bool HALF, int EP>
 __global__ __launch_bounds__(kRouteThreads) void k_route(const void *__restrict__ logits, int T, int E, int topk,
                                                          int renorm, int TB, int32_t *__restrict__ ids,
@@ -76,16 +72,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const void *__restrict_
     __shared__ int bucket[kRouteThreads];
     __shared__ int count[kRouteWaves][kMaxCols];
     __shared__ int total[kMaxCols], first[kMaxCols];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, l = lane & 15;
     const int t0 = blockIdx.x * TB, nt = min(TB, T - t0), cols = E + 1;
-    for (int i = threadIdx.x; i < kRouteWaves * kMaxCols; i += kRouteThreads) (&count[0][0])[i] = 0;
     const float ninf = -__builtin_inff();
-    for (int tt = wv; tt < nt; tt += kRouteWaves) {
-        const int64_t t = t0 + tt;
+    for (int i = threadIdx.x; i < kRouteWaves * kMaxCols; i += kRouteThreads) (&count[0][0])[i] = 0;
+    for (int tw = 4 * wv; tw < nt; tw += 4 * kRouteWaves) {   // (wave-uniform)
+        const int tt = tw + (lane >> 4);
+        const int64_t t = t0 + min(tt, nt - 1);  // (rows past the end repeat the last token and write nothing)
         float v[EP];
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
-            const int e = EP * lane + i;
+            const int e = EP * l + i;
             v[i] = ninf;
             if (e < E) {
                 const float x = HALF ? h2f(static_cast<const uint16_t *>(logits)[t * E + e])
@@ -93,17 +90,17 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const void *__restrict_
                 v[i] = x == x ? x : ninf;
             }
         }
-        float top = v[0];
+        float mx = v[0];
 #pragma unroll
-        for (int i = 1; i < EP; ++i) top = fmaxf(top, v[i]);
-        const float mx = wave_max(top);
+        for (int i = 1; i < EP; ++i) mx = fmaxf(mx, v[i]);
+        mx = row_max(mx);
         auto mass = [&](float x) { return x == mx ? 1.f : expf(x - mx); };   // (x, mx > -inf; inf against inf: 1)
         float whole = 0.f;
         if (!renorm) {
 #pragma unroll
             for (int i = 0; i < EP; ++i)
                 if (v[i] > ninf) whole += mass(v[i]);
-            whole = wave_sum(whole);
+            whole = row_sum(whole);
         }
         int my_e = -1;
         float my_v = ninf;
@@ -111,28 +108,24 @@ __global__ __launch_bounds__(kRouteThreads) void k_route(const void *__restrict_
             float best = v[0];
 #pragma unroll
             for (int i = 1; i < EP; ++i) best = fmaxf(best, v[i]);
-            const float w = wave_max(best);
-            if (!(w > ninf)) break;              // (wave-uniform) nothing left to take
-            const int src = __ffsll((unsigned long long)__ballot(best == w)) - 1;
-            int li = 0;
+            const float w = row_max(best);
+            float at = 1024.f;                   // this lane's lowest expert of that value
 #pragma unroll
-            for (int i = EP - 1; i >= 0; --i)
-                if (v[i] == w) li = i;
-            const int e = __builtin_amdgcn_readlane(EP * lane + li, src);
+            for (int i = EP - 1; i >= 0; --i) at = v[i] == w ? (float)(EP * l + i) : at;
+            const int e = (int)row_min(at);
 #pragma unroll
-            for (int i = 0; i < EP; ++i)
-                if (EP * lane + i == e) v[i] = ninf;
-            if (lane == j) {
+            for (int i = 0; i < EP; ++i) v[i] = EP * l + i == e ? ninf : v[i];
+            if (l == j && w > ninf) {
                 my_e = e;
                 my_v = w;
             }
         }
         const float m = my_e >= 0 ? mass(my_v) : 0.f;
-        if (renorm) whole = wave_sum(m);
-        if (lane < topk) {
-            ids[t * topk + lane] = my_e;
-            weights[t * topk + lane] = my_e >= 0 ? m / whole : 0.f;
-            bucket[tt * topk + lane] = my_e >= 0 ? my_e : E;
+        if (renorm) whole = row_sum(m);
+        if (l < topk && tt < nt) {
+            ids[t * topk + l] = my_e;
+            weights[t * topk + l] = my_e >= 0 ? m / whole : 0.f;
+            bucket[tt * topk + l] = my_e >= 0 ? my_e : E;
         }
     }
     __syncthreads();
@@ -226,6 +219,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(int T, int E, int
         const int c = threadIdx.x % cols, s = threadIdx.x / cols;
         int all = 0, prev = 0;
         if (s < slices) {
+#pragma unroll 8
             for (int b = s; b < nb; b += slices) {
                 const int x = hist[(int64_t)b * cols + c];
                 all += x;
@@ -260,7 +254,7 @@ __global__ __launch_bounds__(kRouteThreads) void k_route_place(int T, int E, int
     }
 }
 
-// One workgroup does all of it while its pairs fit its threads and a wave has few tokens.
+// One workgroup does all of it while its pairs fit its threads and a row of lanes has few tokens.
 bool route_single(int T, int topk) { return (int64_t)T * topk <= kRouteThreads && T <= 4 * kRouteTokens; }
 int route_blocks(int T) { return (T + kRouteTokens - 1) / kRouteTokens; }
 // From here on the counts are scanned by a launch of their own (below, every workgroup adds all of them).
@@ -940,15 +934,16 @@ int launch_route(const void *logits, bool half, int T, int E, int topk, bool ren
         hipLaunchKernelGGL(kernel, dim3(blocks), dim3(kRouteThreads), 0, s, logits, T, E, topk, renorm ? 1 : 0, TB, ids,
                            weights, offsets, rows, pos, hist);
     };
-    if (half) {
-        if (E <= 64) go(k_route<true, 1>);
-        else if (E <= 128) go(k_route<true, 2>);
-        else go(k_route<true, 4>);
-    } else {
-        if (E <= 64) go(k_route<false, 1>);
-        else if (E <= 128) go(k_route<false, 2>);
-        else go(k_route<false, 4>);
-    }
+    auto go_ep = [&](auto h) {
+        constexpr bool H = decltype(h)::value;
+        if (E <= 16) go(k_route<H, 1>);
+        else if (E <= 32) go(k_route<H, 2>);
+        else if (E <= 64) go(k_route<H, 4>);
+        else if (E <= 128) go(k_route<H, 8>);
+        else go(k_route<H, 16>);
+    };
+    if (half) go_ep(std::true_type{});
+    else go_ep(std::false_type{});
     if (!single) {
         const bool scan = blocks > kRouteScanBlocks;
         if (scan) hipLaunchKernelGGL(k_route_scan, dim3(E + 1), dim3(kRouteThreads), 0, s, blocks, E + 1, hist);
