@@ -409,6 +409,252 @@ __global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict_
     }
 }
 
+// ---------------------------------------------------------------- product, 17 rows and more
+
+typedef __attribute__((address_space(3))) char *lds_ptr_t;
+
+// s_waitcnt vmcnt(N): at most N vector memory loads of this wave still outstanding (they retire in issue order)
+template <int N>
+__device__ __forceinline__ void wait_vm()
+{
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (((N >> 4) & 3) << 14));
+}
+
+// A barrier that waits for nothing itself: what it has to order (loads to LDS of this wave, and its LDS reads, whose values
+// every product before it has used) is waited for explicitly.  __syncthreads() would wait for every load to LDS that is
+// still in flight.
+__device__ __forceinline__ void group_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);          // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// A workgroup computes 16 MT rows (MT = 2 or 4) x 128 outputs: four waves of two 16-output blocks side by side, and two
+// such groups, each over every other step of the row, whose sums are added in LDS at the end.
+//
+// With more than 16 rows the activations, not the weights, are what is read most, so the four waves of a group share them:
+// each step's 16 MT x 128 values are written into one of four LDS buffers by loads to LDS, up to three steps ahead, and a
+// decoded B operand serves MT products.  In a buffer, piece q (8 values) of row r lies at position q ^ (r % 16) of its row,
+// so that the 16 rows which one read touches at one piece fall in 16 distinct bank groups; a load instruction fills four
+// rows, 256 consecutive bytes each.  Weights and scales go to registers, as far ahead.  The order of issue, a step's weights
+// and then its activations, is what the waits count on.
+//
+// Measured at 64 rows, 8192 -> 28672, group 64: 53 us, of which the loads alone take 38 (the weights alone 28) and the
+// products and decoding alone 36: the two overlap by half.  More outputs per wave, one group or four, two or three buffers
+// were no faster (54 - 99 us).
+constexpr int kMmWaves = 8;                      // waves of a workgroup: two groups of four
+
+template <int MT, int GPS, bool ZP, bool TAIL>
+__global__ __launch_bounds__(64 * kMmWaves) void k_int4_mm(const uint16_t *__restrict__ X, const uint8_t *__restrict__ codes,
+                                                      const uint16_t *__restrict__ scales,
+                                                      const uint8_t *__restrict__ zeros, int M, int N, int K, int KS,
+                                                      const uint16_t *R, uint16_t *Y)
+{
+    constexpr int NB = 2, NW = 4, KG = 2, D = 4; // blocks per wave, waves per group, groups, buffers
+    constexpr int NI = 4 * MT / NW;              // load instructions per wave and step: 16 MT rows, four each
+    constexpr int NWL = NB * (ZP ? 3 : 2);       // loads of weights, scales and zero points per wave and step
+    constexpr int kCols = NW * 16 * NB;           // outputs per workgroup
+    constexpr int kBuf = MT * 16 * 16;           // 16-byte pieces of a group's step
+    // (separate arrays, not one indexed by a variable: loads to LDS are waited for before LDS reads that the compiler
+    // cannot prove disjoint from them, and it proves it for distinct arrays)
+    __shared__ u32x4 buf0[KG * kBuf], buf1[KG * kBuf], buf2[KG * kBuf], buf3[KG * kBuf];
+    auto buf_of = [&](int i) -> u32x4 * { return i == 0 ? buf0 : i == 1 ? buf1 : i == 2 ? buf2 : buf3; };
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wn = wave % NW, kg = wave / NW;
+    const int g = lane >> 4, j = lane & 15;
+    // consecutive workgroups of an XCD (every eighth) take the row tiles of the same outputs
+    const int tiles_m = (M + 16 * MT - 1) / (16 * MT);
+    int wg = (int)blockIdx.x;
+    if ((gridDim.x & 7) == 0) wg = (wg & 7) * ((int)gridDim.x >> 3) + (wg >> 3);
+    const int m0 = wg % tiles_m * 16 * MT;
+    const int64_t n0 = (int64_t)(wg / tiles_m) * kCols;
+    const int64_t b0 = n0 / 16 + NB * wn;        // this wave's first block
+    const int64_t blocks = ((int64_t)N + 15) / 16;
+    const int nb = (int)(blocks - b0 < NB ? (blocks - b0 > 0 ? blocks - b0 : 0) : NB);
+    const int64_t bs = b0 < blocks ? b0 : 0;     // (waves past the last block read nothing: empty resources)
+    const int mm = min(16 * MT, M - m0);
+
+    // Resources begin at the step that is read, so that a lane's offsets never change: a step costs scalar work only.
+    const uint8_t *const cbase = codes + bs * KS * 1024;
+    const uint16_t *const sbase = scales + bs * KS * (16 * GPS);
+    const uint8_t *const zbase = ZP ? zeros + bs * KS * (16 * GPS) : nullptr;
+    const uint16_t *const xbase = X + (int64_t)m0 * K;
+    const uint32_t xbytes = __builtin_amdgcn_readfirstlane((uint32_t)mm * (uint32_t)K * 2u);
+
+    // load instruction i of this wave: rows 4 (wn NI + i) + lane / 16, position lane % 16
+    uint32_t xoff[NI];
+    int klim[NI];                                // the piece's values exist in steps that begin below
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int row = 4 * (wn * NI + i) + g, q = j ^ (row & 15);
+        xoff[i] = row < mm ? ((uint32_t)row * (uint32_t)K + 8u * (uint32_t)q) * 2u : kOob;
+        klim[i] = K - 8 * q;
+    }
+    auto load_a = [&](int s, int buf) __attribute__((always_inline)) {
+        const lds_ptr_t dst = (lds_ptr_t)(buf_of(buf) + kg * kBuf + wn * NI * 64);
+        const bool in = s < KS;                  // (past the row's end: an empty resource)
+        const __amdgpu_buffer_rsrc_t xr = rsrc(xbase + 128 * (int64_t)(in ? s : 0), in ? xbytes - 256u * (uint32_t)s : 0u);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)             // (TAIL: pieces past K read zeros)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                xr, dst + 1024 * i, 16, (int)(!TAIL || 128 * s < klim[i] ? xoff[i] : kOob), 0, 0, 0);
+    };
+    struct Step {
+        u32x4 w[NB];
+        uint32_t s[NB][GPS == 4 ? 2 : 1];
+        uint32_t z[NB];
+    };
+    auto load_w = [&](int s, Step &t) __attribute__((always_inline)) {
+        const int si = s < KS ? s : 0;
+        const uint32_t left = s < KS && nb > 0 ? (uint32_t)(nb * KS - s) : 0u;   // tiles from this step on (none past the end)
+        const __amdgpu_buffer_rsrc_t wr = rsrc(cbase + 1024 * (int64_t)si, left * 1024u);
+        const __amdgpu_buffer_rsrc_t sr = rsrc(sbase + 16 * GPS * (int64_t)si, left * (32u * GPS));
+        const __amdgpu_buffer_rsrc_t zr = rsrc(ZP ? zbase + 16 * GPS * (int64_t)si : nullptr, ZP ? left * (16u * GPS) : 0u);
+#pragma unroll
+        for (int r = 0; r < NB; ++r) {
+            const uint32_t wo = (uint32_t)(r * KS) * 1024u + 16u * (uint32_t)lane, so = ((uint32_t)(r * KS) * 16u + (uint32_t)j) * GPS;
+            t.w[r] = __builtin_amdgcn_raw_buffer_load_b128(wr, (int)wo, 0, 0);
+            if constexpr (GPS == 4) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b64(sr, (int)(so * 2u), 0, 0);
+                t.s[r][0] = v[0];
+                t.s[r][1] = v[1];
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b32(zr, (int)so, 0, 0);
+            } else if constexpr (GPS == 2) {
+                t.s[r][0] = __builtin_amdgcn_raw_buffer_load_b32(sr, (int)(so * 2u), 0, 0);
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b16(zr, (int)so, 0, 0);
+            } else {
+                t.s[r][0] = __builtin_amdgcn_raw_buffer_load_b16(sr, (int)(so * 2u), 0, 0);
+                if constexpr (ZP) t.z[r] = __builtin_amdgcn_raw_buffer_load_b8(zr, (int)so, 0, 0);
+            }
+        }
+    };
+    uint32_t b10, b6;
+    asm volatile("v_mov_b32 %0, 0x64006400" : "=v"(b10));
+    asm volatile("v_mov_b32 %0, 0x54005400" : "=v"(b6));
+    const float4_t zero4 = {0.f, 0.f, 0.f, 0.f};
+    float4_t tot[MT][NB];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < NB; ++r) tot[m][r] = zero4;
+    auto run = [&](const Step &t, int buf) __attribute__((always_inline)) {
+        const u32x4 *const as = buf_of(buf) + kg * kBuf;
+        float4_t d[MT][NB];
+        u32x4 a[2][MT], b[2][NB];                // operands of two pieces in turn
+        auto operands = [&](int p) __attribute__((always_inline)) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) a[p % 2][m] = as[(16 * m + j) * 16 + ((4 * p + g) ^ j)];
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                uint32_t lo = 0xE408E408u, hi = 0xD480D480u;
+                if constexpr (ZP) {
+                    const uint32_t z = (t.z[r] >> (8 * (p * GPS / 4))) & 15u, zz = z | z << 16;
+                    lo = 0xE400E400u + zz;
+                    hi = 0xD400D400u + (zz << 4);
+                }
+                b[p % 2][r] = decode(t.w[r][p], b10, b6, lo, hi);
+            }
+        };
+        operands(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            if (p < 3) operands(p + 1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < NB; ++r) d[m][r] = mfma(a[p % 2][m], b[p % 2][r], p % (4 / GPS) ? d[m][r] : zero4);
+            // the next piece's reads and decoding between the products
+#pragma unroll
+            for (int i = 0; i < MT * NB; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // 1 MFMA
+                if (i % NB == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // 1 LDS read
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // 4 VALU
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if ((p + 1) % (4 / GPS) == 0) {
+                constexpr int kPer = GPS == 4 ? 2 : 1;
+#pragma unroll
+                for (int r = 0; r < NB; ++r) {
+                    const int i = p * GPS / 4;
+                    const float sc = h2f((uint16_t)(t.s[r][kPer == 2 ? i / 2 : 0] >> (GPS == 1 ? 0 : 16 * (i % 2))));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tot[m][r][e] = fmaf(d[m][r][e], sc, tot[m][r][e]);
+                }
+            }
+        }
+    };
+
+    // step i of this group is step kg + KG i of the row; steps past the end read zeros
+    const int turns = ((KS + KG - 1) / KG + D - 1) / D * D;
+    Step t[D];
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        load_w(kg + KG * i, t[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        load_a(kg + KG * i, i);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    for (int i = 0; i < turns; i += D) {
+#pragma unroll
+        for (int h = 0; h < D; ++h) {
+            // this wave's share of the step's activations is in (younger: the D - 2 steps after it); behind the barrier
+            // everybody's is, and everybody is done with the step before, whose buffer and registers are free
+            wait_vm<(D - 2) * (NWL + NI)>();
+            group_barrier();
+            const int s = kg + KG * (i + h + D - 1), f = (h + D - 1) % D;
+            __builtin_amdgcn_sched_barrier(0);
+            load_w(s, t[f]);
+            __builtin_amdgcn_sched_barrier(0);
+            load_a(s, f);
+            __builtin_amdgcn_sched_barrier(0);
+            run(t[h], h);
+        }
+    }
+    wait_vm<0>();                                // (the last loads to LDS, past the end, are in)
+    __syncthreads();
+
+    // the second group leaves its sums in a buffer, lane for lane, and the first adds them
+    static_assert(KG == 2 && MT * NB * 64 * NW <= KG * kBuf, "a group's sums in one buffer");
+    const int at = (int)threadIdx.x % (64 * NW);
+    if (kg == 1) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < NB; ++r) buf0[(m * NB + r) * 64 * NW + at] = __builtin_bit_cast(u32x4, tot[m][r]);
+    }
+    __syncthreads();
+    if (kg == 1) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < NB; ++r) tot[m][r] += __builtin_bit_cast(float4_t, buf0[(m * NB + r) * 64 * NW + at]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int row = 16 * m + 4 * g + e;
+            if (row >= mm) continue;
+#pragma unroll
+            for (int r = 0; r < NB; ++r) {
+                const int64_t n = 16 * (b0 + r) + j, o = (int64_t)(m0 + row) * N + n;
+                if (n >= N) continue;
+                float y = tot[m][r][e];
+                if (R) y += h2f(R[o]);
+                Y[o] = __builtin_bit_cast(uint16_t, (_Float16)y);
+            }
+        }
+}
+
 uint16_t *scales_of(uint8_t *Wp, const Int4Map &m) { return reinterpret_cast<uint16_t *>(Wp + m.tiles() * 1024); }
 uint8_t *zeros_of(uint8_t *Wp, const Int4Map &m) { return Wp + m.tiles() * 1024 + m.scales() * 2; }
 
@@ -519,12 +765,48 @@ void mv_rb(const Int4Args &a, int gps, hipStream_t s)
     }
 }
 
+constexpr int kMmMaxK = 1 << 24;                 // 32-bit offsets over 64 activation rows
+
+template <int MT, int GPS, bool ZP>
+void mm_go(const Int4Args &a, hipStream_t s)
+{
+    const int64_t wgs = (int64_t)((a.M + 16 * MT - 1) / (16 * MT)) * (((int64_t)a.N + 127) / 128);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)wgs), dim3(64 * kMmWaves), 0, s, a.X, a.codes, a.scales, a.zeros, a.M, a.N, a.K, a.KS,
+                           a.R, a.Y);
+    };
+    if (a.K % 128) go(k_int4_mm<MT, GPS, ZP, true>);
+    else go(k_int4_mm<MT, GPS, ZP, false>);
+}
+
+template <int MT>
+void mm_fmt(const Int4Args &a, int gps, hipStream_t s)
+{
+    if (a.zeros) {
+        if (gps == 1) mm_go<MT, 1, true>(a, s);
+        else if (gps == 2) mm_go<MT, 2, true>(a, s);
+        else mm_go<MT, 4, true>(a, s);
+    } else {
+        if (gps == 1) mm_go<MT, 1, false>(a, s);
+        else if (gps == 2) mm_go<MT, 2, false>(a, s);
+        else mm_go<MT, 4, false>(a, s);
+    }
+}
+
 void mv_rows(const Int4Args &a, int gps, hipStream_t s)
 {
     if (a.K % 8) {
         if (a.M <= 4) mv_fmt<4, 1, false>(a, gps, s);
         else mv_fmt<16, 1, false>(a, gps, s);
         return;
+    }
+    // The shared-activation kernel from five eighths of a round of its smaller tiles on (32 x 128), with the larger ones (64
+    // rows) where those still make as many.  64 rows: 8192 -> 28672 94 -> 47 us (group 128), 4096 -> 11008 23.4 -> 15.2 us;
+    // with 64 tiles (11008 -> 4096) it would lose, 17.6 against 31 us.
+    if (a.M > 16 && a.K < kMmMaxK) {
+        const int64_t cols = ((int64_t)a.N + 127) / 128, enough = 5 * (int64_t)cu_count() / 8;
+        if ((a.M + 63) / 64 * cols >= enough && a.M > 32) return mm_fmt<4>(a, gps, s);
+        if ((a.M + 31) / 32 * cols >= enough) return mm_fmt<2>(a, gps, s);
     }
     // up to four rows one block per workgroup: the activations are few (more blocks lost 10 - 90% at 256 and 688 blocks,
     // and at most 5% was won at 1792)

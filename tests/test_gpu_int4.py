@@ -144,10 +144,28 @@ def test_product(M, N, K):
             check(host(Y), X, dense(Q, S, Z, group), what="M=%d N=%d K=%d group=%d zeros=%d" % (M, N, K, group, zeros))
 
 
-@pytest.mark.parametrize("M", [1, 6, 16, 40])
-def test_residual_and_in_place(M):
+@pytest.mark.parametrize("M,N", [(20, 20500), (33, 20500), (100, 6500), (130, 20490), (600, 2100)])
+@pytest.mark.parametrize("K", [128, 264, 1024, 1160])
+def test_product_of_many_tiles(M, N, K):
+    """Enough row and column tiles for the kernel whose waves share their activations: both of its tile heights, rows and
+    columns that end inside a tile, rows of one step, of whole steps and of a part."""
+    rng = np.random.default_rng([47, M, N, K])
+    X = rng.standard_normal((M, K)).astype(np.float16)
+    R = rng.standard_normal((M, N)).astype(np.float16)
+    Xd, Rd = cuda(X), cuda(R)
+    for group, zeros in ((32, True), (64, False), (128, True), (32, False), (64, True), (128, False)):
+        Q, S, Z = matrix(rng, N, K, group, zeros)
+        Wp = tri.int4_pack(cuda(Q), cuda(S), group, None if Z is None else cuda(Z))
+        say("int4 M=%d N=%d K=%d group=%d zeros=%d" % (M, N, K, group, zeros))
+        res = zeros and group == 64
+        Y = tri.int4_linear(Xd, Wp, N, group, zeros, residual=Rd if res else None)
+        check(host(Y), X, dense(Q, S, Z, group), R if res else None, what="M=%d N=%d K=%d group=%d zeros=%d" % (M, N, K, group, zeros))
+
+
+@pytest.mark.parametrize("M,N", [(1, 300), (6, 300), (16, 300), (40, 300), (70, 20500)])
+def test_residual_and_in_place(M, N):
     rng = np.random.default_rng([44, M])
-    N, K, group = 300, 768, 64
+    K, group = 768, 64
     Q, S, Z = matrix(rng, N, K, group, True)
     X, R = rng.standard_normal((M, K)).astype(np.float16), rng.standard_normal((M, N)).astype(np.float16)
     Wp, Xd, Rd = tri.int4_pack(cuda(Q), cuda(S), group, cuda(Z)), cuda(X), cuda(R)
