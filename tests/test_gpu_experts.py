@@ -203,6 +203,30 @@ def test_products_of_long_rows(K, M, fmt):
 
 
 @pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("K", [72, 520, 4096, 6000, 11008])
+def test_products_of_one_token(K, fmt):
+    """A token's experts, one place each, and rows that share one although few experts have any; every length of row whose
+    operands stay in registers, with outputs for several turns of a workgroup and a part of a block."""
+    rng = np.random.default_rng([64, fmt, K])
+    for sizes in ([0, 1, 0, 0, 0, 1, 0, 0], [0, 0, 0, 3, 0, 0, 0, 0, 0], [2, 0, 0, 9, 0, 0, 0, 0, 0, 1]):
+        R = sum(sizes)
+        check_experts(rng, 1, len(sizes), 100, K, fmt, sizes, True, True, rows=np.zeros(R, dtype=np.int32))
+        check_experts(rng, R, len(sizes), 100, K, fmt, sizes, False, False)
+    check_experts(rng, 1, 4, 13000 if K < 4096 else 2000, K, fmt, [0, 1, 0, 1], True, True, rows=np.zeros(2, dtype=np.int32))
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+def test_more_experts_than_lanes(fmt):
+    """Tiles of more than 64 experts are listed four to a lane."""
+    rng = np.random.default_rng([65, fmt])
+    for E in (65, 200, 256):
+        for each in (0.1, 2, 5, 40):
+            sizes = rng.poisson(each, E)
+            sizes[E - 1] = 3
+            check_experts(rng, int(sizes.sum()), E, 20, 256, fmt, sizes, False, each == 2)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
 def test_products_of_whole_tiles(fmt):
     """Sizes at the edges of the large tiles, in rows and in columns."""
     rng = np.random.default_rng([56, fmt])
