@@ -125,6 +125,23 @@ __device__ __forceinline__ uint32_t byte_pair(const u32x4 v, int q)
 // 16-byte global load.
 __device__ __forceinline__ uint4 ld16(const void *p) { return *reinterpret_cast<const uint4 *>(p); }
 
+// Eight fp16 values from a 2-byte aligned address (global loads need no more alignment), and the first n (< 8) of eight,
+// zeros behind them.
+__device__ __forceinline__ u32x4 ld16_any(const uint16_t *p)
+{
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ u32x4 ld16_part(const uint16_t *p, int n)
+{
+    u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n) v[e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
+    return v;
+}
+
 // NH consecutive fp16 values x[k0 .. k0+NH) of one activation row, as NH/2 registers
 // (x[2q], x[2q+1]); zero beyond K.  `vec` says the row start is 16-byte aligned.
 template <int NH>

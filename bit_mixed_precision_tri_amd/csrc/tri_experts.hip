@@ -360,13 +360,8 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
             xv[i] = u32x4{0u, 0u, 0u, 0u};
             if constexpr (VEC) {
                 if (xrow[i] && k < K) xv[i] = *reinterpret_cast<const u32x4 *>(xrow[i] + k);
-            } else if (xrow[i]) {                // rows that are no whole pieces: value by value
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t lo = k + 2 * e < K ? xrow[i][k + 2 * e] : 0u;
-                    const uint32_t hi = k + 2 * e + 1 < K ? xrow[i][k + 2 * e + 1] : 0u;
-                    xv[i][e] = lo | hi << 16;
-                }
+            } else if (xrow[i] && k < K) {       // rows that are no whole pieces
+                xv[i] = k + 8 <= K ? ld16_any(xrow[i] + k) : ld16_part(xrow[i] + k, K - k);
             }
         }
     };

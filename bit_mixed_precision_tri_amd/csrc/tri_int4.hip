@@ -202,6 +202,7 @@ __global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict_
 
     const int ac = j / MA, aa = j % MA;          // this lane's A row: piece ac of the load, activation row aa
     const uint32_t xrow = aa < mm ? (uint32_t)aa * (uint32_t)K * 2u : kOob;
+    const uint16_t *const xlane = X + ((int64_t)m0 + aa) * K;
     const int tl = U == 4 ? g : U == 2 ? g >> 1 : 0;   // the step of a unit that this lane scales
 
     struct Unit {
@@ -217,15 +218,9 @@ __global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict_
             const int k = 128 * s0 + 32 * (CL * q + ac) + 8 * g;
             if constexpr (VEC) {
                 t.a[q] = __builtin_amdgcn_raw_buffer_load_b128(xr, (int)(k < K ? xrow + 2u * (uint32_t)k : kOob), 0, 0);
-            } else {                             // rows that are no whole pieces: value by value
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t lo = __builtin_amdgcn_raw_buffer_load_b16(
-                        xr, (int)(k + 2 * e < K ? xrow + 2u * (uint32_t)(k + 2 * e) : kOob), 0, 0);
-                    const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b16(
-                        xr, (int)(k + 2 * e + 1 < K ? xrow + 2u * (uint32_t)(k + 2 * e + 1) : kOob), 0, 0);
-                    t.a[q][e] = (lo & 0xFFFFu) | hi << 16;
-                }
+            } else {                             // rows that are no whole pieces
+                t.a[q] = u32x4{0u, 0u, 0u, 0u};
+                if (aa < mm && k < K) t.a[q] = k + 8 <= K ? ld16_any(xlane + k) : ld16_part(xlane + k, K - k);
             }
         }
 #pragma unroll
@@ -754,14 +749,14 @@ int blocks_per_workgroup(int64_t blocks, int64_t slices)
     return best;
 }
 
-template <int MA>
+template <int MA, bool VEC>
 void mv_rb(const Int4Args &a, int gps, hipStream_t s)
 {
     switch (blocks_per_workgroup((a.N + 15) / 16, (a.M + MA - 1) / MA)) {
-    case 1: mv_fmt<MA, 1, true>(a, gps, s); break;
-    case 2: mv_fmt<MA, 2, true>(a, gps, s); break;
-    case 3: mv_fmt<MA, 3, true>(a, gps, s); break;
-    default: mv_fmt<MA, 4, true>(a, gps, s); break;
+    case 1: mv_fmt<MA, 1, VEC>(a, gps, s); break;
+    case 2: mv_fmt<MA, 2, VEC>(a, gps, s); break;
+    case 3: mv_fmt<MA, 3, VEC>(a, gps, s); break;
+    default: mv_fmt<MA, 4, VEC>(a, gps, s); break;
     }
 }
 
@@ -797,7 +792,7 @@ void mv_rows(const Int4Args &a, int gps, hipStream_t s)
 {
     if (a.K % 8) {
         if (a.M <= 4) mv_fmt<4, 1, false>(a, gps, s);
-        else mv_fmt<16, 1, false>(a, gps, s);
+        else mv_rb<16, false>(a, gps, s);
         return;
     }
     // The shared-activation kernel from five eighths of a round of its smaller tiles on (32 x 128), with the larger ones (64
@@ -813,8 +808,8 @@ void mv_rows(const Int4Args &a, int gps, hipStream_t s)
     if (a.M <= 1) mv_fmt<1, 1, true>(a, gps, s);
     else if (a.M <= 2) mv_fmt<2, 1, true>(a, gps, s);
     else if (a.M <= 4) mv_fmt<4, 1, true>(a, gps, s);
-    else if (a.M <= 8) mv_rb<8>(a, gps, s);
-    else mv_rb<16>(a, gps, s);
+    else if (a.M <= 8) mv_rb<8, true>(a, gps, s);
+    else mv_rb<16, true>(a, gps, s);
 }
 
 }  // namespace
