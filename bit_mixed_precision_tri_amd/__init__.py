@@ -341,6 +341,16 @@ def linear(X, Wp, scale, K, fmt, algo=TRI_ALGO_AUTO, out=None, stream=None):
 # The helpers below take the tensors' device (whichever device is current) and its current stream, or `stream`; they
 # raise ValueError for tensors of another type, shape, device or layout than they name.
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
@@ -348,16 +358,16 @@ def _need(ok, what):
 
 def _launch(name, device, stream, *args):
     """The entry point `name` on `device` (an ordinal) with the stream appended."""
-    import torch
-    if device != torch.cuda.current_device():
+    torch = _torch
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return _launch(name, device, stream, *args)
     if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device)
-    else:
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    rc = getattr(_lib or lib(), name)(*args, handle)
-    if rc != TRI_OK:
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    rc = getattr(_lib or lib(), name)(*args, stream)
+    if rc:
         raise TriError(rc, name)
 
 
@@ -375,10 +385,9 @@ def _tensors(device, dtype, **named):
 
 def _keep(t, stream):
     """Tell torch's allocator that temporary `t` is used on a stream that the caller named."""
-    import torch
     if stream is not None:
         h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        t.record_stream(torch.cuda.ExternalStream(h, device=t.device))
+        t.record_stream(_torch.cuda.ExternalStream(h, device=t.device))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -399,7 +408,7 @@ def _row_nbytes(K, fmt):
 def int4_pack(Q, S, group, Z=None, stream=None):
     """Lay out 4-bit codes Q (N, K) uint8 with group scales S (N, ceil(K/group)) float16 and, optionally, zero points
     Z of S's shape uint8 (8 everywhere without); returns a new uint8 tensor for int4_linear."""
-    import torch
+    torch = _torch or _load_torch()
     _need(Q.is_cuda and Q.dim() == 2 and Q.numel() > 0, "Q must be an (N, K) tensor on the GPU")
     (N, K), dev = Q.shape, Q.get_device()
     _tensors(dev, torch.uint8, Q=Q, Z=Z)
@@ -416,7 +425,7 @@ def int4_pack(Q, S, group, Z=None, stream=None):
 
 def int4_unpack(Wp, N, K, group, zeros=False, stream=None):
     """The codes, scales and zero points (None where zeros is false) of a packed 4-bit matrix."""
-    import torch
+    torch = _torch or _load_torch()
     _need(Wp.is_cuda, "Wp must be on the GPU")
     dev = Wp.get_device()
     _tensors(dev, torch.uint8, Wp=Wp)
@@ -433,7 +442,7 @@ def int4_unpack(Wp, N, K, group, zeros=False, stream=None):
 
 def int4_quantize(W, group, zeros=False, stream=None):
     """Quantise an (N, K) float32 tensor to 4-bit codes with group scales (and zero points), laid out for int4_linear."""
-    import torch
+    torch = _torch or _load_torch()
     _need(W.is_cuda and W.dim() == 2 and W.numel() > 0, "W must be an (N, K) tensor on the GPU")
     (N, K), dev = W.shape, W.get_device()
     _tensors(dev, torch.float32, W=W)
@@ -447,19 +456,23 @@ def int4_quantize(W, group, zeros=False, stream=None):
 def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=None):
     """Y = fp16(residual + X @ W.T) for an (M, K) fp16 tensor X and a packed 4-bit matrix of N rows.  `residual` may be
     `out` itself."""
-    import torch
+    torch = _torch or _load_torch()
     half, dev, shape = torch.float16, X.get_device(), X.shape
-    _need(dev >= 0 and len(shape) == 2 and _plain(X, half, dev), "X must be a contiguous (M, K) float16 tensor on the GPU")
+    if not (len(shape) == 2 and dev >= 0 and shape[0] > 0 and X.dtype is half and X.is_contiguous()):
+        raise ValueError("X must be a contiguous (M, K) float16 tensor on the GPU")
     M, K = shape
-    _need(_plain(Wp, torch.uint8, dev) and Wp.numel() == _int4_nbytes(N, K, group, bool(zeros)) and M > 0,
-          "Wp must be a uint8 tensor on X's device of tri_int4_bytes(N, K, group, zeros) bytes for X's width")
-    Y = out if out is not None else torch.empty((M, N), dtype=half, device=X.device)
-    _need(Y.shape == (M, N) and _plain(Y, half, dev), "out must be a contiguous (M, N) float16 tensor on X's device")
+    if not (Wp.dtype is torch.uint8 and Wp.get_device() == dev and Wp.is_contiguous() and
+            Wp.numel() == _int4_nbytes(N, K, group, zeros)):
+        raise ValueError("Wp must be a contiguous uint8 tensor on X's device of tri_int4_bytes(N, K, group, zeros) bytes for "
+                         "X's width")
+    Y = torch.empty((M, N), dtype=half, device=X.device) if out is None else out
     res = None
     if residual is not None:
         _need(residual.shape == (M, N) and _plain(residual, half, dev),
               "residual must be a contiguous (M, N) float16 tensor on X's device")
         res = residual.data_ptr()
+    if not (Y.shape == (M, N) and Y.dtype is half and Y.get_device() == dev and Y.is_contiguous()):
+        raise ValueError("out must be a contiguous (M, N) float16 tensor on X's device")
     _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0, res,
             Y.data_ptr())
     return Y
@@ -473,7 +486,7 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     """The top-k experts of every row of (T, E) float16 or float32 logits, their weights, and the order of the (token,
     expert) pairs by expert, as a Routing (the tensors of `out`, if it is given).  `workspace`: a uint8 tensor of at
     least tri_experts_route_workspace_bytes(T, E, topk) bytes; allocated where it is None."""
-    import torch
+    torch = _torch or _load_torch()
     dtype, dev, shape = logits.dtype, logits.get_device(), logits.shape
     _need(dev >= 0 and len(shape) == 2 and (dtype is torch.float16 or dtype is torch.float32) and logits.is_contiguous(),
           "logits must be a contiguous (T, E) float16 or float32 tensor on the GPU")
@@ -506,7 +519,7 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
 
 
 def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
-    import torch
+    torch = _torch or _load_torch()
     half, i32, dev, shape = torch.float16, torch.int32, X.get_device(), X.shape
     _need(dev >= 0 and len(shape) == 2 and shape[1] == K and shape[0] > 0 and _plain(X, half, dev),
           "X must be a contiguous (T, K) float16 tensor on the GPU")
@@ -545,20 +558,24 @@ def experts_pair(X, offsets, rows, Wp_gate, scale_gate, Wp_up, scale_up, K, fmt,
 def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
     """Y[t] = fp16(residual[t] + sum_j weights[t, j] * Z[pos[t, j]]); pairs with pos outside Z are left out.  `residual`
     may be `out` itself."""
-    import torch
-    half, dev, shape = torch.float16, Z.get_device(), Z.shape
-    _need(dev >= 0 and len(shape) == 2 and _plain(Z, half, dev) and Z.numel() > 0,
-          "Z must be a contiguous (R, N) float16 tensor on the GPU")
-    _need(_plain(pos, torch.int32, dev) and pos.dim() == 2 and _plain(weights, torch.float32, dev) and
-          weights.shape == pos.shape, "pos must be a contiguous (T, topk) int32 tensor on Z's device, weights float32 like it")
-    (R, N), (T, topk) = shape, pos.shape
-    Y = out if out is not None else torch.empty((T, N), dtype=half, device=Z.device)
-    _need(_plain(Y, half, dev) and Y.shape == (T, N), "out must be a contiguous (T, N) float16 tensor on Z's device")
+    torch = _torch or _load_torch()
+    half, dev, shape, pshape = torch.float16, Z.get_device(), Z.shape, pos.shape
+    if not (len(shape) == 2 and dev >= 0 and shape[0] > 0 and Z.dtype is half and Z.is_contiguous()):
+        raise ValueError("Z must be a contiguous (R, N) float16 tensor on the GPU")
+    if not (len(pshape) == 2 and pos.dtype is torch.int32 and pos.get_device() == dev and pos.is_contiguous() and
+            weights.shape == pshape and weights.dtype is torch.float32 and weights.get_device() == dev and
+            weights.is_contiguous()):
+        raise ValueError("pos must be a contiguous (T, topk) int32 tensor on Z's device, weights a float32 one like it")
+    (R, N), (T, topk) = shape, pshape
+    Y = torch.empty((T, N), dtype=half, device=Z.device) if out is None else out
     res = None
     if residual is not None:
-        _need(_plain(residual, half, dev) and residual.shape == (T, N),
-              "residual must be a contiguous (T, N) float16 tensor on Z's device")
+        if not (residual.shape == (T, N) and residual.dtype is half and residual.get_device() == dev and
+                residual.is_contiguous()):
+            raise ValueError("residual must be a contiguous (T, N) float16 tensor on Z's device")
         res = residual.data_ptr()
+    if not (Y.shape == (T, N) and Y.dtype is half and Y.get_device() == dev and Y.is_contiguous()):
+        raise ValueError("out must be a contiguous (T, N) float16 tensor on Z's device")
     _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), res, T, topk, N,
             Y.data_ptr())
     return Y
@@ -568,7 +585,7 @@ def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None
     """A gated MLP of experts: for every row of X, the weighted sum over its top-k experts of
     down(silu(gate(x)) * up(x)), plus `residual`.  gate, up and down are (packed weights, scales) as experts_pair and
     experts_linear take them, logits (T, E) as experts_route takes them.  Four launches or a few more, no waiting."""
-    import torch
+    torch = _torch or _load_torch()
     (T, hidden), inner = X.shape, gate[0].shape[1]
     r = experts_route(logits, topk, renorm=renorm, stream=stream)
     H = torch.empty((T * topk, inner), dtype=torch.float16, device=X.device)
