@@ -153,7 +153,8 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
     constexpr int kGM = 4;
     const int nwg = gridDim.x;
     int bid = blockIdx.x;
-    if ((nwg & 7) == 0) bid = (bid & 7) * (nwg >> 3) + (bid >> 3);
+    // (Not for experts: the list's unused tail would fall to one XCD; 2048 tokens, pair: 620 -> 635 us.)
+    if (!EXP && (nwg & 7) == 0) bid = (bid & 7) * (nwg >> 3) + (bid >> 3);
     constexpr int kParts = 4 / NT;               // workgroups per 128 x 512 tile
     static_assert(NT == 1 || NT == 2 || NT == 4, "tile widths");
     const int t = tile_base + bid / kParts;
@@ -412,7 +413,8 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
                     for (int nt = 0; nt < NB; ++nt) {
                         const int n = n0 + 32 * nt + c;
                         float y = acc[mt][nt][4 * i + v] * scale;
-                        if constexpr (PAIR) y = y / (1.f + __expf(-y)) * (acc[mt][nt + NB][4 * i + v] * scale2);
+                        if constexpr (PAIR)              // (v_exp and v_rcp: about 1 ulp)
+                            y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * (acc[mt][nt + NB][4 * i + v] * scale2);
                         if (n < N) Y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (_Float16)y);
                     }
                 }
@@ -442,8 +444,9 @@ __global__ __launch_bounds__(256) void k_gemm(const uint16_t *__restrict__ X, co
     gemm_tile<FMT, NT, BM, kLayer>(X, Wp, scale, M, N, K, C, tiles_m, tiles_n, tile_base, Y, Experts{});
 }
 
+// (three workgroups per CU: at most 168 registers)
 template <int FMT, int NT, int BM, int MODE>
-__global__ __launch_bounds__(256) void k_gemm_experts(const Experts ex, int C, int tiles_m, int tiles_n, int tile_base)
+__global__ __launch_bounds__(256, 3) void k_gemm_experts(const Experts ex, int C, int tiles_m, int tiles_n, int tile_base)
 {
     gemm_tile<FMT, NT, BM, MODE>(ex.X, nullptr, 0.f, 0, ex.N, ex.K, C, tiles_m, tiles_n, tile_base, ex.Y, ex);
 }
