@@ -276,10 +276,11 @@ __device__ __forceinline__ float4_t mfma(const u32x4 a, const u32x4 b, float4_t 
                                                   0, 0);
 }
 
-// A few rows per expert (tiles of MA = 1, 4 or 16 places): workgroup (x, y) computes RB blocks of 16 outputs of tile y.
+// A few rows per expert, of any length (tiles of MA = 4 or 16 places): workgroup (x, y) computes 16 outputs of tile y.  It
+// serves rows that are no whole 16-byte pieces or too long for the kernel after it.
 //
 // The eight waves split the row; wave w takes the chunk-steps w, w + 8, ..., where lane (g = lane/16, j = lane%16) reads
-// 16-byte chunk 4 s + g of weight row j of every block and decodes it to digits d = t + 1 in place, as exact fp16 values
+// 16-byte chunk 4 s + g of weight row j and decodes it to digits d = t + 1 in place, as exact fp16 values
 // d * 2^-24 (2-bit: masked, d * 4^p * 2^-24 at position p of a 16-bit half; 1.6-bit: multiply-shift quotients).  One
 // v_mfma_f32_16x16x32_f16 per position p contracts them; sum_k x, from products with ones, is taken off at the end.
 //
@@ -290,14 +291,14 @@ __device__ __forceinline__ float4_t mfma(const u32x4 a, const u32x4 b, float4_t 
 // reads its row's pieces whole and pairs the values in registers.
 //
 // Loads of the next step's activations and of the next kAhead steps' weights are in flight in registers.
-template <int FMT, int MA, int RB, bool PAIR, bool VEC>
+template <int FMT, int MA, bool PAIR, bool VEC>
 __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int slot0)
 {
     constexpr int NW = 8;
     constexpr bool TWO = FMT == TRI_FMT_2BIT;
     constexpr int XH = TWO ? 64 : 80;            // values per chunk
     constexpr int NOP = TWO ? 8 : 10;            // products per chunk
-    constexpr int CL = MA == 1 ? NOP : 16 / MA;  // products per gathered A operand
+    constexpr int CL = 16 / MA;                  // products per gathered A operand
     constexpr int NSET = (NOP + CL - 1) / CL;
     constexpr int NM = PAIR ? 2 : 1;             // matrices
     constexpr int PR = 4 * XH / 8;               // 16-byte pieces of a row per step
@@ -307,7 +308,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     // accumulators: one per product of an A operand and scale of its digits
     constexpr int NACC = MA == 16 ? (TWO ? 6 : 2) : (TWO ? 8 : CL);
     __shared__ __attribute__((aligned(16))) uint16_t xs[NW][MA][ROW];
-    __shared__ float red[NW][MA][16 * RB * NM + 1];
+    __shared__ float red[NW][MA][16 * NM + 1];
 
     const int lane = threadIdx.x & 63;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -316,7 +317,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     if (et.e < 0) return;                        // (the whole workgroup)
     const int K = ex.K, N = ex.N;
     const int64_t S = (int64_t)C * 16;
-    const int n0 = (int)blockIdx.x * 16 * RB;
+    const int n0 = (int)blockIdx.x * 16;
 
     // source rows of the tile, -1 where there is none: lane l holds row l's
     int src = -1;
@@ -324,20 +325,17 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
         src = ex.rows ? ex.rows[et.r0 + lane] : et.r0 + lane;
         if (src < 0 || src >= ex.T) src = -1;
     }
-    const int wrows = min(16 * RB, N - n0);
+    const int wrows = min(16, N - n0);
     __amdgpu_buffer_rsrc_t wr[NM];
 #pragma unroll
     for (int q = 0; q < NM; ++q)
         wr[q] = rsrc(ex.Wp[q] + ((int64_t)et.e * N + n0) * S, __builtin_amdgcn_readfirstlane((uint32_t)(wrows * S)));
-    u32x4 w[kAhead][NM][RB];
-    auto load_w = [&](int s, u32x4 (&t)[NM][RB]) __attribute__((always_inline)) {
+    u32x4 w[kAhead][NM];
+    auto load_w = [&](int s, u32x4 (&t)[NM]) __attribute__((always_inline)) {
         const int c = 4 * s + g;
 #pragma unroll
         for (int q = 0; q < NM; ++q)
-#pragma unroll
-            for (int r = 0; r < RB; ++r)
-                t[q][r] = __builtin_amdgcn_raw_buffer_load_b128(
-                    wr[q], (int)(c < C ? (uint32_t)((16 * r + j) * S + 16 * c) : kOob), 0, 0);
+            t[q] = __builtin_amdgcn_raw_buffer_load_b128(wr[q], (int)(c < C ? (uint32_t)(j * S + 16 * c) : kOob), 0, 0);
     };
     const int ns = (C + 3) / 4;                  // steps of the row
 #pragma unroll
@@ -368,13 +366,11 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     if (wv < ns) load_x(wv);
 
     const float4_t zero4 = {0.f, 0.f, 0.f, 0.f};
-    float4_t acc[NM][RB][NACC], accx = zero4;
+    float4_t acc[NM][NACC], accx = zero4;
 #pragma unroll
     for (int q = 0; q < NM; ++q)
 #pragma unroll
-        for (int r = 0; r < RB; ++r)
-#pragma unroll
-            for (int c = 0; c < NACC; ++c) acc[q][r][c] = zero4;
+        for (int c = 0; c < NACC; ++c) acc[q][c] = zero4;
     const u32x4 ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 
     // digits of a chunk for product p (and, 1.6-bit, half hh: products 2 p + hh)
@@ -399,7 +395,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
             }
         }
     };
-    auto step = [&](int s, u32x4 (&wc)[NM][RB]) __attribute__((always_inline)) {
+    auto step = [&](int s, u32x4 (&wc)[NM]) __attribute__((always_inline)) {
         // this step's activations into LDS, the next step's on the way
 #pragma unroll
         for (int i = 0; i < NLD; ++i) {
@@ -439,15 +435,13 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 #pragma unroll
             for (int p = 0; p < NOP; ++p) accx = mfma(a[p], ones, accx);
 #pragma unroll
-            for (int q = 0; q < NM; ++q)
-#pragma unroll
-                for (int r = 0; r < RB; ++r) contract(a, wc[q][r], acc[q][r]);
+            for (int q = 0; q < NM; ++q) contract(a, wc[q], acc[q]);
         } else {
             u32x4 a[NSET];
-            const int aa = j % MA, c = j / MA;   // (MA = 1: A rows past the products repeat the last one's, unused)
+            const int aa = j % MA, c = j / MA;
 #pragma unroll
             for (int t = 0; t < NSET; ++t) {
-                const int op = min(CL * t + (MA == 1 ? min(c, CL - 1) : c), NOP - 1);
+                const int op = min(CL * t + c, NOP - 1);
                 const uint16_t *x = &xs[wv][aa][XH * g + (TWO ? op : 5 * 4 * (op & 1) + (op >> 1))];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
@@ -458,9 +452,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
                 accx = mfma(a[t], ones, accx);
             }
 #pragma unroll
-            for (int q = 0; q < NM; ++q)
-#pragma unroll
-                for (int r = 0; r < RB; ++r) contract(a, wc[q][r], acc[q][r]);
+            for (int q = 0; q < NM; ++q) contract(a, wc[q], acc[q]);
         }
     };
     for (int s = wv; s < ns; s += NW * kAhead) {
@@ -476,74 +468,36 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     // Merge: product op's rows of result r lie in A rows MA c + a, c = op % CL: lane group (MA c + a) / 4, element
     // (MA c + a) % 4.  Lanes take what is theirs, and the lane groups that hold the same row are added.
     auto unit = [&](int p) { return TWO ? 1.f / (float)(1 << (2 * (p < 6 ? p : p - 6))) : 1.f; };
-    auto put = [&](int col, float (&v)[4]) __attribute__((always_inline)) {   // v[e]: this lane's rows
-        if constexpr (MA == 16) {
+    auto put = [&](int col, float (&v)[4], bool leader) __attribute__((always_inline)) {   // v[e]: this lane's rows
 #pragma unroll
-            for (int e = 0; e < 4; ++e) red[wv][4 * g + e][col] = v[e];
-        } else {
-#pragma unroll
-            for (int e = 0; e < MA; ++e) {
-                const float t = sum_over_rows(v[e]);
-                if (g == 0) red[wv][e][col] = t;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const float t = MA == 16 ? v[e] : sum_over_rows(v[e]);
+            if (leader) red[wv][MA == 16 ? 4 * g + e : e][col] = t;
         }
     };
 #pragma unroll
-    for (int q = 0; q < NM; ++q)
-#pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (MA == 16) {
-#pragma unroll
-                for (int c = 0; c < NACC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += acc[q][r][c][e] * unit(c);
-            } else if constexpr (MA == 4) {      // class c in lane group c
-#pragma unroll
-                for (int c = 0; c < NACC; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] += g == c % 4 ? acc[q][r][c][e] * unit(c) : 0.f;
-            } else {                             // product c: lane group c / 4, element c % 4
-#pragma unroll
-                for (int c = 0; c < NACC; ++c) v[0] += g == c / 4 ? acc[q][r][c][c % 4] * unit(c) : 0.f;
-            }
-            put(16 * (RB * q + r) + j, v);
-        }
-    // sum_k x: every product of an A operand counts once
-    {
+    for (int q = 0; q < NM; ++q) {
         float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if constexpr (MA == 1) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[0] += 4 * g + c < CL ? accx[c] : 0.f;
-        } else {
+        for (int c = 0; c < NACC; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = accx[e];
-        }
-        if constexpr (MA == 16) {
-            if (j == 0) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) red[wv][4 * g + e][16 * RB * NM] = v[e];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < MA; ++e) {
-                const float t = sum_over_rows(v[e]);
-                if (lane == 0) red[wv][e][16 * RB * NM] = t;
-            }
-        }
+            for (int e = 0; e < 4; ++e) v[e] += MA == 16 || g == c % 4 ? acc[q][c][e] * unit(c) : 0.f;
+        put(16 * q + j, v, MA == 16 || g == 0);
     }
+    float vx[4] = {accx[0], accx[1], accx[2], accx[3]};   // sum_k x: every product of an A operand counts once
+    put(16 * NM, vx, MA == 16 ? j == 0 : lane == 0);
     __syncthreads();
-    for (int o = threadIdx.x; o < MA * 16 * RB; o += 64 * NW) {
-        const int m = o / (16 * RB), c = o % (16 * RB);
+    for (int o = threadIdx.x; o < MA * 16; o += 64 * NW) {
+        const int m = o / 16, c = o % 16;
         if (m >= et.rows || n0 + c >= N) continue;
         const int row = ex.rows ? ex.rows[et.r0 + m] : et.r0 + m;
         if (row < 0 || row >= ex.T) continue;
         float sx = 0.f, sd[NM] = {};
 #pragma unroll
         for (int q = 0; q < NW; ++q) {
-            sx += red[q][m][16 * RB * NM];
+            sx += red[q][m][16 * NM];
 #pragma unroll
-            for (int p = 0; p < NM; ++p) sd[p] += red[q][m][16 * RB * p + c];
+            for (int p = 0; p < NM; ++p) sd[p] += red[q][m][16 * p + c];
         }
         float y = (sd[0] * 16777216.0f - sx) * ex.scale[0][et.e];
         if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16777216.0f - sx) * ex.scale[1][et.e]);
@@ -612,7 +566,7 @@ __global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int 
     // which the q-th takes blocks q, q + G, ...
     int G = 1;
     const ExpertTile et = expert_tile(ex.offsets, ex.E, ex.R, MA, [&](int tiles) {
-        G = min((int)gridDim.x / max(tiles, 1), nblk);
+        G = max(min((int)gridDim.x / max(tiles, 1), nblk), 1);   // (offsets that decrease list more tiles than there may be)
         return (int)blockIdx.x / G;
     });
     if (et.e < 0) return;                        // (the whole workgroup)
@@ -950,14 +904,14 @@ int launch_route(const void *logits, bool half, int T, int E, int topk, bool ren
 
 namespace {
 
-template <int FMT, int MA, int RB, bool PAIR, bool VEC>
+template <int FMT, int MA, bool PAIR, bool VEC>
 void experts_go(const Experts &ex, hipStream_t s)
 {
     const int C = (int)(row_bytes(ex.K, FMT) / 16);
     const int64_t slots = expert_slots(ex.R, ex.E, MA);
     for (int64_t s0 = 0; s0 < slots; s0 += 65535) {   // (the second grid dimension's limit)
-        const dim3 grid((ex.N + 16 * RB - 1) / (16 * RB), (unsigned)(slots - s0 < 65535 ? slots - s0 : 65535));
-        hipLaunchKernelGGL((k_experts_mv<FMT, MA, RB, PAIR, VEC>), grid, dim3(512), 0, s, ex, C, (int)s0);
+        const dim3 grid((ex.N + 15) / 16, (unsigned)(slots - s0 < 65535 ? slots - s0 : 65535));
+        hipLaunchKernelGGL((k_experts_mv<FMT, MA, PAIR, VEC>), grid, dim3(512), 0, s, ex, C, (int)s0);
     }
 }
 
@@ -1013,8 +967,8 @@ int experts_ma(const Experts &ex, hipStream_t s)
         if (ex.R / 2 > ex.E && experts_gemm_fits(ex, FMT)) return launch_experts_gemm(ex, FMT, s);
     }
     // rows too long for the loop, or no whole 16-byte pieces
-    if (ex.R <= ex.E) experts_go<FMT, 4, 1, PAIR, VEC>(ex, s);
-    else experts_go<FMT, 16, 1, PAIR, VEC>(ex, s);
+    if (ex.R <= ex.E) experts_go<FMT, 4, PAIR, VEC>(ex, s);
+    else experts_go<FMT, 16, PAIR, VEC>(ex, s);
     return launched();
 }
 

@@ -257,6 +257,64 @@ def test_offsets_past_the_places_are_clamped(fmt):
         check_experts(rng, R, 3, 64, 256, fmt, [2, R, 40], False, False, R=R)
 
 
+@pytest.mark.parametrize("fmt", [F2, F16])
+def test_offsets_that_decrease_stay_inside(fmt):
+    """Offsets against the contract: what is written is unspecified, but only places 0 .. R - 1 are, and the call ends."""
+    import torch
+    E, N, K = 16, 48, 256
+    W = torch.zeros((E, N, tri.tri_row_bytes(K, fmt)), dtype=torch.uint8, device="cuda")
+    s = torch.ones(E, device="cuda")
+    for R in (1, 7, 100, 1000):
+        X = torch.zeros((R, K), dtype=torch.float16, device="cuda")
+        for off in ([0, R] * 8 + [0], [R] * 17, [-5, 1 << 30] * 8 + [-(1 << 31)], list(range(16, -1, -1))):
+            o = torch.tensor(off, dtype=torch.int32, device="cuda")
+            Y = torch.full((R + 64, N), 7.0, dtype=torch.float16, device="cuda")
+            say("decreasing offsets R=%d fmt=%d" % (R, fmt))
+            tri.tri_experts_linear(X, R, o, None, R, W, s, E, N, K, fmt, Y)
+            tri.tri_experts_pair(X, R, o, None, R, W, s, W, s, E, N, K, fmt, Y)
+            assert np.all(host(Y)[R:] == 7.0)
+
+
+@pytest.mark.parametrize("places", [3, 200])
+def test_gathered_rows_near_the_end_of_four_gigabytes(places):
+    """X of almost 4 GiB, its rows gathered from both ends, by the kernels of few and of many places."""
+    import torch
+    rng = np.random.default_rng([66, places])
+    K, N = 4096, 40
+    T = ((1 << 31) - 8) // K
+    X = torch.zeros((T, K), dtype=torch.float16, device="cuda")
+    rows = np.concatenate([rng.integers(0, 50, places // 2), T - 1 - rng.integers(0, 50, places - places // 2),
+                           [T // 2 - 1, T // 2]]).astype(np.int32)
+    x = rng.standard_normal((len(rows), K)).astype(np.float16)
+    X[cuda(rows).long()] = cuda(x)               # (of a row named twice, one copy stays)
+    W = synth.trits(rng, N, K)
+    Wp = tri.pack(cuda(W), F2).view(1, N, -1)
+    off = cuda(np.array([0, len(rows)], dtype=np.int32))
+    Y = host(tri.experts_linear(X, off, cuda(rows), Wp, torch.full((1,), 0.02, device="cuda"), K, F2)).astype(np.float64)
+    x = host(X[cuda(rows).long()]).astype(np.float64)
+    ref = float(np.float32(0.02)) * (x @ W.astype(np.float64).T)
+    assert np.all(np.abs(Y - ref) <= sum_bound(K, 0.02, x) + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25)
+
+
+@pytest.mark.parametrize("M", [1, 3, 40])
+def test_weights_past_four_gigabytes(M):
+    """The last expert of a stack of more than 4 GiB gives what it gives alone."""
+    import torch
+    rng = np.random.default_rng([67, M])
+    E, N, K = 9, 65536, 32768
+    Wp = torch.zeros((E, N, tri.tri_row_bytes(K, F2)), dtype=torch.uint8, device="cuda").fill_(0x55)
+    assert Wp.numel() > 1 << 32
+    Wp[-1, -100:] = tri.pack(cuda(synth.trits(rng, 100, K)), F2)
+    X = cuda(rng.standard_normal((M, K)).astype(np.float16))
+    s = torch.full((E,), 0.01, device="cuda")
+    all_ = tri.experts_linear(X, cuda(np.array([0] * E + [M], dtype=np.int32)), None, Wp, s, K, F2)
+    one = tri.experts_linear(X, cuda(np.array([0, M], dtype=np.int32)), None, Wp[-1:, -100:].contiguous(), s[:1], K, F2)
+    a, b = host(all_).astype(np.float64), host(one).astype(np.float64)
+    x = host(X).astype(np.float64)
+    assert np.all(np.abs(a[:, :-100]) <= sum_bound(K, 0.01, x) + 2.0 ** -25)   # zero trits
+    assert np.all(np.abs(a[:, -100:] - b) <= 2 * sum_bound(K, 0.01, x) + 2.0 ** -10 * np.abs(b) + 2.0 ** -24)
+
+
 def test_one_expert_equals_the_layer():
     """Against tri_linear on the same matrix, within both tolerances, and the packed rows of one tri_pack2 call for all
     experts are those of one call each."""

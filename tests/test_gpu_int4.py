@@ -196,6 +196,27 @@ def test_extreme_values(M):
     assert np.all(np.abs(Y[fits].astype(np.float64) - ref[fits]) <= tol[fits])
 
 
+@pytest.mark.parametrize("M", [1, 7, 40])
+def test_weights_past_four_gigabytes(M):
+    """The last blocks of a matrix of more than 4 GiB of codes give what they give alone."""
+    import torch
+    rng = np.random.default_rng([48, M])
+    N, K, group = (1 << 20) + 4096, 8192, 128
+    nb, ks = N // 16, K // 128
+    Wp = torch.zeros(tri.tri_int4_bytes(N, K, group, False), dtype=torch.uint8, device="cuda")
+    n = 64
+    Q, S, _ = matrix(rng, n, K, group, False)
+    small = tri.int4_pack(cuda(Q), cuda(S), group)
+    codes, scales = n // 16 * ks * 1024, n // 16 * ks * 32
+    assert nb * ks * 1024 > 1 << 32 and small.numel() == codes + scales
+    Wp[nb * ks * 1024 - codes:nb * ks * 1024] = small[:codes]
+    Wp[Wp.numel() - scales:] = small[codes:]
+    X = rng.standard_normal((M, K)).astype(np.float16)
+    Y = host(tri.int4_linear(cuda(X), Wp, N, group))
+    check(Y[:, -n:], X, dense(Q, S, None, group))
+    assert np.all(Y[:, :-n] == 0.0)
+
+
 def test_rows_behind_the_output_are_untouched():
     """Only M x N values are written, and only the codes of N rows count."""
     import torch
