@@ -198,17 +198,18 @@ def test_extreme_values(M):
 
 @pytest.mark.parametrize("M", [1, 7, 40])
 def test_weights_past_four_gigabytes(M):
-    """The last blocks of a matrix of more than 4 GiB of codes give what they give alone."""
+    """The last blocks of the largest matrix, whose scales lie past 4 GiB, give what they give alone."""
     import torch
     rng = np.random.default_rng([48, M])
-    N, K, group = (1 << 20) + 4096, 8192, 128
+    N, K, group = (1 << 20) - 16, 8192, 128
+    assert tri.tri_int4_bytes(N + 16, K, group, False) == -1
     nb, ks = N // 16, K // 128
     Wp = torch.zeros(tri.tri_int4_bytes(N, K, group, False), dtype=torch.uint8, device="cuda")
     n = 64
     Q, S, _ = matrix(rng, n, K, group, False)
     small = tri.int4_pack(cuda(Q), cuda(S), group)
     codes, scales = n // 16 * ks * 1024, n // 16 * ks * 32
-    assert nb * ks * 1024 > 1 << 32 and small.numel() == codes + scales
+    assert Wp.numel() > 1 << 32 and small.numel() == codes + scales
     Wp[nb * ks * 1024 - codes:nb * ks * 1024] = small[:codes]
     Wp[Wp.numel() - scales:] = small[codes:]
     X = rng.standard_normal((M, K)).astype(np.float16)
