@@ -28,7 +28,7 @@ Int4Map int4_map(int64_t N, int64_t K, int group) { return {(N + 15) / 16, (K + 
 // bit position of value i of a word
 __device__ __forceinline__ int nibble_at(int i) { return 4 * (i / 2) + 16 * (i % 2); }
 
-// One workgroup per tile (block b, step s): thread (j, q) packs piece q (8 values) of row j.  Threads
+// The layout kernels move each byte once.  One workgroup per tile (block b, step s): thread (j, q) packs piece q (8 values) of row j.  Threads
 // q < gps also write a scale and a zero point.
 __global__ __launch_bounds__(256) void k_int4_pack(const uint8_t *__restrict__ Q, const uint16_t *__restrict__ S,
                                                    const uint8_t *__restrict__ Z, int N, int K, int KS, int gps,
@@ -171,6 +171,11 @@ __device__ __forceinline__ u32x4 decode(uint32_t w, uint32_t b10, uint32_t b6, u
 // of the result holds row j's products of step tl(g), so it loads the scales of that row and step.  Zero points
 // shift the codes as they are decoded (U == 1), or are taken off by sum_k x, formed by one more product with
 // ones per A load (U > 1, where a lane decodes other steps than it scales).
+//
+// One row is bound by the weight stream: 4096 -> 11008 (23.3 MB, group 128) takes 6.6 us, a plain read of as many bytes
+// 4.7 us, an empty launch 1.9 us; 8192 -> 28672 (121 MB) 24.6 us against 19.4.  From about eight rows on the activations
+// that every workgroup reads weigh as much (16 rows: 7.9 us, and 12.7 us on 11008 -> 4096).  Twelve or sixteen waves, or
+// three to six units in flight, changed a few shapes by 5% either way and are not used.
 template <int MA, int RB, int GPS, bool ZP, int NW, bool VEC>
 __global__ __launch_bounds__(64 * NW) void k_int4_mv(const uint16_t *__restrict__ X, const uint8_t *__restrict__ codes,
                                                      const uint16_t *__restrict__ scales,
