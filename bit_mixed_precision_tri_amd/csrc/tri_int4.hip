@@ -444,7 +444,7 @@ __device__ __forceinline__ void group_barrier()
 // rows, 256 consecutive bytes each.  Weights and scales go to registers, as far ahead.  The order of issue, a step's weights
 // and then its activations, is what the waits count on.
 //
-// Measured at 64 rows, 8192 -> 28672, group 64: 53 us, of which the loads alone take 38 (the weights alone 28) and the
+// Measured at 64 rows, 8192 -> 28672, group 64: 50 us, of which the loads alone take 38 (the weights alone 28) and the
 // products and decoding alone 36: the two overlap by half.  More outputs per wave, one group or four, two or three buffers
 // were no faster (54 - 99 us).
 constexpr int kMmWaves = 8;                      // waves of a workgroup: two groups of four
@@ -825,9 +825,12 @@ int launch_int4_linear(const uint16_t *X, const uint8_t *Wp, int M, int N, int K
     const Int4Map m = int4_map(N, K, group);
     if (m.tiles() >= kInt4MaxTiles || K >= kInt4MaxK) return TRI_EINVAL;
     uint8_t *p = const_cast<uint8_t *>(Wp);      // (read only)
-    // 16-row slices go to the second grid dimension, at most 65535 of them per launch
-    for (int64_t m0 = 0; m0 < M; m0 += 16 * 65535) {
-        const int rows = (int)(M - m0 < 16 * 65535 ? M - m0 : 16 * 65535);
+    // Rows per launch: at most 65535 16-row slices (the second grid dimension) and 2^22 tiles of 32 x 128 (a grid has
+    // fewer than 2^32 threads), a multiple of 64.
+    const int64_t cols = ((int64_t)N + 127) / 128, tiles = ((int64_t)1 << 22) / cols * 32 / 64 * 64;
+    const int64_t most = tiles < 64 ? 64 : tiles < 16 * 65535 ? tiles : 16 * 65535;
+    for (int64_t m0 = 0; m0 < M; m0 += most) {
+        const int rows = (int)(M - m0 < most ? M - m0 : most);
         const Int4Args a{X + m0 * K, Wp, scales_of(p, m), zeros ? zeros_of(p, m) : nullptr, rows, N, K, (int)m.KS,
                          R ? R + m0 * N : nullptr, Y + m0 * N};
         mv_rows(a, m.gps, s);

@@ -218,6 +218,23 @@ def test_weights_past_four_gigabytes(M):
     assert np.all(Y[:, :-n] == 0.0)
 
 
+def test_more_rows_than_one_launch_takes():
+    """An output of more than 2^22 tiles of 32 x 128 (34 GB) is made by several launches: rows at their seam and the last."""
+    import torch
+    rng = np.random.default_rng(49)
+    N, K, group = 1 << 16, 128, 128
+    seam = (1 << 22) // (N // 128) * 32
+    M = seam + 40
+    Q, S, _ = matrix(rng, N, K, group, False)
+    X = rng.standard_normal((M, K)).astype(np.float16)
+    out = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+    tri.int4_linear(cuda(X), tri.int4_pack(cuda(Q), cuda(S), group), N, group, out=out)
+    for m0 in range(0, M, 1 << 14):
+        assert not bool(out[m0:m0 + (1 << 14)].isnan().any())
+    rows = np.r_[0:3, seam - 20:seam, seam:M]
+    check(host(out[torch.from_numpy(rows).cuda()]), X[rows], dense(Q, S, None, group))
+
+
 def test_rows_behind_the_output_are_untouched():
     """Only M x N values are written, and only the codes of N rows count."""
     import torch
