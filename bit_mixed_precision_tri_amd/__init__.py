@@ -384,7 +384,7 @@ def _tensors(device, dtype, **named):
 
 
 def _keep(t, stream):
-    """Tell torch's allocator that temporary `t` is used on a stream that the caller named."""
+    """Tell torch's allocator that `t`, allocated here on the current stream, is used on a stream that the caller named."""
     if stream is not None:
         h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         t.record_stream(_torch.cuda.ExternalStream(h, device=t.device))
@@ -420,6 +420,7 @@ def int4_pack(Q, S, group, Z=None, stream=None):
     Wp = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
     _launch("tri_int4_pack", dev, stream, Q.data_ptr(), S.data_ptr(), None if Z is None else Z.data_ptr(), N, K, group,
             Wp.data_ptr())
+    _keep(Wp, stream)
     return Wp
 
 
@@ -437,6 +438,8 @@ def int4_unpack(Wp, N, K, group, zeros=False, stream=None):
     Z = torch.empty(shape, dtype=torch.uint8, device=Wp.device) if zeros else None
     _launch("tri_int4_unpack", dev, stream, Wp.data_ptr(), N, K, group, 1 if zeros else 0, Q.data_ptr(), S.data_ptr(),
             None if Z is None else Z.data_ptr())
+    for made in (Q, S) if Z is None else (Q, S, Z):
+        _keep(made, stream)
     return Q, S, Z
 
 
@@ -450,6 +453,7 @@ def int4_quantize(W, group, zeros=False, stream=None):
     _need(nbytes > 0, "group must be 32, 64 or 128 (and the matrix below 2^22 tiles)")
     Wp = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
     _launch("tri_int4_quantize", dev, stream, W.data_ptr(), N, K, group, 1 if zeros else 0, Wp.data_ptr())
+    _keep(Wp, stream)
     return Wp
 
 
@@ -475,6 +479,8 @@ def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=No
         raise ValueError("out must be a contiguous (M, N) float16 tensor on X's device")
     _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0, res,
             Y.data_ptr())
+    if out is None:
+        _keep(Y, stream)
     return Y
 
 
@@ -493,8 +499,8 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     T, E = shape
     need = _route_nbytes(T, E, topk)
     _need(need >= 0, "1 <= E <= %d, 1 <= topk <= min(E, %d) and T * topk < 2^31 are taken" % (TRI_MAX_EXPERTS, TRI_MAX_TOPK))
-    i32 = torch.int32
-    if out is None:
+    i32, mine = torch.int32, out is None
+    if mine:
         kw = dict(dtype=i32, device=logits.device)
         out = Routing(torch.empty((T, topk), **kw), torch.empty((T, topk), dtype=torch.float32, device=logits.device),
                       torch.empty(E + 1, **kw), torch.empty(T * topk, **kw), torch.empty((T, topk), **kw))
@@ -513,8 +519,9 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     _launch("tri_experts_route", dev, stream, logits.data_ptr(), TRI_F16 if dtype is torch.float16 else TRI_F32, T, E, topk,
             1 if renorm else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), ws,
             nbytes)
-    if temporary:
-        _keep(workspace, stream)
+    if stream is not None:
+        for made in (out if mine else ()) + ((workspace,) if temporary else ()):
+            _keep(made, stream)
     return out
 
 
@@ -540,6 +547,8 @@ def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
               "weights must be contiguous (E, N, tri_row_bytes(K, fmt)) uint8 tensors, scales (E) float32, on X's device")
         args += [W.data_ptr(), scale.data_ptr()]
     _launch(name, dev, stream, X.data_ptr(), T, offsets.data_ptr(), rp, R, *args, E, N, K, fmt, Y.data_ptr())
+    if out is None:
+        _keep(Y, stream)
     return Y
 
 
@@ -578,6 +587,8 @@ def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
         raise ValueError("out must be a contiguous (T, N) float16 tensor on Z's device")
     _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), res, T, topk, N,
             Y.data_ptr())
+    if out is None:
+        _keep(Y, stream)
     return Y
 
 
@@ -593,6 +604,6 @@ def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None
     experts_pair(X, r.offsets, r.rows, *gate, *up, hidden, fmt, out=H, stream=stream)
     experts_linear(H, r.offsets, None, *down, inner, fmt, out=Z, stream=stream)
     Y = experts_combine(Z, r.pos, r.weights, residual=residual, stream=stream)
-    for t in r + (H, Z):
-        _keep(t, stream)
+    for made in (H, Z):
+        _keep(made, stream)
     return Y

@@ -489,6 +489,29 @@ def test_two_streams_at_once():
             assert torch.equal(a, b)
 
 
+def test_results_of_a_named_stream_outlive_their_tensors():
+    """Helpers that allocate and run on a stream that is not the current one: memory that the caller lets go while that
+    stream is still at work is not handed to the current stream's next allocation."""
+    import torch
+    rng = np.random.default_rng(68)
+    T, E, topk, hidden, inner = 300, 8, 2, 256, 384
+    Wr, (gate, up, down) = mixed_block(rng, T, E, topk, hidden, inner, F2)
+    X = cuda(rng.standard_normal((T, hidden)).astype(np.float16))
+    want = tri.experts_mlp(X, tri.int4_linear(X, Wr, E, 64), topk, gate, up, down, F2).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        Y = tri.experts_mlp(X, tri.int4_linear(X, Wr, E, 64, stream=s), topk, gate, up, down, F2, stream=s)
+        for n in (T * topk * inner, T * topk * hidden, T * hidden, T * E):   # sizes of what was let go
+            torch.full((n,), float("nan"), dtype=torch.float16, device="cuda")
+        got.append(Y)
+    torch.cuda.synchronize()
+    for Y in got:
+        assert torch.equal(Y, want)
+
+
 def test_refusals_of_the_helpers():
     import torch
     h, i, u, f = (dict(dtype=d, device="cuda") for d in (torch.float16, torch.int32, torch.uint8, torch.float32))
