@@ -43,7 +43,7 @@ __device__ __forceinline__ ExpertTile expert_tile_of(const int32_t *__restrict__
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int rows = PER * lane + i < E ? max(at[i + 1] - at[i], 0) : 0;
-        n[i] = (rows + height - 1) / height;
+        n[i] = (int)(((unsigned)rows + height - 1) / height);   // (unsigned: rows up to 2^31 - 1)
         sum += n[i];
     }
     const int run = wave_scan(sum);

@@ -165,7 +165,7 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
     const int in_band = t - band * kGM * tiles_n;
     const int tm = first_m + in_band % band_m;
     const int tn = in_band / band_m;
-    const int m0 = tm * kBMt;
+    const int m0 = EXP ? 0 : tm * kBMt;          // (experts: rows count from the tile's first)
     constexpr int kCols = PAIR ? kBN / 2 : kBN;  // output columns of a tile
     const int n0 = tn * kCols + (bid % kParts) * (kCols / kParts) + 32 * NB * wv;   // this wave's first column
 
@@ -185,7 +185,7 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
         }
         __syncthreads();
         Y += (int64_t)et.r0 * N;
-        M = m0 + et.rows;
+        M = et.rows;
         scale = ex.scale[0][et.e];
     }
 

@@ -275,6 +275,28 @@ def test_offsets_that_decrease_stay_inside(fmt):
             assert np.all(host(Y)[R:] == 7.0)
 
 
+@pytest.mark.parametrize("K", [8, 5])
+def test_the_most_places_that_one_expert_may_own(K):
+    """2^31 - 1 places of one expert out of three: the last tile's bounds stay below 2^31, nothing is lost (small integers:
+    every sum is exact)."""
+    import torch
+    rng = np.random.default_rng([69, K])
+    R, T, E, N = (1 << 31) - 1, 5, 3, 1
+    W = rng.integers(-1, 2, (E * N, K)).astype(np.int8)
+    X = rng.integers(-4, 5, (T, K)).astype(np.float16)
+    want = cuda((X.astype(np.float64) @ W[1].astype(np.float64)).astype(np.float16))
+    rows = torch.empty(R, dtype=torch.int32, device="cuda")
+    step = 1 << 28
+    for r in range(0, R, step):
+        rows[r:r + step] = torch.arange(r, min(r + step, R), device="cuda") % T
+    offsets = torch.tensor([0, 0, R, R], dtype=torch.int32, device="cuda")
+    Y = torch.full((R, N), float("nan"), dtype=torch.float16, device="cuda")
+    tri.experts_linear(cuda(X), offsets, rows, tri.pack(cuda(W), F2).view(E, N, -1), torch.ones(E, device="cuda"), K,
+                       F2, out=Y)
+    for r in range(0, R, step):
+        assert torch.equal(Y[r:r + step, 0], want[rows[r:r + step].long()]), r
+
+
 @pytest.mark.parametrize("places", [3, 200])
 def test_gathered_rows_near_the_end_of_four_gigabytes(places):
     """X of almost 4 GiB, its rows gathered from both ends, by the kernels of few and of many places."""
