@@ -508,7 +508,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 }
 
 // The same product with the activations kept: rows short enough that a wave's A operands of all its CST steps stay in
-// registers (gathered once, as above; tiles of MA = 1, 4, 8 or 16 places).  The workgroup then runs through blocks of 16
+// registers (gathered once, as above; tiles of MA = 1, 8 or 16 places).  The workgroup then runs through blocks of 16
 // outputs, blockIdx.x, + gridDim.x, ...: only weights are read, the next block's chunks in flight while one is
 // contracted; the waves' partial sums meet in one of two LDS buffers in turn, so a block costs one barrier.
 //
@@ -522,6 +522,9 @@ constexpr int kHeld = 16;                        // blocks whose results wait in
 // (two workgroups per CU) that the compiler spills nothing, or next to nothing; limits as found by compiling.
 constexpr bool loop_fits(int fmt, int ma, int cst, bool pair, int d)
 {
+    // (84 KB of LDS: one workgroup per CU.  Eight experts, two per token, pair, with 256 registers and the next block's
+    // chunks in flight against 128: 64 tokens 2048 -> 5632 28 / 31 us, 4096 -> 11008 76 / 71, 96 tokens 85 / 86)
+    if (ma == 16 && fmt == TRI_FMT_1P6BIT) return false;
     const int nop = fmt == TRI_FMT_2BIT ? 8 : 10, cl = ma == 1 ? nop : 16 / ma, na = (nop + cl - 1) / cl;
     return 4 * cst * (na + (pair ? 2 : 1) * d) <= (fmt == TRI_FMT_2BIT ? 80 : ma == 1 ? 40 : 64);
 }

@@ -535,9 +535,10 @@ bool experts_gemm_fits(const Experts &ex, int fmt)
 
 // Tiles of 64 places, whatever the sizes: several such workgroups share a CU, the last tile of an expert wastes little,
 // and 128-place tiles lost at every measured size (pair, 2-bit, 4096 -> 11008, eight experts, two per token: 256 tokens
-// 150 against 202 us, 2048 tokens 655 against 654 (256 columns) and 727 us (512); 1.6-bit 798 against 828 - 1029).  Two
-// column tiles per wave for a pair; for one matrix one, or two for 2-bit digits where those still make two rounds
-// (11008 -> 4096, 2048 tokens 369 -> 332 us, 256 tokens 82 -> 85 us; 1.6-bit 421 -> 422 us, 256 tokens 101 -> 122 us).
+// 150 against 202 us, 2048 tokens 655 against 654 (256 columns) and 727 us (512); 1.6-bit 798 against 828 - 1029; with the
+// gate as it is now the 64-place tiles take 612 and 730).  Two column tiles per wave for a pair; for one matrix one, or
+// two for 2-bit digits where those still make two rounds (11008 -> 4096, 2048 tokens 369 -> 332 us, 256 tokens 82 -> 85
+// us; 1.6-bit 421 -> 422 us, 256 tokens 101 -> 122 us).
 template <int FMT>
 static int launch_experts_fmt(const Experts &ex, hipStream_t s)
 {
