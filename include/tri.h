@@ -250,9 +250,11 @@ int tri_int4_quantize(const float *W, int64_t N, int64_t K, int group, int zeros
 /* The 4-bit layer:  Y[m][n] = fp16_rne( residual[m][n] + sum_k W[n][k] X[m][k] ), accumulated in
  * fp32 (codes minus zero points are exact in fp16; a group's sum is scaled in fp32).
  * X: M*K fp16 row-major; Wp: as packed for this N, K, group and zeros; residual: M*N fp16 or
- * NULL (it may be Y itself); Y: M*N fp16.  X, Wp, residual and Y must be 16-byte aligned; any M
- * and K.  X is expected finite.
- * Errors: TRI_EINVAL (a size < 1 or >= 2^31, null, unknown group), TRI_EALIGN, TRI_EHIP. */
+ * NULL (it may be Y itself); Y: M*N fp16.  X, Wp, residual and Y must be 16-byte aligned; any M,
+ * and any N and K that tri_int4_bytes takes.  Y must not alias X or Wp.  X is expected finite (a
+ * row that is not spoils no other row's results).
+ * Errors: TRI_EINVAL (a size < 1, M >= 2^31, N and K past tri_int4_bytes, null, unknown group),
+ * TRI_EALIGN, TRI_EHIP. */
 int tri_int4_linear(const _Float16 *X, const uint8_t *Wp, int64_t M, int64_t N, int64_t K, int group, int zeros,
                     const _Float16 *residual, _Float16 *Y, hipStream_t stream);
 
@@ -294,7 +296,8 @@ int tri_experts_route(const void *logits, int dtype, int64_t T, int E, int topk,
  * int32, not decreasing, at most R (values outside are clamped); rows: R int32; Y: R*N fp16.
  * Rows of Y behind offsets[E] stay as they are, so do rows whose x(r) lies outside 0..T-1.  X,
  * Wp and Y must be 16-byte aligned, the rest 4-byte.  1 <= E <= TRI_MAX_EXPERTS,
- * N < 2^27, K < 2^26; with rows, X of at most 4 GiB - 16.  Y must not alias an input.  X is expected finite.
+ * N < 2^27, K < 2^26; with rows, X of at most 4 GiB - 16.  Y must not alias an input.  X is expected
+ * finite (a row that is not spoils only the places that name it).
  * Errors: TRI_EINVAL (a size < 1 or >= 2^31, null, unknown fmt), TRI_EALIGN, TRI_EHIP. */
 int tri_experts_linear(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,
                        const uint8_t *Wp, const float *scale, int E, int64_t N, int64_t K, int fmt, _Float16 *Y,
@@ -309,7 +312,7 @@ int tri_experts_pair(const _Float16 *X, int64_t T, const int32_t *offsets, const
 
 /* Y[t][n] = fp16_rne( residual[t][n] + sum_j weights[t][j] * Z[pos[t][j]][n] ), added in fp32, j
  * rising; pairs whose pos lies outside 0..R-1 are left out (nothing is read for them).  Z: R*N
- * fp16; pos, weights: T*topk; residual: T*N fp16 or NULL (it may be Y itself); Y: T*N fp16.  Z,
+ * fp16; pos, weights: T*topk; residual: T*N fp16 or NULL (it may be Y itself, no other input may); Y: T*N fp16.  Z,
  * residual and Y must be 16-byte aligned, pos and weights 4-byte.  1 <= topk <= TRI_MAX_TOPK.
  * Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
 int tri_experts_combine(const _Float16 *Z, int64_t R, const int32_t *pos, const float *weights,

@@ -275,6 +275,57 @@ def test_offsets_that_decrease_stay_inside(fmt):
             assert np.all(host(Y)[R:] == 7.0)
 
 
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("name", ["one", "few", "hole", "mixed", "single", "many", "long"])
+@pytest.mark.parametrize("K", [640, 328, 5632, 129])
+def test_rows_that_are_not_finite_spoil_no_other(name, pair, fmt, K):
+    """Tokens of NaN and infinities (padding that was routed all the same): other tokens' results keep every bit."""
+    import torch
+    rng = np.random.default_rng([70, K, fmt, pair])
+    sizes, T, N = RAGGED[name], 9, 100
+    E, R = len(sizes), sum(sizes)
+    rows = rng.integers(0, T, R).astype(np.int32)
+    mats = [(tri.pack(cuda(synth.trits(rng, E * N, K)), fmt).view(E, N, -1), torch.full((E,), 0.05, device="cuda"))
+            for _ in range(2 if pair else 1)]
+    X = rng.standard_normal((T, K)).astype(np.float16)
+    off, rd = cuda(places(sizes)), cuda(rows)
+    args = [a for m in mats for a in m]
+    run = tri.experts_pair if pair else tri.experts_linear
+    want = host(run(cuda(X), off, rd, *args, K, fmt))
+    X[[1, 4]] = rng.choice(np.array([np.nan, np.inf, -np.inf], dtype=np.float16), (2, K))
+    got = host(run(cuda(X), off, rd, *args, K, fmt))
+    bad = (rows == 1) | (rows == 4)
+    np.testing.assert_array_equal(got[~bad].view(np.uint16), want[~bad].view(np.uint16))
+    if not pair:
+        assert not np.any(np.isfinite(got[bad]))
+
+
+def test_experts_of_a_slice():
+    """A rank that holds some of the experts: offsets from its first expert on, its own weights, the places of the others
+    untouched; the slices together give what one call gives."""
+    import torch
+    rng = np.random.default_rng(71)
+    for T in (3, 40, 300):
+        E, topk, K, N = 8, 2, 256, 200
+        r = tri.experts_route(cuda(rng.standard_normal((T, E)).astype(np.float32)), topk)
+        W = tri.pack(cuda(synth.trits(rng, E * N, K)), F2).view(E, N, -1)
+        s = cuda(rng.uniform(0.02, 0.05, E).astype(np.float32))
+        X = cuda(rng.standard_normal((T, K)).astype(np.float16))
+        parts = torch.full((T * topk, N), float("nan"), dtype=torch.float16, device="cuda")
+        off = host(r.offsets)
+        for a, b in ((0, 3), (3, 4), (4, 8)):
+            before = host(parts)
+            tri.experts_linear(X, r.offsets[a:b + 1], r.rows, W[a:b], s[a:b], K, F2, out=parts)
+            after, own = host(parts), np.zeros(T * topk, dtype=bool)
+            own[off[a]:off[b]] = True
+            np.testing.assert_array_equal(after[~own].view(np.uint16), before[~own].view(np.uint16))
+        want = host(tri.experts_linear(X, r.offsets, r.rows, W, s, K, F2)).astype(np.float64)
+        # two kernels' results: twice the bound of one
+        d = sum_bound(K, float(s.max()), host(X)[host(r.rows)].astype(np.float64))
+        assert np.all(np.abs(host(parts) - want) <= 2 * (d + 2.0 ** -11 * np.abs(want) + 2.0 ** -25))
+
+
 @pytest.mark.parametrize("K", [8, 5])
 def test_the_most_places_that_one_expert_may_own(K):
     """2^31 - 1 places of one expert out of three: the last tile's bounds stay below 2^31, nothing is lost (small integers:

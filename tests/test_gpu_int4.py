@@ -196,6 +196,22 @@ def test_extreme_values(M):
     assert np.all(np.abs(Y[fits].astype(np.float64) - ref[fits]) <= tol[fits])
 
 
+@pytest.mark.parametrize("M,N", [(2, 300), (4, 300), (7, 300), (16, 300), (40, 300), (40, 20500), (70, 20500)])
+@pytest.mark.parametrize("K", [256, 264, 129])
+def test_rows_that_are_not_finite_spoil_no_other(M, N, K):
+    """A padded batch whose padding holds NaN and infinities: the other rows' results keep every bit."""
+    rng = np.random.default_rng([50, M, N, K])
+    Q, S, Z = matrix(rng, N, K, 64, True)
+    Wp = tri.int4_pack(cuda(Q), cuda(S), 64, cuda(Z))
+    X = rng.standard_normal((M, K)).astype(np.float16)
+    want = host(tri.int4_linear(cuda(X), Wp, N, 64, True))
+    bad = np.arange(M) % 3 == 1
+    X[bad] = rng.choice(np.array([np.nan, np.inf, -np.inf], dtype=np.float16), (int(bad.sum()), K))
+    got = host(tri.int4_linear(cuda(X), Wp, N, 64, True))
+    np.testing.assert_array_equal(got[~bad].view(np.uint16), want[~bad].view(np.uint16))
+    assert not np.any(np.isfinite(got[bad]))
+
+
 @pytest.mark.parametrize("M", [1, 7, 40])
 def test_weights_past_four_gigabytes(M):
     """The last blocks of the largest matrix, whose scales lie past 4 GiB, give what they give alone."""
