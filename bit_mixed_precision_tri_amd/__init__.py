@@ -598,6 +598,7 @@ def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None
     experts_linear take them, logits (T, E) as experts_route takes them.  Four launches or a few more, no waiting."""
     torch = _torch or _load_torch()
     (T, hidden), inner = X.shape, gate[0].shape[1]
+    _need(logits.dim() == 2 and logits.shape[0] == T, "logits must have a row for every row of X")
     r = experts_route(logits, topk, renorm=renorm, stream=stream)
     H = torch.empty((T * topk, inner), dtype=torch.float16, device=X.device)
     Z = torch.empty((T * topk, down[0].shape[1]), dtype=torch.float16, device=X.device)

@@ -607,3 +607,13 @@ def test_refusals_of_the_helpers():
                 lambda: tri.experts_combine(x, rows.view(1, 5), torch.zeros((1, 5), **f), out=torch.zeros((2, 64), **h))]:
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("T", [3, 5])
+def test_a_block_refuses_logits_of_other_tokens(T):
+    import torch
+    rng = np.random.default_rng(72)
+    _, mats = mixed_block(rng, 4, 8, 2, 256, 384, F2)
+    X = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        tri.experts_mlp(X, torch.zeros((T, 8), device="cuda"), 2, *mats, F2)
