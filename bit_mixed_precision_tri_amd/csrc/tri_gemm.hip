@@ -329,73 +329,81 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
         return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(abuf_of(buf)) + aadr[s] +
                                                 16 * 32 * PR * mt);
     };
-    u32x4 afr[kMTt], bop[kNT];
+    // The whole row with MT of the 32-row tiles (the rest of acc stays zero).
+    auto sweep = [&](auto mt_tag) __attribute__((always_inline)) {
+        constexpr int MT = decltype(mt_tag)::value;
+        u32x4 afr[MT], bop[kNT];
 #pragma unroll
-    for (int mt = 0; mt < kMTt; ++mt) afr[mt] = read_a(0, 0, mt);
+        for (int mt = 0; mt < MT; ++mt) afr[mt] = read_a(0, 0, mt);
 #pragma unroll
-    for (int nt = 0; nt < kNT; ++nt) bop[nt] = decode(w0, 0, nt);
+        for (int nt = 0; nt < kNT; ++nt) bop[nt] = decode(w0, 0, nt);
 
-    // One K tile: wc holds its weights, wx those of the next tile.  MORE (compile-time, so the
-    // tile body has no branches) says whether a next tile exists.
-    auto tile = [&](int kt, auto more_tag, auto buf_tag, u32x4 (&wc)[kNT], u32x4 (&wx)[kNT]) __attribute__((always_inline)) {
-        constexpr bool MORE = decltype(more_tag)::value;
-        constexpr int buf = decltype(buf_tag)::value;
+        // One K tile: wc holds its weights, wx those of the next tile.  MORE (compile-time, so the
+        // tile body has no branches) says whether a next tile exists.
+        auto tile = [&](int kt, auto more_tag, auto buf_tag, u32x4 (&wc)[kNT], u32x4 (&wx)[kNT]) __attribute__((always_inline)) {
+            constexpr bool MORE = decltype(more_tag)::value;
+            constexpr int buf = decltype(buf_tag)::value;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            if (MORE && s == KS - 1) {
-                // this wave's share of the next tile's activations is in (only the weight
-                // loads issued after it may still be in flight) and its reads of this tile are
-                // done; after the barrier, every wave's are
-                __builtin_amdgcn_s_waitcnt(0x0070 | kNT);   // vmcnt(kNT) lgkmcnt(0)
-                __syncthreads();
-            }
-            u32x4 an[kMTt], bn[kNT];
-            if (s + 1 < KS) {
+            for (int s = 0; s < KS; ++s) {
+                if (MORE && s == KS - 1) {
+                    // this wave's share of the next tile's activations is in (only the weight
+                    // loads issued after it may still be in flight) and its reads of this tile are
+                    // done; after the barrier, every wave's are
+                    __builtin_amdgcn_s_waitcnt(0x0070 | kNT);   // vmcnt(kNT) lgkmcnt(0)
+                    __syncthreads();
+                }
+                u32x4 an[MT], bn[kNT];
+                if (s + 1 < KS) {
 #pragma unroll
-                for (int mt = 0; mt < kMTt; ++mt) an[mt] = read_a(buf, s + 1, mt);
+                    for (int mt = 0; mt < MT; ++mt) an[mt] = read_a(buf, s + 1, mt);
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) bn[nt] = decode(wc, s + 1, nt);
-            } else if (MORE) {
+                    for (int nt = 0; nt < kNT; ++nt) bn[nt] = decode(wc, s + 1, nt);
+                } else if (MORE) {
 #pragma unroll
-                for (int mt = 0; mt < kMTt; ++mt) an[mt] = read_a(buf ^ 1, 0, mt);
-                take_codes(wx);                  // the last decode of this tile's stream was at step KS - 2
+                    for (int mt = 0; mt < MT; ++mt) an[mt] = read_a(buf ^ 1, 0, mt);
+                    take_codes(wx);                  // the last decode of this tile's stream was at step KS - 2
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) bn[nt] = decode(wx, 0, nt);
-            }
+                    for (int nt = 0; nt < kNT; ++nt) bn[nt] = decode(wx, 0, nt);
+                }
 #pragma unroll
-            for (int mt = 0; mt < kMTt; ++mt)
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) acc[mt][nt] = mfma32(afr[mt], bop[nt], acc[mt][nt]);
-            // interleave: each MFMA is followed by a share of the next step's decode and reads
+                    for (int nt = 0; nt < kNT; ++nt) acc[mt][nt] = mfma32(afr[mt], bop[nt], acc[mt][nt]);
+                // interleave: each MFMA is followed by a share of the next step's decode and reads
 #pragma unroll
-            for (int i = 0; i < kMTt * kNT; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // 1 MFMA
-                __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);   // 3 VALU
-                if (i % 4 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // 1 LDS read
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            if (MORE && s == KS - 1) {
-                // this tile's buffer and weight registers are free: the tile after next
-                load_a(kt + 2, buf);
+                for (int i = 0; i < MT * kNT; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // 1 MFMA
+                    __builtin_amdgcn_sched_group_barrier(0x002, 3 * kMTt / MT, 0);   // 3 VALU (or as many more)
+                    if (i % 4 == 0) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // 1 LDS read
+                }
                 __builtin_amdgcn_sched_barrier(0);
-                load_b(kt + 2, wc);
-            }
-            if (s + 1 < KS || MORE) {
+                if (MORE && s == KS - 1) {
+                    // this tile's buffer and weight registers are free: the tile after next
+                    load_a(kt + 2, buf);
+                    __builtin_amdgcn_sched_barrier(0);
+                    load_b(kt + 2, wc);
+                }
+                if (s + 1 < KS || MORE) {
 #pragma unroll
-                for (int mt = 0; mt < kMTt; ++mt) afr[mt] = an[mt];
+                    for (int mt = 0; mt < MT; ++mt) afr[mt] = an[mt];
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) bop[nt] = bn[nt];
+                    for (int nt = 0; nt < kNT; ++nt) bop[nt] = bn[nt];
+                }
             }
+        };
+        // An even number of tiles keeps a single code path: an odd count gets one more tile past
+        // the end, whose activations read as zero, so it adds exact zeros.
+        for (int kt = 0; kt + 2 < KTe; kt += 2) {
+            tile(kt, std::true_type{}, std::integral_constant<int, 0>{}, w0, w1);
+            tile(kt + 1, std::true_type{}, std::integral_constant<int, 1>{}, w1, w0);
         }
+        tile(KTe - 2, std::true_type{}, std::integral_constant<int, 0>{}, w0, w1);
+        tile(KTe - 1, std::false_type{}, std::integral_constant<int, 1>{}, w1, w0);
     };
-    // An even number of tiles keeps a single code path: an odd count gets one more tile past
-    // the end, whose activations read as zero, so it adds exact zeros.
-    for (int kt = 0; kt + 2 < KTe; kt += 2) {
-        tile(kt, std::true_type{}, std::integral_constant<int, 0>{}, w0, w1);
-        tile(kt + 1, std::true_type{}, std::integral_constant<int, 1>{}, w1, w0);
-    }
-    tile(KTe - 2, std::true_type{}, std::integral_constant<int, 0>{}, w0, w1);
-    tile(KTe - 1, std::false_type{}, std::integral_constant<int, 1>{}, w1, w0);
+    // (An expert's last tile may need half the products: 333 tokens, 6 of 64 experts, 2048 -> 1408, 1.6-bit, about 31 rows
+    // per expert: 72 -> 64 us; with 700 to 2048 tokens 1 - 5%.)
+    if (EXP && et.rows <= 32) sweep(std::integral_constant<int, 1>{});
+    else sweep(std::integral_constant<int, kMTt>{});
     wait_vm<0>();                                // (the last tile's loads to LDS, past the end, are in)
 
     // epilogue: lane (h, c) holds rows 32mt + 8i + 4h + v of column 32nt + c
@@ -536,7 +544,7 @@ bool experts_gemm_fits(const Experts &ex, int fmt)
 // Tiles of 64 places, whatever the sizes: several such workgroups share a CU, the last tile of an expert wastes little,
 // and 128-place tiles lost at every measured size (pair, 2-bit, 4096 -> 11008, eight experts, two per token: 256 tokens
 // 150 against 202 us, 2048 tokens 655 against 654 (256 columns) and 727 us (512); 1.6-bit 798 against 828 - 1029; with the
-// gate as it is now the 64-place tiles take 612 and 730).  Two column tiles per wave for a pair; for one matrix one, or
+// gate as it is now the 64-place tiles take 608 and 675).  Two column tiles per wave for a pair; for one matrix one, or
 // two for 2-bit digits where those still make two rounds (11008 -> 4096, 2048 tokens 369 -> 332 us, 256 tokens 82 -> 85
 // us; 1.6-bit 421 -> 422 us, 256 tokens 101 -> 122 us).
 template <int FMT>
