@@ -99,6 +99,38 @@ __device__ __forceinline__ void base3_digits_u16x2(uint32_t b, uint32_t (&d)[5])
     d[4] = __builtin_bit_cast(uint32_t, q4);
 }
 
+// The same digits at bits 10 and 11 of each lane, where they read as the NORMAL fp16 value d * 2^-14.  A matrix instruction
+// aligns its products by the operands' exponents: those of a subnormal count as 2^-14 however small it is, so sums over
+// digits d * 2^-24 lose ten bits, always to the same side (measured on 11008 values: 7e-5 of the result against 1e-7 here).
+// d_j 2^10 = q_j 2^10 - 3 q_{j+1} 2^10 holds modulo 2^16, so that only the low six bits of a quotient matter: a product
+// with twice the multiplier has them in its top bits.  Two operations more than the digits above.
+__device__ __forceinline__ void base3_digits_normal(uint32_t b, uint32_t (&d)[5])
+{
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const u16x2 v = __builtin_bit_cast(u16x2, b);
+    const u16x2 top = {0xFC00, 0xFC00}, two = {0x0C00, 0x0C00};
+    const u16x2 q0 = v << (uint16_t)10;
+    const u16x2 q1 = (v * (uint16_t)342) & top;
+    const u16x2 q2 = (v * (uint16_t)114) & top;
+    const u16x2 q3 = (v * (uint16_t)38) & top;
+    const u16x2 q4 = ((v * (uint16_t)203) >> (uint16_t)4) & two;
+    d[0] = __builtin_bit_cast(uint32_t, (u16x2)(q0 - q1 * (uint16_t)3));
+    d[1] = __builtin_bit_cast(uint32_t, (u16x2)(q1 - q2 * (uint16_t)3));
+    d[2] = __builtin_bit_cast(uint32_t, (u16x2)(q2 - q3 * (uint16_t)3));
+    d[3] = __builtin_bit_cast(uint32_t, (u16x2)(q3 - q4 * (uint16_t)3));
+    d[4] = __builtin_bit_cast(uint32_t, q4);
+}
+
+// 2-bit digits of four words at position p (0..7, a constant) of their 16-bit halves: odd positions at bits 10 and 11
+// (d * 2^-14, normal), even ones at bits 8 and 9 (d * 2^-16: two of the ten bits that subnormals can lose).  Three shifts
+// serve a word's eight positions.
+__device__ __forceinline__ u32x4 digits_2bit(const u32x4 v, int p)
+{
+    const int at = p % 2 ? 10 : 8, by = at - 2 * p;
+    const u32x4 u = by >= 0 ? v << (uint32_t)(by & 31) : v >> (uint32_t)(-by & 31);
+    return u & (0x00030003u << at);
+}
+
 // The quotients q_j = floor(b / 3^j), j = 0..4, of two bytes at once (q_0 = b), by the same
 // multiply-shifts.  Since d_j = q_j - 3 q_{j+1} (q_5 = 0), a dot product with the digits is
 //   sum_j x_j d_j = sum_j x_j q_j - 3 sum_{j<4} x_j q_{j+1},

@@ -282,8 +282,8 @@ __device__ __forceinline__ float4_t mfma(const u32x4 a, const u32x4 b, float4_t 
 // serves rows that are no whole 16-byte pieces or too long for the kernel after it.
 //
 // The eight waves split the row; wave w takes the chunk-steps w, w + 8, ..., where lane (g = lane/16, j = lane%16) reads
-// 16-byte chunk 4 s + g of weight row j and decodes it to digits d = t + 1 in place, as exact fp16 values
-// d * 2^-24 (2-bit: masked, d * 4^p * 2^-24 at position p of a 16-bit half; 1.6-bit: multiply-shift quotients).  One
+// 16-byte chunk 4 s + g of weight row j and decodes it to digits d = t + 1 in place, as exact fp16 values d * 2^-14 (2-bit:
+// shifted and masked, d * 2^-16 at even positions of a 16-bit half; 1.6-bit: multiply-shift quotients).  One
 // v_mfma_f32_16x16x32_f16 per position p contracts them; sum_k x, from products with ones, is taken off at the end.
 //
 // A operands.  A product's 8 values per lane are strided over the chunk (2-bit: 16 v + p and 16 v + 8 + p; 1.6-bit:
@@ -307,8 +307,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     constexpr int NLD = (MA * PR + 63) / 64;
     constexpr int ROW = 4 * XH + 8;              // values of a row's place in LDS (16 bytes more than a step: banks)
     constexpr int kAhead = 2;
-    // accumulators: one per product of an A operand and scale of its digits
-    constexpr int NACC = MA == 16 ? (TWO ? 6 : 2) : (TWO ? 8 : CL);
+    constexpr int NACC = MA == 16 ? 2 : CL;      // accumulators: one per product of an A operand, two at least
     __shared__ __attribute__((aligned(16))) uint16_t xs[NW][MA][ROW];
     __shared__ float red[NW][MA][16 * NM + 1];
 
@@ -379,20 +378,18 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
     auto contract = [&](const u32x4 (&a)[MA == 16 ? NOP : NSET], const u32x4 v, float4_t (&ac)[NACC]) __attribute__((always_inline)) {
         auto A = [&](int op) -> const u32x4 & { return a[MA == 16 ? op : op / CL]; };
         if constexpr (TWO) {
-            const u32x4 u = v >> 12u;
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const u32x4 b = p < 6 ? v & (0x00030003u << (2 * p)) : u & (0x00030003u << (2 * (p - 6)));
-                const int c = MA == 16 && p >= 6 ? p - 6 : p;
-                ac[c] = mfma(A(p), b, ac[c]);
+            for (int i = 0; i < 8; ++i) {
+                const int p = i ^ 4;             // (positions 4 and 5 need no shift)
+                ac[p % NACC] = mfma(A(p), digits_2bit(v, p), ac[p % NACC]);
             }
         } else {
             uint32_t d[8][5];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) base3_digits_u16x2(byte_pair(v, q), d[q]);
+            for (int q = 0; q < 8; ++q) base3_digits_normal(byte_pair(v, q), d[q]);
 #pragma unroll
             for (int op = 0; op < 10; ++op) {
-                const int p = op / 2, q = 4 * (op % 2), c = MA == 16 ? op % 2 : op % CL;
+                const int p = op / 2, q = 4 * (op % 2), c = op % NACC;
                 ac[c] = mfma(A(op), u32x4{d[q][p], d[q + 1][p], d[q + 2][p], d[q + 3][p]}, ac[c]);
             }
         }
@@ -469,7 +466,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 
     // Merge: product op's rows of result r lie in A rows MA c + a, c = op % CL: lane group (MA c + a) / 4, element
     // (MA c + a) % 4.  Lanes take what is theirs, and the lane groups that hold the same row are added.
-    auto unit = [&](int p) { return TWO ? 1.f / (float)(1 << (2 * (p < 6 ? p : p - 6))) : 1.f; };
+    auto unit = [&](int c) { return TWO && c % 2 == 0 ? 4.f : 1.f; };   // (2-bit digits of even positions: 2^-16)
     auto put = [&](int col, float (&v)[4], bool leader) __attribute__((always_inline)) {   // v[e]: this lane's rows
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -501,8 +498,8 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 #pragma unroll
             for (int p = 0; p < NM; ++p) sd[p] += red[q][m][16 * p + c];
         }
-        float y = (sd[0] * 16777216.0f - sx) * ex.scale[0][et.e];
-        if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16777216.0f - sx) * ex.scale[1][et.e]);
+        float y = (sd[0] * 16384.f - sx) * ex.scale[0][et.e];
+        if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sx) * ex.scale[1][et.e]);
         ex.Y[(int64_t)(et.r0 + m) * N + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)y);
     }
 }
@@ -513,10 +510,11 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 // contracted; the waves' partial sums meet in one of two LDS buffers in turn, so a block costs one barrier.
 //
 // Measured on eight experts, two per token: gate and up 4096 -> 11008 of one token (45 MB of 2-bit weights) 13.1 us, where
-// a plain read takes 7.6; of 16 tokens (180 MB) 45 us against 28; down 11008 -> 4096 of 16 tokens, 1.6-bit (72 MB) 35 us
-// against 12.  What bounds it is the vector ALU (about 19 of 44 us at 16 tokens, the matrix cores another 9, hardly
+// a plain read takes 7.6; of 16 tokens (180 MB) 43 us against 28; down 11008 -> 4096 of 16 tokens, 1.6-bit (72 MB) 36 us
+// against 12.  What bounds it is the vector ALU (about 19 of 43 us at 16 tokens, the matrix cores another 9, hardly
 // overlapped) and the waits around a block's barrier; splitting the waves by outputs instead, with all of the row per
-// wave and no barrier, was slower (59 us), as were deeper loads (48 us).
+// wave and no barrier, was slower (59 us), as were deeper loads (48 us).  Digits as subnormals d * 2^-24 would save the
+// 1.6-bit products 4 - 8% (down 34 us) and the 2-bit ones nothing, at the price of ten bits of every sum.
 constexpr int kHeld = 16;                        // blocks whose results wait in LDS
 // Whether the loop's registers for A operands and for D blocks' chunks leave the rest of its code enough of 128 registers
 // (two workgroups per CU) that the compiler spills nothing, or next to nothing; limits as found by compiling.
@@ -556,8 +554,7 @@ __global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int 
     constexpr int PR = 4 * XH / 8;               // 16-byte pieces of a row per step
     constexpr int NLD = (MA * PR + 63) / 64;
     constexpr int ROW = 4 * XH + 8;              // values of a row's place in LDS (16 bytes more than a step: banks)
-    // accumulators by (product's place in the A operand, scale of its digits)
-    constexpr int NACC = TWO ? (MA >= 8 ? 6 : 8) : (MA == 16 ? 2 : CL);
+    constexpr int NACC = MA == 16 ? 2 : CL;      // accumulators: one per product of an A operand, two at least
     // (the activations' passage and, after it, the partial sums use the same LDS)
     constexpr int XS = NW * MA * ROW * 2, RED = 2 * NW * MA * (16 * NM + 1) * 4;
     __shared__ u32x4 smem[((XS > RED ? XS : RED) + 15) / 16];
@@ -712,26 +709,23 @@ __global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int 
     auto contract = [&](const u32x4 (&x)[NA], const u32x4 v, float4_t (&ac)[NACC]) __attribute__((always_inline)) {
         auto A = [&](int op) -> const u32x4 & { return x[MA == 16 ? op : op / CL]; };
         if constexpr (TWO) {
-            const u32x4 u = v >> 12u;
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                const u32x4 d = p < 6 ? v & (0x00030003u << (2 * p)) : u & (0x00030003u << (2 * (p - 6)));
-                const int c = NACC == 6 && p >= 6 ? p - 6 : p;
-                ac[c] = mfma(A(p), d, ac[c]);
+            for (int i = 0; i < 8; ++i) {
+                const int p = i ^ 4;             // (positions 4 and 5 need no shift)
+                ac[p % NACC] = mfma(A(p), digits_2bit(v, p), ac[p % NACC]);
             }
         } else {
             uint32_t d[8][5];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) base3_digits_u16x2(byte_pair(v, q), d[q]);
+            for (int q = 0; q < 8; ++q) base3_digits_normal(byte_pair(v, q), d[q]);
 #pragma unroll
             for (int op = 0; op < 10; ++op) {
-                const int p = op / 2, q = 4 * (op % 2), c = MA == 16 ? op % 2 : op % CL;
+                const int p = op / 2, q = 4 * (op % 2), c = op % NACC;
                 ac[c] = mfma(A(op), u32x4{d[q][p], d[q + 1][p], d[q + 2][p], d[q + 3][p]}, ac[c]);
             }
         }
     };
-    // scale of accumulator c's digits
-    auto unit = [&](int c) { return TWO ? 1.f / (float)(1 << (2 * (c < 6 ? c : c - 6))) : 1.f; };
+    auto unit = [&](int c) { return TWO && c % 2 == 0 ? 4.f : 1.f; };   // (2-bit digits of even positions: 2^-16)
     auto run = [&](const u32x4 (&wc)[NM][CST], int buf, int held) __attribute__((always_inline)) {
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
@@ -778,8 +772,8 @@ __global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int 
             for (int q = 0; q < NW; ++q)
 #pragma unroll
                 for (int p = 0; p < NM; ++p) sd[p] += red[buf][q][m][16 * p + c];
-            float y = (sd[0] * 16777216.0f - sxt[m]) * scale[0];
-            if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16777216.0f - sxt[m]) * scale[NM - 1]);
+            float y = (sd[0] * 16384.f - sxt[m]) * scale[0];
+            if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sxt[m]) * scale[NM - 1]);
             done[held][m][c] = __builtin_bit_cast(uint16_t, (_Float16)y);
         }
     };
@@ -960,7 +954,7 @@ bool loop_cst(const Experts &ex, hipStream_t s)
 //                                4: - / 45.5 / 43.4 / 69.8,  16: - / 96.4 / 60.1 / 74.3,  32: - / 156 / 87 / 118
 //   down, 11008 -> 4096          R/E = 1: 19.4 / 23.0 / - / 45.3,  4: - / 29.5 / - / 53.8,  16: - / 58.7 / - / 66.3,
 //                                24: - / 77.0 / - / 67.5
-// (MA = 4 won nowhere by more than 3%.)
+// (MA = 4 won nowhere by more than 3%.  Taken with digits as subnormals: the loop's times are now 4% less to 4% more.)
 template <int FMT, bool PAIR>
 bool loop_ma(const Experts &ex, hipStream_t s)
 {

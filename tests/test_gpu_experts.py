@@ -617,3 +617,38 @@ def test_a_block_refuses_logits_of_other_tokens(T):
     X = torch.zeros((4, 256), dtype=torch.float16, device="cuda")
     with pytest.raises(ValueError):
         tri.experts_mlp(X, torch.zeros((T, 8), device="cuda"), 2, *mats, F2)
+
+
+SUMS = {"one place": [0, 1, 0, 0, 0, 0, 1, 0, 0], "three places": [2, 1], "eight places": [3, 5], "seventy places": [30, 40],
+        "many places": [200]}
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("name", list(SUMS))
+@pytest.mark.parametrize("K", [256, 1001, 4096, 11008, 28672])
+def test_sums_are_those_of_fp32(K, name, fmt):
+    """How far the sums are off before they are rounded, over all outputs at once (the bound of single outputs above lets
+    every rounding fall the same way).  A sum that is off by d moves a result to a neighbouring fp16 value with probability
+    d / step, so the mean distance from the correctly rounded results, in steps, is the mean of d / step.  d by the model of
+    independent roundings: 80 + K/16 additions, each off by at most 2^-23 of a partial sum of digits t + 1, whose size is the
+    root of sum_k (t+1)^2 x^2; twice its root mean square, 2 sqrt(80 + K/16) 2^-23 of that.  Results below 1/16 of their root
+    mean square (6%) are left out, their steps are too fine; 1/200 is added for chance, four deviations of 8000 results'
+    share at 1%."""
+    rng = np.random.default_rng([73, K, fmt, list(SUMS).index(name)])
+    sizes, N = SUMS[name], 4000
+    E, R = len(sizes), sum(sizes)
+    X = rng.standard_normal((R, K)).astype(np.float16)
+    W = synth.trits(rng, N, K)
+    mats = tri.pack(cuda(W), fmt).expand(E, N, -1).contiguous()
+    say("sums K=%d fmt=%d %s" % (K, fmt, name))
+    Y = host(tri.experts_linear(cuda(X), cuda(places(sizes)), None, mats, cuda(np.full(E, 1 / 64, np.float32)), K, fmt))
+    x = X.astype(np.float64)
+    ref = x @ W.astype(np.float64).T / 64
+    size = np.sqrt((x * x) @ ((W + 1.0) ** 2).T) / 64
+    near = ref.astype(np.float16)
+    step = np.spacing(np.abs(near)).astype(np.float64)
+    live = np.abs(ref) > np.sqrt(np.mean(ref * ref)) / 16
+    off = np.abs(Y.astype(np.float64) - near.astype(np.float64)) / step
+    d = 2 * np.sqrt(80 + K / 16) * 2.0 ** -23 * size
+    say("  mean distance %.5f steps, %.5f allowed" % (off[live].mean(), (d / step)[live].mean() + 0.005))
+    assert off[live].mean() <= (d / step)[live].mean() + 0.005
