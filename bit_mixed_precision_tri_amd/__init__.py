@@ -338,8 +338,9 @@ def linear(X, Wp, scale, K, fmt, algo=TRI_ALGO_AUTO, out=None, stream=None):
     return Y
 
 
-# The helpers below take the tensors' device (whichever device is current) and its current stream, or `stream`; they
-# raise ValueError for tensors of another type, shape, device or layout than they name.
+# The helpers below take the tensors' device (whichever device is current) and its current stream, or `stream` (ordering
+# that stream behind what writes their inputs, and whoever reads their results behind it, is the caller's); they raise
+# ValueError for tensors of another type, shape, device or layout than they name.
 
 _torch = None
 
@@ -383,11 +384,20 @@ def _tensors(device, dtype, **named):
             raise ValueError("%s must be a contiguous %s tensor on device %d" % (name, dtype, device))
 
 
-def _keep(t, stream):
-    """Tell torch's allocator that `t`, allocated here on the current stream, is used on a stream that the caller named."""
-    if stream is not None:
-        h = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-        t.record_stream(_torch.cuda.ExternalStream(h, device=t.device))
+def _new(shape, dtype, device, stream, result=True):
+    """An uninitialised tensor for a call on `stream`.  A stream that the caller named writes it without waiting for the
+    current one, so its memory comes from that stream's own pool: the current stream's pool hands out memory that kernels
+    queued there may still use.  A result is not reused, either, before the current stream is done with it, where the
+    caller reads it after the two were ordered."""
+    torch = _torch
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if handle is None or handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 @functools.lru_cache(maxsize=4096)
@@ -417,10 +427,9 @@ def int4_pack(Q, S, group, Z=None, stream=None):
     _need(nbytes > 0, "group must be 32, 64 or 128 (and the matrix below 2^22 tiles)")
     shape = (N, -(-K // group))
     _need(S.shape == shape and (Z is None or Z.shape == shape), "S and Z must be (N, ceil(K/group))")
-    Wp = torch.empty(nbytes, dtype=torch.uint8, device=Q.device)
+    Wp = _new(nbytes, torch.uint8, Q.device, stream)
     _launch("tri_int4_pack", dev, stream, Q.data_ptr(), S.data_ptr(), None if Z is None else Z.data_ptr(), N, K, group,
             Wp.data_ptr())
-    _keep(Wp, stream)
     return Wp
 
 
@@ -433,13 +442,11 @@ def int4_unpack(Wp, N, K, group, zeros=False, stream=None):
     nbytes = tri_int4_bytes(N, K, group, zeros)
     _need(nbytes > 0 and Wp.numel() == nbytes, "Wp does not hold tri_int4_bytes(N, K, group, zeros) bytes")
     shape = (N, -(-K // group))
-    Q = torch.empty((N, K), dtype=torch.uint8, device=Wp.device)
-    S = torch.empty(shape, dtype=torch.float16, device=Wp.device)
-    Z = torch.empty(shape, dtype=torch.uint8, device=Wp.device) if zeros else None
+    Q = _new((N, K), torch.uint8, Wp.device, stream)
+    S = _new(shape, torch.float16, Wp.device, stream)
+    Z = _new(shape, torch.uint8, Wp.device, stream) if zeros else None
     _launch("tri_int4_unpack", dev, stream, Wp.data_ptr(), N, K, group, 1 if zeros else 0, Q.data_ptr(), S.data_ptr(),
             None if Z is None else Z.data_ptr())
-    for made in (Q, S) if Z is None else (Q, S, Z):
-        _keep(made, stream)
     return Q, S, Z
 
 
@@ -451,9 +458,8 @@ def int4_quantize(W, group, zeros=False, stream=None):
     _tensors(dev, torch.float32, W=W)
     nbytes = tri_int4_bytes(N, K, group, zeros)
     _need(nbytes > 0, "group must be 32, 64 or 128 (and the matrix below 2^22 tiles)")
-    Wp = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
+    Wp = _new(nbytes, torch.uint8, W.device, stream)
     _launch("tri_int4_quantize", dev, stream, W.data_ptr(), N, K, group, 1 if zeros else 0, Wp.data_ptr())
-    _keep(Wp, stream)
     return Wp
 
 
@@ -469,7 +475,7 @@ def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=No
             Wp.numel() == _int4_nbytes(N, K, group, zeros)):
         raise ValueError("Wp must be a contiguous uint8 tensor on X's device of tri_int4_bytes(N, K, group, zeros) bytes for "
                          "X's width")
-    Y = torch.empty((M, N), dtype=half, device=X.device) if out is None else out
+    Y = _new((M, N), half, X.device, stream) if out is None else out
     res = None
     if residual is not None:
         _need(residual.shape == (M, N) and _plain(residual, half, dev),
@@ -479,8 +485,6 @@ def int4_linear(X, Wp, N, group, zeros=False, residual=None, out=None, stream=No
         raise ValueError("out must be a contiguous (M, N) float16 tensor on X's device")
     _launch("tri_int4_linear", dev, stream, X.data_ptr(), Wp.data_ptr(), M, N, K, group, 1 if zeros else 0, res,
             Y.data_ptr())
-    if out is None:
-        _keep(Y, stream)
     return Y
 
 
@@ -499,19 +503,17 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     T, E = shape
     need = _route_nbytes(T, E, topk)
     _need(need >= 0, "1 <= E <= %d, 1 <= topk <= min(E, %d) and T * topk < 2^31 are taken" % (TRI_MAX_EXPERTS, TRI_MAX_TOPK))
-    i32, mine = torch.int32, out is None
-    if mine:
-        kw = dict(dtype=i32, device=logits.device)
-        out = Routing(torch.empty((T, topk), **kw), torch.empty((T, topk), dtype=torch.float32, device=logits.device),
-                      torch.empty(E + 1, **kw), torch.empty(T * topk, **kw), torch.empty((T, topk), **kw))
+    i32 = torch.int32
+    if out is None:
+        out = Routing(*(_new(sh, torch.float32 if i == 1 else i32, logits.device, stream)
+                        for i, sh in enumerate(((T, topk), (T, topk), (E + 1,), (T * topk,), (T, topk)))))
     ids, weights, offsets, rows, pos = out
     _need(_plain(ids, i32, dev) and _plain(weights, torch.float32, dev) and _plain(offsets, i32, dev) and
           _plain(rows, i32, dev) and _plain(pos, i32, dev) and ids.shape == weights.shape == pos.shape == (T, topk) and
           offsets.shape == (E + 1,) and rows.shape == (T * topk,),
           "out: ids, weights, pos (T, topk), offsets (E + 1), rows (T * topk); int32, the weights float32")
-    temporary = workspace is None and need > 0
-    if temporary:
-        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device)
+    if workspace is None and need > 0:
+        workspace = _new(need, torch.uint8, logits.device, stream, result=False)
     ws, nbytes = None, 0
     if workspace is not None:
         _need(_plain(workspace, torch.uint8, dev), "workspace must be a contiguous uint8 tensor on the logits' device")
@@ -519,9 +521,6 @@ def experts_route(logits, topk, renorm=True, workspace=None, out=None, stream=No
     _launch("tri_experts_route", dev, stream, logits.data_ptr(), TRI_F16 if dtype is torch.float16 else TRI_F32, T, E, topk,
             1 if renorm else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(), ws,
             nbytes)
-    if stream is not None:
-        for made in (out if mine else ()) + ((workspace,) if temporary else ()):
-            _keep(made, stream)
     return out
 
 
@@ -538,7 +537,7 @@ def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
     if rows is not None:
         _need(_plain(rows, i32, dev) and rows.dim() == 1, "rows must be a contiguous one-dimensional int32 tensor on X's device")
         R, rp = rows.shape[0], rows.data_ptr()
-    Y = out if out is not None else torch.empty((R, N), dtype=half, device=X.device)
+    Y = out if out is not None else _new((R, N), half, X.device, stream)
     _need(_plain(Y, half, dev) and Y.dim() == 2 and Y.shape[0] >= R and Y.shape[1] == N,
           "out must be a contiguous (R, N) float16 tensor on X's device")
     args = []
@@ -547,8 +546,6 @@ def _experts(name, X, offsets, rows, mats, K, fmt, out, stream):
               "weights must be contiguous (E, N, tri_row_bytes(K, fmt)) uint8 tensors, scales (E) float32, on X's device")
         args += [W.data_ptr(), scale.data_ptr()]
     _launch(name, dev, stream, X.data_ptr(), T, offsets.data_ptr(), rp, R, *args, E, N, K, fmt, Y.data_ptr())
-    if out is None:
-        _keep(Y, stream)
     return Y
 
 
@@ -576,7 +573,7 @@ def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
             weights.is_contiguous()):
         raise ValueError("pos must be a contiguous (T, topk) int32 tensor on Z's device, weights a float32 one like it")
     (R, N), (T, topk) = shape, pshape
-    Y = torch.empty((T, N), dtype=half, device=Z.device) if out is None else out
+    Y = _new((T, N), half, Z.device, stream) if out is None else out
     res = None
     if residual is not None:
         if not (residual.shape == (T, N) and residual.dtype is half and residual.get_device() == dev and
@@ -587,8 +584,6 @@ def experts_combine(Z, pos, weights, residual=None, out=None, stream=None):
         raise ValueError("out must be a contiguous (T, N) float16 tensor on Z's device")
     _launch("tri_experts_combine", dev, stream, Z.data_ptr(), R, pos.data_ptr(), weights.data_ptr(), res, T, topk, N,
             Y.data_ptr())
-    if out is None:
-        _keep(Y, stream)
     return Y
 
 
@@ -600,11 +595,8 @@ def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None
     (T, hidden), inner = X.shape, gate[0].shape[1]
     _need(logits.dim() == 2 and logits.shape[0] == T, "logits must have a row for every row of X")
     r = experts_route(logits, topk, renorm=renorm, stream=stream)
-    H = torch.empty((T * topk, inner), dtype=torch.float16, device=X.device)
-    Z = torch.empty((T * topk, down[0].shape[1]), dtype=torch.float16, device=X.device)
+    H = _new((T * topk, inner), torch.float16, X.device, stream, result=False)
+    Z = _new((T * topk, down[0].shape[1]), torch.float16, X.device, stream, result=False)
     experts_pair(X, r.offsets, r.rows, *gate, *up, hidden, fmt, out=H, stream=stream)
     experts_linear(H, r.offsets, None, *down, inner, fmt, out=Z, stream=stream)
-    Y = experts_combine(Z, r.pos, r.weights, residual=residual, stream=stream)
-    for made in (H, Z):
-        _keep(made, stream)
-    return Y
+    return experts_combine(Z, r.pos, r.weights, residual=residual, stream=stream)
