@@ -101,7 +101,8 @@ int run_experts(const _Float16 *X, int64_t T, const int32_t *offsets, const int3
     if (T < 1 || R < 1 || N < 1 || K < 1 || T >= kMaxDim || R >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
         return TRI_EINVAL;
     if (E < 1 || E > TRI_MAX_EXPERTS || (!rows && T < R)) return TRI_EINVAL;
-    if (N >= kMaxDim / 16 || K >= kMaxDim / 32) return TRI_EINVAL;   // grid size; 32-bit offsets in a block of rows
+    // a workgroup of 512 threads per 16 outputs, fewer than 2^32 threads in a row of the grid; 32-bit offsets in a block of rows
+    if (N > kMaxDim / 16 - 16 || K >= kMaxDim / 32) return TRI_EINVAL;
     if (rows && T > (((int64_t)1 << 31) - 8) / K) return TRI_EINVAL;   // gathered rows: 32-bit buffer offsets
     if (misaligned(X) || misaligned(Wp) || misaligned(Wp_up) || misaligned(Y)) return TRI_EALIGN;
     if (misaligned_to(offsets, 4) || misaligned_to(rows, 4) || misaligned_to(scale, 4) || misaligned_to(scale_up, 4))

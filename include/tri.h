@@ -296,7 +296,7 @@ int tri_experts_route(const void *logits, int dtype, int64_t T, int E, int topk,
  * int32, not decreasing, at most R (values outside are clamped); rows: R int32; Y: R*N fp16.
  * Rows of Y behind offsets[E] stay as they are, so do rows whose x(r) lies outside 0..T-1.  X,
  * Wp and Y must be 16-byte aligned, the rest 4-byte.  1 <= E <= TRI_MAX_EXPERTS,
- * N < 2^27, K < 2^26; with rows, X of at most 4 GiB - 16.  Y must not alias an input.  X is expected
+ * N <= 2^27 - 16, K < 2^26; with rows, X of at most 4 GiB - 16.  Y must not alias an input.  X is expected
  * finite (a row that is not spoils only the places that name it).
  * Errors: TRI_EINVAL (a size < 1 or >= 2^31, null, unknown fmt), TRI_EALIGN, TRI_EHIP. */
 int tri_experts_linear(const _Float16 *X, int64_t T, const int32_t *offsets, const int32_t *rows, int64_t R,

@@ -127,3 +127,11 @@ def test_helpers_refuse_tensors_off_the_gpu():
                  lambda: tri.experts_linear(x, i, i, w, x, 64, 0)]:
         with pytest.raises(ValueError):
             call()
+
+
+def test_experts_products_refuse_more_outputs_than_a_grid_takes():
+    """2^27 - 15 outputs would be 2^23 workgroups of 512 threads, one thread more than a grid's row may have."""
+    for N in ((1 << 27) - 15, (1 << 27) - 1, 1 << 27):
+        for K, fmt in ((5, 0), (8, 1)):
+            assert raw("tri_experts_linear", A, 16, B, B, 32, C, D, 8, N, K, fmt, A, None) == EINVAL
+            assert raw("tri_experts_pair", A, 16, B, B, 32, C, D, C, D, 8, N, K, fmt, A, None) == EINVAL

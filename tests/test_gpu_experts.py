@@ -652,3 +652,21 @@ def test_sums_are_those_of_fp32(K, name, fmt):
     d = 2 * np.sqrt(80 + K / 16) * 2.0 ** -23 * size
     say("  mean distance %.5f steps, %.5f allowed" % (off[live].mean(), (d / step)[live].mean() + 0.005))
     assert off[live].mean() <= (d / step)[live].mean() + 0.005
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("K", [5, 8])
+def test_the_most_outputs_of_a_product(K, fmt):
+    """2^27 - 16 outputs, the last that are taken, by the kernel of a workgroup per 16 outputs (K = 5) and the resident grid
+    (K = 8): rows that repeat, small integers, so that every result is exact."""
+    import torch
+    rng = np.random.default_rng([74, K, fmt])
+    N, n = (1 << 27) - 16, 1 << 12
+    W = rng.integers(-1, 2, (n, K)).astype(np.int8)
+    X = rng.integers(-4, 5, (1, K)).astype(np.float16)
+    Wp = tri.pack(cuda(W), fmt).repeat(N // n + 1, 1)[:N].view(1, N, -1)
+    want = cuda((X.astype(np.float64) @ W.T.astype(np.float64)).astype(np.float16)[0])
+    say("outputs N=%d K=%d fmt=%d" % (N, K, fmt))
+    Y = torch.full((1, N), float("nan"), dtype=torch.float16, device="cuda")
+    tri.experts_linear(cuda(X), cuda(places([1])), None, Wp, torch.ones(1, device="cuda"), K, fmt, out=Y)
+    assert torch.equal(Y[0], want.repeat(N // n + 1)[:N])
