@@ -499,7 +499,7 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
             for (int p = 0; p < NM; ++p) sd[p] += red[q][m][16 * p + c];
         }
         float y = (sd[0] * 16384.f - sx) * ex.scale[0][et.e];
-        if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sx) * ex.scale[1][et.e]);
+        if constexpr (PAIR) y = y / (1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sx) * ex.scale[1][et.e]);
         ex.Y[(int64_t)(et.r0 + m) * N + n0 + c] = __builtin_bit_cast(uint16_t, (_Float16)y);
     }
 }
@@ -773,7 +773,7 @@ __global__ __launch_bounds__(512, EU) void k_experts_loop(const Experts ex, int 
 #pragma unroll
                 for (int p = 0; p < NM; ++p) sd[p] += red[buf][q][m][16 * p + c];
             float y = (sd[0] * 16384.f - sxt[m]) * scale[0];
-            if constexpr (PAIR) y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sxt[m]) * scale[NM - 1]);
+            if constexpr (PAIR) y = y / (1.f + __expf(-y)) * ((sd[NM - 1] * 16384.f - sxt[m]) * scale[NM - 1]);
             done[held][m][c] = __builtin_bit_cast(uint16_t, (_Float16)y);
         }
     };

@@ -422,7 +422,9 @@ __device__ __forceinline__ void gemm_tile(const uint16_t *__restrict__ X, const 
                     for (int nt = 0; nt < NB; ++nt) {
                         const int n = n0 + 32 * nt + c;
                         float y = acc[mt][nt][4 * i + v] * scale;
-                        if constexpr (PAIR)              // (v_exp and v_rcp: about 1 ulp)
+                        // The quotient by v_rcp, 2^-23 off at most, where exp already is by 2^-23 |y|: a division in full
+                        // takes 1.3% more (2048 tokens 607 -> 615 us; in the kernels of few places it costs nothing).
+                        if constexpr (PAIR)
                             y = y * __builtin_amdgcn_rcpf(1.f + __expf(-y)) * (acc[mt][nt + NB][4 * i + v] * scale2);
                         if (n < N) Y[(int64_t)m * N + n] = __builtin_bit_cast(uint16_t, (_Float16)y);
                     }

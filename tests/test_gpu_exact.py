@@ -128,3 +128,27 @@ def test_every_code_counts(M, group, zeros):
         say("exact int4 M=%d N=%d K=%d group=%d zeros=%d" % (M, N, K, group, zeros))
         Y = tri.int4_linear(X, tri.int4_pack(Q, S, group, Z), N, group, zeros)
         assert torch.equal(Y, (X.float() @ W.t()).half()), (N, K)   # (integers below 2^24; past 65504: infinities)
+
+
+@pytest.mark.parametrize("fmt", [F2, F16])
+@pytest.mark.parametrize("K", [520, 129])
+@pytest.mark.parametrize("name", ["one place each", "few", "sixteen", "many"])
+def test_gates_of_any_size(name, K, fmt):
+    """Gates up to thousands of either sign: exp of the negative ones passes fp32, and their results are zeros.  (exp's
+    argument is off by 2^-24 of the gate, which weighs where the gate's result is not yet nothing: up to 2^-18 at 64; past
+    -64 the result is below 2^-80.)"""
+    import torch
+    sizes, N = SIZES[name], 100
+    E, R = len(sizes), sum(sizes)
+    X = integers(K + R, -2, 2, (R, K), torch.float16)
+    Ws = [integers(K + 70 + q, -1, 1, (E, N, K), torch.int8) for q in range(2)]
+    off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device="cuda")
+    Wp = [tri.pack(W.reshape(E * N, K), fmt).view(E, N, -1) for W in Ws]
+    sums = products(X, Ws, sizes, N)
+    for gate in (1 / 4, 4.0, 64.0):
+        say("gates", name, K, fmt, gate)
+        Y = tri.experts_pair(X, off, None, Wp[0], torch.full((E,), gate, device="cuda"), Wp[1],
+                             torch.full((E,), 1 / 256, device="cuda"), K, fmt)
+        g, u = sums[0] * gate, sums[1] / 256
+        ref = g / (1 + torch.exp(-g)) * u
+        assert bool(((Y.double() - ref).abs() <= (2.0 ** -17 + 2.0 ** -11) * ref.abs() + 2.0 ** -25).all())
