@@ -288,12 +288,38 @@ def tri_probe_stream(src, nbytes, workgroups, unroll, sink, stream=None):
 
 # ---------------------------------------------------------------- allocating helpers
 
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
+def _new(shape, dtype, device, stream, result=True):
+    """An uninitialised tensor for a call on `stream`.  A stream that the caller named writes it without waiting for the
+    current one, so its memory comes from that stream's own pool: the current stream's pool hands out memory that kernels
+    queued there may still use.  A result is not reused, either, before the current stream is done with it, where the
+    caller reads it after the two were ordered."""
+    torch = _torch or _load_torch()
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if handle is None or handle == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if result:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def pack(W, fmt, stream=None):
     """Pack a (N, K) int8 CUDA tensor; returns a new (N, row_bytes) uint8 tensor."""
     import torch
     N, K = W.shape
     assert W.dtype == torch.int8 and W.is_cuda and W.is_contiguous()
-    Wp = torch.empty((N, tri_row_bytes(K, fmt)), dtype=torch.uint8, device=W.device)
+    Wp = _new((N, tri_row_bytes(K, fmt)), torch.uint8, W.device, stream)
     (tri_pack2 if fmt == TRI_FMT_2BIT else tri_pack16)(W, N, K, Wp, stream)
     return Wp
 
@@ -304,7 +330,7 @@ def unpack(Wp, K, fmt, stream=None):
     N = Wp.shape[0]
     assert Wp.dtype == torch.uint8 and Wp.is_cuda and Wp.is_contiguous()
     assert Wp.shape[1] == tri_row_bytes(K, fmt)
-    W = torch.empty((N, K), dtype=torch.int8, device=Wp.device)
+    W = _new((N, K), torch.int8, Wp.device, stream)
     tri_unpack(Wp, N, K, fmt, W, stream)
     return W
 
@@ -315,10 +341,10 @@ def quantize(W, fmt, stream=None):
     import torch
     N, K = W.shape
     assert W.dtype == torch.float32 and W.is_cuda and W.is_contiguous()
-    Wp = torch.empty((N, tri_row_bytes(K, fmt)), dtype=torch.uint8, device=W.device)
-    scale = torch.empty(1, dtype=torch.float32, device=W.device)
+    Wp = _new((N, tri_row_bytes(K, fmt)), torch.uint8, W.device, stream)
+    scale = _new(1, torch.float32, W.device, stream)
     nbytes = tri_quantize_workspace_bytes(N, K)
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=W.device)
+    ws = _new(max(nbytes, 16), torch.uint8, W.device, stream, result=False)
     tri_quantize(W, N, K, fmt, Wp, scale, ws, nbytes, stream)
     return Wp, scale
 
@@ -330,7 +356,7 @@ def linear(X, Wp, scale, K, fmt, algo=TRI_ALGO_AUTO, out=None, stream=None):
     N = Wp.shape[0]
     assert X.dtype == torch.float16 and X.is_cuda and X.is_contiguous() and X.shape[1] == K
     assert Wp.dtype == torch.uint8 and Wp.is_contiguous() and Wp.shape[1] == tri_row_bytes(K, fmt)
-    Y = out if out is not None else torch.empty((M, N), dtype=torch.float16, device=X.device)
+    Y = out if out is not None else _new((M, N), torch.float16, X.device, stream)
     if algo == TRI_ALGO_AUTO:
         tri_linear(X, Wp, scale, M, N, K, fmt, Y, stream)
     else:
@@ -341,16 +367,6 @@ def linear(X, Wp, scale, K, fmt, algo=TRI_ALGO_AUTO, out=None, stream=None):
 # The helpers below take the tensors' device (whichever device is current) and its current stream, or `stream` (ordering
 # that stream behind what writes their inputs, and whoever reads their results behind it, is the caller's); they raise
 # ValueError for tensors of another type, shape, device or layout than they name.
-
-_torch = None
-
-
-def _load_torch():
-    global _torch
-    import torch
-    _torch = torch
-    return torch
-
 
 def _need(ok, what):
     if not ok:
@@ -382,22 +398,6 @@ def _tensors(device, dtype, **named):
     for name, t in named.items():
         if t is not None and not _plain(t, dtype, device):
             raise ValueError("%s must be a contiguous %s tensor on device %d" % (name, dtype, device))
-
-
-def _new(shape, dtype, device, stream, result=True):
-    """An uninitialised tensor for a call on `stream`.  A stream that the caller named writes it without waiting for the
-    current one, so its memory comes from that stream's own pool: the current stream's pool hands out memory that kernels
-    queued there may still use.  A result is not reused, either, before the current stream is done with it, where the
-    caller reads it after the two were ordered."""
-    torch = _torch
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if handle is None or handle == torch._C._cuda_getCurrentRawStream(device.index):
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if result:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 @functools.lru_cache(maxsize=4096)

@@ -38,7 +38,13 @@ def calls():
     H = tri.experts_pair(X, r.offsets, r.rows, *gate, *up, K, F2)
     Y = tri.experts_linear(H, r.offsets, None, *down, N, F2)
     ws = tri.tri_experts_route_workspace_bytes(T, E, topk)
+    trits = cuda(synth.trits(rng, N, K))
+    packed = tri.pack(trits, F2)
     return {
+        "pack": (lambda s: [tri.pack(trits, F2, stream=s)], []),
+        "unpack": (lambda s: [tri.unpack(packed, K, F2, stream=s)], []),
+        "quantize": (lambda s: list(tri.quantize(W, F2, stream=s)), [tri.tri_quantize_workspace_bytes(N, K)]),
+        "linear": (lambda s: [tri.linear(X, packed, 0.03, K, F2, stream=s)], []),
         "int4_pack": (lambda s: [tri.int4_pack(Q, S, group, Z, stream=s)], []),
         "int4_unpack": (lambda s: list(tri.int4_unpack(Wp, N, K, group, True, stream=s)), []),
         "int4_quantize": (lambda s: [tri.int4_quantize(W, group, True, stream=s)], []),
@@ -52,8 +58,8 @@ def calls():
     }
 
 
-NAMES = ["int4_pack", "int4_unpack", "int4_quantize", "int4_linear", "experts_route", "experts_linear", "experts_pair",
-         "experts_combine", "experts_mlp"]
+NAMES = ["pack", "unpack", "quantize", "linear", "int4_pack", "int4_unpack", "int4_quantize", "int4_linear", "experts_route",
+         "experts_linear", "experts_pair", "experts_combine", "experts_mlp"]
 
 
 @pytest.mark.parametrize("kind", ["stream", "handle"])
