@@ -509,12 +509,12 @@ __global__ __launch_bounds__(512) void k_experts_mv(const Experts ex, int C, int
 // outputs, blockIdx.x, + gridDim.x, ...: only weights are read, the next block's chunks in flight while one is
 // contracted; the waves' partial sums meet in one of two LDS buffers in turn, so a block costs one barrier.
 //
-// Measured on eight experts, two per token: gate and up 4096 -> 11008 of one token (45 MB of 2-bit weights) 13.1 us, where
-// a plain read takes 7.6; of 16 tokens (180 MB) 43 us against 28; down 11008 -> 4096 of 16 tokens, 1.6-bit (72 MB) 36 us
-// against 12.  What bounds it is the vector ALU (about 19 of 43 us at 16 tokens, the matrix cores another 9, hardly
-// overlapped) and the waits around a block's barrier; splitting the waves by outputs instead, with all of the row per
-// wave and no barrier, was slower (59 us), as were deeper loads (48 us).  Digits as subnormals d * 2^-24 would save the
-// 1.6-bit products 4 - 8% (down 34 us) and the 2-bit ones nothing, at the price of ten bits of every sum.
+// Measured on eight experts, two per token: gate and up 4096 -> 11008 of one token (45 MB of 2-bit weights) 13.6 us, where
+// a plain read takes 7.6; of 16 tokens (180 MB) 44 us against 28; down 11008 -> 4096 of 16 tokens, 1.6-bit (72 MB) 37 us
+// against 12.  What bounds it is the vector ALU (19 of 44 us at 16 tokens, 22 of 37 with 1.6-bit digits; the matrix cores
+// another 10 and 7, hardly overlapped) and the waits around a block's barrier; splitting the waves by outputs instead, with
+// all of the row per wave and no barrier, was slower (59 us), as were deeper loads (48 us).  Digits as subnormals d * 2^-24
+// would save the 1.6-bit products 4 - 8% (down 34 us) and the 2-bit ones nothing, at the price of ten bits of every sum.
 constexpr int kHeld = 16;                        // blocks whose results wait in LDS
 // Whether the loop's registers for A operands and for D blocks' chunks leave the rest of its code enough of 128 registers
 // (two workgroups per CU) that the compiler spills nothing, or next to nothing; limits as found by compiling.

@@ -43,7 +43,7 @@
 // (expert_tile: the sizes are on the device, the grid is their upper bound and tiles past the list end at once); the
 // tile's rows of X are gathered by the load offsets, its weights and scale are its expert's.  kPair: half of a wave's
 // column tiles are those of the second matrix, for the same output columns, and silu(gate) * up is formed from the two
-// accumulators.  2048 tokens, two of eight experts each, gate and up 4096 -> 11008 (0.74 TFLOP): 620 us, 1190 TFLOP/s,
+// accumulators.  2048 tokens, two of eight experts each, gate and up 4096 -> 11008 (0.74 TFLOP): 600 us, 1230 TFLOP/s,
 // where a dense fp16 library product reaches 1385.
 #include <type_traits>
 
@@ -546,7 +546,7 @@ bool experts_gemm_fits(const Experts &ex, int fmt)
 // Tiles of 64 places, whatever the sizes: several such workgroups share a CU, the last tile of an expert wastes little,
 // and 128-place tiles lost at every measured size (pair, 2-bit, 4096 -> 11008, eight experts, two per token: 256 tokens
 // 150 against 202 us, 2048 tokens 655 against 654 (256 columns) and 727 us (512); 1.6-bit 798 against 828 - 1029; with the
-// gate as it is now the 64-place tiles take 608 and 675).  Two column tiles per wave for a pair; for one matrix one, or
+// gate as it is now the 64-place tiles take 600 and 695).  Two column tiles per wave for a pair; for one matrix one, or
 // two for 2-bit digits where those still make two rounds (11008 -> 4096, 2048 tokens 369 -> 332 us, 256 tokens 82 -> 85
 // us; 1.6-bit 421 -> 422 us, 256 tokens 101 -> 122 us).
 template <int FMT>

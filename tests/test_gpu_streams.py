@@ -129,3 +129,39 @@ def test_the_default_stream_named_from_another(handle):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b), name
+
+
+def test_a_named_stream_inside_a_capture():
+    """A helper on a stream that was forked from the one being captured, its results and intermediate tensors made inside the
+    capture, replayed on new inputs with eager calls between the replays."""
+    import torch
+    rng = np.random.default_rng(82)
+    T, E, topk, K, N = 200, 8, 2, 256, 384
+    mk = lambda *shape: torch.zeros(shape, dtype=torch.float16, device="cuda")
+    X, logits = mk(T, K), mk(T, E)
+    stack = lambda n, k: (tri.pack(cuda(synth.trits(rng, E * n, k)), F2).view(E, n, -1), torch.full((E,), 0.03, device="cuda"))
+    mats = stack(N, K), stack(N, K), stack(K, N)
+
+    def step(stream):
+        return tri.experts_mlp(X, logits, topk, *mats, F2, residual=X, stream=stream)
+
+    step(None)
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            other.wait_stream(side)
+            Y = step(other)
+            side.wait_stream(other)
+    torch.cuda.synchronize()
+    for seed in (1, 2, 3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        X.copy_(torch.randn(X.shape, device="cuda", generator=g).half())
+        logits.copy_(torch.randn(logits.shape, device="cuda", generator=g).half())
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = Y.clone()
+        assert torch.equal(got, step(None)) and torch.equal(got, step(other)), seed
+        torch.cuda.synchronize()
+    del graph
