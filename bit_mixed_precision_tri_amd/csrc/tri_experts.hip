@@ -520,16 +520,16 @@ constexpr int kHeld = 16;                        // blocks whose results wait in
 // (two workgroups per CU) that the compiler spills nothing, or next to nothing; limits as found by compiling.
 constexpr bool loop_fits(int fmt, int ma, int cst, bool pair, int d)
 {
-    // (84 KB of LDS: one workgroup per CU.  Eight experts, two per token, pair, with 256 registers and the next block's
-    // chunks in flight against 128: 64 tokens 2048 -> 5632 28 / 31 us, 4096 -> 11008 76 / 71, 96 tokens 85 / 86)
+    // (84 KB of LDS: one workgroup per CU, which may have 256 registers; held to 128 the short rows, where both fit, take
+    // as long: pair of 64 tokens, 2048 -> 5632 31.9 us either way)
     if (ma == 16 && fmt == TRI_FMT_1P6BIT) return false;
     const int nop = fmt == TRI_FMT_2BIT ? 8 : 10, cl = ma == 1 ? nop : 16 / ma, na = (nop + cl - 1) / cl;
     return 4 * cst * (na + (pair ? 2 : 1) * d) <= (fmt == TRI_FMT_2BIT ? 80 : ma == 1 ? 40 : 64);
 }
 // Waves per SIMD to compile for, and blocks in registers: three workgroups per CU with one block each where the registers
-// are very few (a pair of one row: 12.3 us against 13.8 with two of two blocks); else two per CU where they fit, with the
-// next block's chunks in flight (D = 2) or, failing that, one workgroup's loads under the other's products (D = 1); else
-// one.
+// are very few (a pair of two tokens 19.6 us against 20.3 with two of two blocks, of one token 13.2 either way); else two
+// per CU where they fit, with the next block's chunks in flight (D = 2) or, failing that, one workgroup's loads under the
+// other's products (D = 1); else one.
 constexpr bool loop_light(int fmt, int ma, int cst, bool pair) { return ma == 1 && fmt == TRI_FMT_2BIT && pair && cst <= 2; }
 constexpr int loop_waves(int fmt, int ma, int cst, bool pair)
 {
