@@ -31,6 +31,31 @@ class TriGlue(ctypes.Structure):
                 ("pair", ctypes.c_int), ("residual", ctypes.c_void_p)]
 
 
+class TriHeads(ctypes.Structure):
+    """tri_heads of include/tri.h."""
+    _fields_ = [("X", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
+class TriRotary(ctypes.Structure):
+    """tri_rotary of include/tri.h."""
+    _fields_ = [("table", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dims", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("norm", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class TriCache(ctypes.Structure):
+    """tri_cache of include/tri.h."""
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("K_scale", ctypes.c_void_p), ("V_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("page", ctypes.c_int),
+                ("fmt", ctypes.c_int)]
+
+
+class TriSequences(ctypes.Structure):
+    """tri_sequences of include/tri.h."""
+    _fields_ = [("offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("table", ctypes.c_void_p), ("B", ctypes.c_int64),
+                ("width", ctypes.c_int64), ("max_new", ctypes.c_int64), ("max_len", ctypes.c_int64)]
+
+
 class TriError(RuntimeError):
     def __init__(self, code, what):
         super().__init__("%s failed: %s (%d)" % (what, status_string(code), code))
@@ -92,8 +117,14 @@ def lib():
         L.tri_experts_linear.argtypes = [p, i64, p, p, i64, p, p, i32, i64, i64, i32, p, p]
         L.tri_experts_pair.argtypes = [p, i64, p, p, i64, p, p, p, p, i32, i64, i64, i32, p, p]
         L.tri_experts_combine.argtypes = [p, i64, p, p, p, i64, i32, i64, p, p]
+        L.tri_heads_rotate.argtypes = [p, i32, i64, i32, p, p, p]
+        L.tri_cache_append.argtypes = [p, p, i64, p, i64, p, i64, p, p, p, p]
+        L.tri_cache_attend_workspace_bytes.argtypes = [p, p, i64, i32, i64, i64]
+        L.tri_cache_attend_workspace_bytes.restype = i64
+        L.tri_cache_attend.argtypes = [p, p, i64, p, i64, i32, ctypes.c_float, i64, i64, p, i64, p, i64, p]
         for name in ("tri_int4_pack", "tri_int4_unpack", "tri_int4_quantize", "tri_int4_linear", "tri_experts_route",
-                     "tri_experts_linear", "tri_experts_pair", "tri_experts_combine"):
+                     "tri_experts_linear", "tri_experts_pair", "tri_experts_combine", "tri_heads_rotate", "tri_cache_append",
+                     "tri_cache_attend"):
             getattr(L, name).restype = i32
         _lib = L
     return _lib
@@ -254,6 +285,38 @@ def tri_experts_pair(X, T, offsets, rows, R, Wp, scale, Wp_up, scale_up, E, N, K
 def tri_experts_combine(Z, R, pos, weights, residual, T, topk, N, Y, stream=None):
     return _check(lib().tri_experts_combine(_ptr(Z), int(R), _ptr(pos), _ptr(weights), _ptr(residual), int(T),
                                             int(topk), int(N), _ptr(Y), _stream(stream)), "tri_experts_combine")
+
+
+TRI_KV_INT8, TRI_KV_E4M3 = 0, 1
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def tri_heads_rotate(heads, T, dim, rot, positions, stream=None):
+    """heads: a sequence of TriHeads; rot: a TriRotary."""
+    G = len(heads)
+    hs = (TriHeads * max(G, 1))(*heads)
+    return _check(lib().tri_heads_rotate(_ref(hs), G, int(T), int(dim), _ref(rot), _ptr(positions), _stream(stream)),
+                  "tri_heads_rotate")
+
+
+def tri_cache_append(cache, seqs, T, K, k_stride, V, v_stride, rot=None, k_gain=None, queries=None, stream=None):
+    """cache: a TriCache; seqs: a TriSequences; rot: a TriRotary or None; queries: a TriHeads or None."""
+    return _check(lib().tri_cache_append(_ref(cache), _ref(seqs), int(T), _ptr(K), int(k_stride), _ptr(V), int(v_stride),
+                                         _ref(rot), _ptr(k_gain), _ref(queries), _stream(stream)), "tri_cache_append")
+
+
+def tri_cache_attend_workspace_bytes(cache, seqs, T, heads, window=0, sinks=0):
+    return int(lib().tri_cache_attend_workspace_bytes(_ref(cache), _ref(seqs), int(T), int(heads), int(window), int(sinks)))
+
+
+def tri_cache_attend(cache, seqs, T, Q, q_stride, heads, scale, window, sinks, O, o_stride, workspace, workspace_bytes,
+                     stream=None):
+    return _check(lib().tri_cache_attend(_ref(cache), _ref(seqs), int(T), _ptr(Q), int(q_stride), int(heads), float(scale),
+                                         int(window), int(sinks), _ptr(O), int(o_stride), _ptr(workspace),
+                                         int(workspace_bytes), _stream(stream)), "tri_cache_attend")
 
 
 def tri_select_algo(M, N, K, fmt):
@@ -600,3 +663,196 @@ def experts_mlp(X, logits, topk, gate, up, down, fmt, renorm=True, residual=None
     experts_pair(X, r.offsets, r.rows, *gate, *up, hidden, fmt, out=H, stream=stream)
     experts_linear(H, r.offsets, None, *down, inner, fmt, out=Z, stream=stream)
     return experts_combine(Z, r.pos, r.weights, residual=residual, stream=stream)
+
+
+# ---------------------------------------------------------------- heads and the 8-bit cache
+
+def rotary_table(rows, dims, base=10000.0, device="cuda"):
+    """Cosines and sines of positions 0 .. rows-1 for `dims` rotated values, a (rows, dims / 2, 2) float32 tensor: angle
+    p * base^(-2 i / dims), taken in 64 bits."""
+    torch = _torch or _load_torch()
+    freq = base ** (-torch.arange(0, dims, 2, device=device, dtype=torch.float64) / dims)
+    angle = torch.arange(rows, device=device, dtype=torch.float64)[:, None] * freq
+    return torch.stack([torch.cos(angle), torch.sin(angle)], -1).float()
+
+
+class Rotary:
+    """How heads are normalised and rotated (tri_rotary); made once and kept.  table: as rotary_table gives it, or None (no
+    rotation); gains: None, or the norm's fp16 gains of the sets of heads it will be used on, (queries, keys) for
+    cache_append, each (dim) or None."""
+
+    def __init__(self, table, gains=None, norm=True, eps=1e-5, interleaved=False):
+        torch = _torch or _load_torch()
+        if table is not None:
+            _need(table.is_cuda and table.dim() == 3 and table.shape[0] > 0 and table.shape[2] == 2 and
+                  table.dtype is torch.float32 and table.is_contiguous(),
+                  "table must be a contiguous (rows, dims / 2, 2) float32 tensor on the GPU")
+        self.table, self.gains, self.norm = table, None if gains is None else tuple(gains), bool(norm)
+        for g in self.gains or ():
+            _need(g is None or (g.is_cuda and g.dtype is torch.float16 and g.dim() == 1 and g.is_contiguous()),
+                  "gains must be contiguous (dim) float16 tensors on the GPU")
+        rows, half = (0, 0) if table is None else table.shape[:2]
+        self.struct = TriRotary(None if table is None else table.data_ptr(), rows, 2 * half, 1 if interleaved else 0,
+                                1 if norm else 0, eps)
+        self._ref = ctypes.addressof(self.struct)
+
+    def _gain(self, i, n, dim, device):
+        """The gain of set i of n as an address, checked."""
+        if self.table is not None and self.table.get_device() != device:
+            raise ValueError("the rotation's table must be on the heads' device")
+        if self.gains is None:
+            return None
+        _need(len(self.gains) == n, "gains must be one for each set of heads")
+        g = self.gains[i]
+        if g is None:
+            return None
+        _need(g.shape[0] == dim and g.get_device() == device, "gains must be (dim) tensors on the heads' device")
+        return g.data_ptr()
+
+
+class KVCache:
+    """The pages of an 8-bit cache (tri_cache): codes K (pages, heads, page, dim) and V (pages, heads, dim, page), uint8,
+    scales (pages, heads) float32.  KVCache.empty makes a new one."""
+
+    def __init__(self, K, V, K_scale, V_scale, fmt):
+        torch = _torch or _load_torch()
+        _need(K.is_cuda and K.dim() == 4, "K must be a (pages, heads, page, dim) tensor on the GPU")
+        (pages, heads, page, dim), dev = K.shape, K.get_device()
+        _need(dim in (64, 128, 256) and page in (16, 32, 64, 128), "dim must be 64, 128 or 256, page 16, 32, 64 or 128")
+        _need(fmt in (TRI_KV_INT8, TRI_KV_E4M3), "fmt must be TRI_KV_INT8 or TRI_KV_E4M3")
+        _need(V.shape == (pages, heads, dim, page) and K_scale.shape == V_scale.shape == (pages, heads),
+              "V must be (pages, heads, dim, page), the scales (pages, heads)")
+        _tensors(dev, torch.uint8, K=K, V=V)
+        _tensors(dev, torch.float32, K_scale=K_scale, V_scale=V_scale)
+        self.K, self.V, self.K_scale, self.V_scale, self.fmt = K, V, K_scale, V_scale, fmt
+        self.pages, self.heads, self.page, self.dim, self.device = pages, heads, page, dim, dev
+        self.struct = TriCache(K.data_ptr(), V.data_ptr(), K_scale.data_ptr(), V_scale.data_ptr(), pages, heads, dim, page, fmt)
+        self._ref = ctypes.addressof(self.struct)
+
+    @classmethod
+    def empty(cls, pages, heads, dim, page=64, fmt=TRI_KV_INT8, device="cuda"):
+        torch = _torch or _load_torch()
+        K = torch.zeros((pages, heads, page, dim), dtype=torch.uint8, device=device)
+        scales = torch.ones((2, pages, heads), dtype=torch.float32, device=device)
+        return cls(K, torch.zeros((pages, heads, dim, page), dtype=torch.uint8, device=device), scales[0], scales[1], fmt)
+
+
+class Sequences:
+    """A batch of sequences with new tokens (tri_sequences): offsets (B + 1), lens (B) and table (B, width), int32 on the
+    device, read when a call runs (so a step may change them in place, inside a captured graph as well).  max_new: the most
+    new tokens of a sequence; max_len: the most tokens, new ones included (all that the table has room for, if None)."""
+
+    def __init__(self, offsets, lens, table, max_new, max_len=None):
+        torch = _torch or _load_torch()
+        _need(table.is_cuda and table.dim() == 2 and table.numel() > 0, "table must be a (B, width) tensor on the GPU")
+        (B, width), dev = table.shape, table.get_device()
+        _tensors(dev, torch.int32, offsets=offsets, lens=lens, table=table)
+        _need(offsets.shape == (B + 1,) and lens.shape == (B,), "offsets must be (B + 1), lens (B)")
+        _need(max_new > 0 and (max_len is None or max_len > 0), "max_new and max_len must be at least 1")
+        self.offsets, self.lens, self.table, self.device = offsets, lens, table, dev
+        most = min(128 * width, (1 << 31) - 129)
+        self.struct = TriSequences(offsets.data_ptr(), lens.data_ptr(), table.data_ptr(), B, width, max_new,
+                                   most if max_len is None else max_len)
+        self._whole = max_len is None
+        self._ref = ctypes.addressof(self.struct)
+
+    def _fit(self, cache):
+        """The struct's address for a call on `cache`."""
+        if self.device != cache.device:
+            raise ValueError("the sequences must be on the cache's device")
+        if self._whole:
+            self.struct.max_len = min(self.struct.width * cache.page, (1 << 31) - 129)
+        return self._ref
+
+
+def _heads_of(x, what, dim, device, T=None, heads=None):
+    """Address, token stride and heads of a (T, heads, dim) float16 tensor whose tokens may lie apart."""
+    shape = x.shape
+    if not (len(shape) == 3 and x.dtype is _torch.float16 and x.get_device() == device and shape[2] == dim and
+            x.stride(2) == 1 and (shape[1] == 1 or x.stride(1) == dim) and (T is None or shape[0] == T) and
+            (heads is None or shape[1] == heads) and shape[0] > 0 and shape[1] > 0):
+        raise ValueError("%s must be a (T, heads, dim) float16 tensor on device %d whose heads lie one after another" %
+                         (what, device))
+    return x.data_ptr(), x.stride(0) if shape[0] > 1 else shape[1] * dim, shape[1]
+
+
+def heads_rotate(xs, rotary, positions, out=None, stream=None):
+    """The heads of every (T, heads, dim) float16 tensor of `xs` (queries and keys, of the same T tokens) normalised and
+    rotated by their tokens' positions (T) int32, in one launch; returns a tuple of new tensors, or `out`, which may be `xs`
+    itself.  Rows of a token whose position is outside the rotation's table are not written."""
+    torch = _torch or _load_torch()
+    _need(0 < len(xs) <= TRI_MAX_GROUPS and xs[0].dim() == 3 and xs[0].is_cuda, "xs must be 1 to 4 (T, heads, dim) tensors on the GPU")
+    (T, _, dim), dev = xs[0].shape, xs[0].get_device()
+    _need(_plain(positions, torch.int32, dev) and positions.shape == (T,), "positions must be a contiguous (T) int32 tensor on the heads' device")
+    if out is None:
+        out = tuple(_new(tuple(x.shape), torch.float16, x.device, stream) for x in xs)
+    _need(len(out) == len(xs), "out must have a tensor for each of xs")
+    hs = (TriHeads * len(xs))()
+    for i, (x, y) in enumerate(zip(xs, out)):
+        h = hs[i]
+        h.X, h.x_stride, h.heads = _heads_of(x, "xs", dim, dev, T)
+        h.Y, h.y_stride, _ = _heads_of(y, "out", dim, dev, T, h.heads)
+        h.gain = rotary._gain(i, len(xs), dim, dev)
+    _launch("tri_heads_rotate", dev, stream, ctypes.addressof(hs), len(xs), T, dim, rotary._ref, positions.data_ptr())
+    return tuple(out)
+
+
+def cache_append(cache, seqs, K, V, rotary=None, Q=None, out=None, stream=None):
+    """Round the new tokens' keys and values (T, heads, dim) to 8 bits, into the pages of their sequences.  With `rotary`, keys
+    are normalised and rotated first; the queries Q (T, query heads, dim), if given, too, in the same launch: they are returned,
+    in a new tensor or in `out`, which may be Q itself."""
+    torch = _torch or _load_torch()
+    dim, dev = cache.dim, cache.device
+    kp, ks, _ = _heads_of(K, "K", dim, dev, None, cache.heads)
+    T = K.shape[0]
+    vp, vs, _ = _heads_of(V, "V", dim, dev, T, cache.heads)
+    rot = gain = q = None
+    if rotary is not None:
+        rot, gain = rotary._ref, rotary._gain(1, 2, dim, dev)
+    if Q is not None:
+        _need(rotary is not None, "queries are taken with a rotation only")
+        if out is None:
+            out = _new(tuple(Q.shape), torch.float16, Q.device, stream)
+        h = TriHeads()
+        h.X, h.x_stride, h.heads = _heads_of(Q, "Q", dim, dev, T)
+        h.Y, h.y_stride, _ = _heads_of(out, "out", dim, dev, T, h.heads)
+        h.gain = rotary._gain(0, 2, dim, dev)
+        q = ctypes.addressof(h)
+    else:
+        _need(out is None, "out is for queries")
+    _launch("tri_cache_append", dev, stream, cache._ref, seqs._fit(cache), T, kp, ks, vp, vs, rot, gain, q)
+    return out
+
+
+def cache_attend_workspace_bytes(cache, seqs, T, heads, window=0, sinks=0):
+    """What cache_attend needs as workspace for T new tokens of `heads` query heads (0: none)."""
+    seqs._fit(cache)
+    need = tri_cache_attend_workspace_bytes(cache.struct, seqs.struct, T, heads, window, sinks)
+    _need(need >= 0, "sizes that tri_cache_attend does not take")
+    return need
+
+
+def cache_attend(cache, seqs, Q, scale=None, window=0, sinks=0, workspace=None, out=None, stream=None):
+    """Causal attention of the new tokens' queries Q (T, query heads, dim) over their sequences in the cache, where
+    cache_append has put their own keys and values.  window > 0: a token sees the last `window` positions and the first
+    `sinks`.  scale: dim ** -0.5 if None.  Returns (T, query heads, dim), a new tensor (rows of no sequence are not written) or
+    `out`.  `workspace`: a uint8 tensor of at least cache_attend_workspace_bytes; allocated where it is None and needed."""
+    torch = _torch or _load_torch()
+    dim, dev = cache.dim, cache.device
+    qp, qs, H = _heads_of(Q, "Q", dim, dev)
+    T = Q.shape[0]
+    O = _new(tuple(Q.shape), torch.float16, Q.device, stream) if out is None else out
+    op, os_, _ = _heads_of(O, "out", dim, dev, T, H)
+    sref = seqs._fit(cache)
+    ws, nbytes = None, 0
+    if workspace is None:
+        nbytes = _lib.tri_cache_attend_workspace_bytes(cache._ref, sref, T, H, window, sinks) if _lib else \
+            cache_attend_workspace_bytes(cache, seqs, T, H, window, sinks)
+        if nbytes > 0:
+            workspace = _new(nbytes, torch.uint8, Q.device, stream, result=False)
+    if workspace is not None:
+        _need(_plain(workspace, torch.uint8, dev), "workspace must be a contiguous uint8 tensor on the cache's device")
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    _launch("tri_cache_attend", dev, stream, cache._ref, sref, T, qp, qs, H, dim ** -0.5 if scale is None else scale, window,
+            sinks, op, os_, ws, max(nbytes, 0))
+    return O

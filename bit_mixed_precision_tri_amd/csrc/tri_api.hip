@@ -1,6 +1,7 @@
 // tri_api.hip -- the extern "C" entry points of libtri: argument checks and dispatch.
 // Every check runs on the host before any launch; see include/tri.h for the contract.
 #include "tri_internal.h"
+#include <initializer_list>
 
 using namespace tri;
 static_assert(TRI_MAX_GROUPS == kMaxGroups, "group table size");
@@ -122,6 +123,47 @@ int run_experts(const _Float16 *X, int64_t T, const int32_t *offsets, const int3
     ex.N = (int)N;
     ex.K = (int)K;
     return launch_experts(ex, fmt, s);
+}
+
+// Heads and the 8-bit cache.
+constexpr int kMaxHeads = 65535;                 // and sequences
+bool known_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
+bool bad_stride(int64_t stride, int64_t least) { return stride < least || stride % 8 != 0; }
+
+int check_heads(const tri_heads &h, int64_t T, int dim)
+{
+    if (!h.X || !h.Y || h.heads < 1 || h.heads > kMaxHeads || T * h.heads >= kMaxDim) return TRI_EINVAL;
+    if (bad_stride(h.x_stride, (int64_t)h.heads * dim) || bad_stride(h.y_stride, (int64_t)h.heads * dim)) return TRI_EINVAL;
+    if (misaligned(h.X) || misaligned(h.Y) || misaligned(h.gain)) return TRI_EALIGN;
+    return TRI_OK;
+}
+
+int check_rotary(const tri_rotary *r, int dim)
+{
+    if (!r || r->dims < 0 || r->dims > dim || r->dims % 16 != 0) return TRI_EINVAL;
+    if (r->dims > 0 && (!r->table || r->rows < 1 || r->rows >= kMaxDim)) return TRI_EINVAL;
+    if (r->norm && !(r->eps >= 0.f && r->eps <= 3.4e38f)) return TRI_EINVAL;   // (NaN fails)
+    return r->dims > 0 && misaligned(r->table) ? TRI_EALIGN : TRI_OK;
+}
+
+int check_cache(const tri_cache *c, const tri_sequences *q)
+{
+    if (!c || !c->K || !c->V || !c->K_scale || !c->V_scale || c->pages < 1 || c->pages >= kMaxDim) return TRI_EINVAL;
+    if (c->heads < 1 || c->heads > kMaxHeads || !known_dim(c->dim) || (c->fmt != TRI_KV_INT8 && c->fmt != TRI_KV_E4M3))
+        return TRI_EINVAL;
+    if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return TRI_EINVAL;
+    if (!q || !q->offsets || !q->lens || !q->table || q->B < 1 || q->B > kMaxHeads) return TRI_EINVAL;
+    for (const int64_t n : {q->width, q->max_new, q->max_len})
+        if (n < 1 || n >= kMaxDim - 128) return TRI_EINVAL;
+    if (misaligned(c->K) || misaligned(c->V) || misaligned_to(c->K_scale, 4) || misaligned_to(c->V_scale, 4)) return TRI_EALIGN;
+    if (misaligned_to(q->offsets, 4) || misaligned_to(q->lens, 4) || misaligned_to(q->table, 4)) return TRI_EALIGN;
+    return TRI_OK;
+}
+
+bool bad_attend(const tri_cache *c, int64_t T, int heads, int64_t window, int64_t sinks)
+{
+    return T < 1 || T >= kMaxDim || heads < 1 || heads > kMaxHeads || heads % c->heads != 0 || T * heads >= kMaxDim || window < 0 ||
+           window >= kMaxDim || sinks < 0 || sinks >= kMaxDim;
 }
 
 }  // namespace
@@ -380,6 +422,69 @@ int tri_experts_combine(const _Float16 *Z, int64_t R, const int32_t *pos, const 
     return launch_combine(reinterpret_cast<const uint16_t *>(Z), R, pos, weights,
                           reinterpret_cast<const uint16_t *>(residual), (int)T, topk, (int)N,
                           reinterpret_cast<uint16_t *>(Y), stream);
+}
+
+int tri_heads_rotate(const tri_heads *heads, int G, int64_t T, int dim, const tri_rotary *rot, const int32_t *positions,
+                     hipStream_t stream)
+{
+    if (!heads || G < 1 || G > TRI_MAX_GROUPS || T < 1 || T >= kMaxDim || !known_dim(dim) || !positions) return TRI_EINVAL;
+    int rc = check_rotary(rot, dim);
+    for (int g = 0; g < G && rc == TRI_OK; ++g) rc = check_heads(heads[g], T, dim);
+    if (rc == TRI_OK && misaligned_to(positions, 4)) rc = TRI_EALIGN;
+    return rc != TRI_OK ? rc : launch_rotate(heads, G, (int)T, dim, *rot, positions, stream);
+}
+
+int tri_cache_append(const tri_cache *cache, const tri_sequences *seqs, int64_t T, const _Float16 *K, int64_t k_stride,
+                     const _Float16 *V, int64_t v_stride, const tri_rotary *rot, const _Float16 *k_gain,
+                     const tri_heads *queries, hipStream_t stream)
+{
+    int rc = check_cache(cache, seqs);
+    if (rc != TRI_OK) return rc;
+    const int64_t row = (int64_t)cache->heads * cache->dim;
+    if (T < 1 || T >= kMaxDim || T * cache->heads >= kMaxDim || !K || !V || bad_stride(k_stride, row) || bad_stride(v_stride, row)) return TRI_EINVAL;
+    if (rot) rc = check_rotary(rot, cache->dim);
+    else if (queries) rc = TRI_EINVAL;
+    if (rc == TRI_OK && queries) rc = check_heads(*queries, T, cache->dim);
+    if (rc != TRI_OK) return rc;
+    if (misaligned(K) || misaligned(V) || misaligned(k_gain)) return TRI_EALIGN;
+    return launch_append(*cache, *seqs, (int)T, reinterpret_cast<const uint16_t *>(K), k_stride,
+                         reinterpret_cast<const uint16_t *>(V), v_stride, rot, reinterpret_cast<const uint16_t *>(k_gain), queries,
+                         stream);
+}
+
+int64_t tri_cache_attend_workspace_bytes(const tri_cache *cache, const tri_sequences *seqs, int64_t T, int heads,
+                                         int64_t window, int64_t sinks)
+{
+    if (check_cache(cache, seqs) != TRI_OK || bad_attend(cache, T, heads, window, sinks)) return -1;
+    return attend_workspace_bytes(*cache, *seqs, (int)T, heads, window, sinks);
+}
+
+int tri_cache_attend(const tri_cache *cache, const tri_sequences *seqs, int64_t T, const _Float16 *Q, int64_t q_stride,
+                     int heads, float scale, int64_t window, int64_t sinks, _Float16 *O, int64_t o_stride, void *workspace,
+                     int64_t workspace_bytes, hipStream_t stream)
+{
+    const int rc = check_cache(cache, seqs);
+    if (rc != TRI_OK) return rc;
+    const int64_t row = (int64_t)heads * cache->dim;
+    if (bad_attend(cache, T, heads, window, sinks) || !Q || !O || bad_stride(q_stride, row) || bad_stride(o_stride, row)) return TRI_EINVAL;
+    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return TRI_EINVAL;           // (NaN fails)
+    const int64_t need = attend_workspace_bytes(*cache, *seqs, (int)T, heads, window, sinks);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return TRI_EINVAL;
+    if (misaligned(Q) || misaligned(O) || misaligned(workspace)) return TRI_EALIGN;
+    Attend at{};
+    at.c = *cache;
+    at.sq = *seqs;
+    at.Q = reinterpret_cast<const uint16_t *>(Q);
+    at.O = reinterpret_cast<uint16_t *>(O);
+    at.q_stride = q_stride;
+    at.o_stride = o_stride;
+    at.T = (int)T;
+    at.H = heads;
+    at.G = heads / cache->heads;
+    at.scale = scale;
+    at.window = (int)window;
+    at.sinks = (int)sinks;
+    return launch_attend(at, workspace, stream);
 }
 
 const char *tri_status_string(int code)

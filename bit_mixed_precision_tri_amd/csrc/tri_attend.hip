@@ -1,0 +1,420 @@
+// tri_attend.hip -- causal attention of new tokens over the 8-bit cache (tri_cache_attend).
+//
+// With q a row, k_j and v_j codes, s_j and u_j the scales of the keys' and values' pages, everything in base 2:
+//     x_j = scale log2(e) s_j (q . k_j),   y_j = x_j + log2 u_j,   m = max y_j,   w_j = 2^(y_j - m + 10),
+//     o = sum_j w_j v_j / sum_j (w_j / u_j).
+// The values' scales sit in the exponents, so that w_j (at most 2^10, rounded to fp16: normal numbers down to 2^-24 of the
+// largest) is the operand of the second product and the codes, exact in fp16, are the other; however small a scale is,
+// nothing underflows.  m, the two sums and o run on over the tokens (when m grows, the others shrink by 2^(m - m')).
+//
+// Both products are taken transposed: S^T = K Q^T (a row of A is a token, a column of B a query row), O^T = V^T W^T.  A lane of
+// S^T then holds weights of one query row, and they are its part of the second product's B operand as they lie: the
+// weights never leave their lanes.  Which token a row of A is can be chosen freely; rows are taken so that a lane's 16
+// weights are of 16 consecutive tokens, all in one page.
+#include "tri_cache.h"
+
+namespace tri {
+
+namespace {
+
+constexpr int kStep = 64;                        // tokens of a step
+constexpr float kLift = 10.f;                    // weights are lifted by 2^10
+constexpr float kNone = -1e30f;                  // the running maximum of a row that has seen nothing
+
+// The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
+struct Steps {
+    int head, from, tail;
+    __device__ __forceinline__ int count() const { return head + tail; }
+    __device__ __forceinline__ int at(int i) const { return i < head ? i : from + (i - head); }
+};
+__device__ __forceinline__ Steps steps_of(int pa, int pb, int window, int sinks)
+{
+    if (pb < 0) return Steps{0, 0, 0};
+    const int last = pb / kStep + 1;
+    if (window == 0) return Steps{0, 0, last};
+    const int from = max((int)((int64_t)pa - window + 1 < 0 ? 0 : pa - window + 1), 0) / kStep;
+    const int head = min((int)(((int64_t)min(sinks, pb + 1) + kStep - 1) / kStep), from);
+    return Steps{head, from, last - from};
+}
+
+// A row tile's sequence, rows and steps.  Rows are a sequence's (new token, head of the group) pairs.
+struct Tile {
+    Span sp;
+    int rows, pa, pb;                            // rows of the tile that exist; positions of the first and the last
+    Steps st;
+};
+__device__ __forceinline__ Tile tile_of(const Attend &at, int b, int r0, int height)
+{
+    Tile t;
+    t.sp = span_of(at.sq, at.T, b);
+    const int64_t R = (int64_t)t.sp.n * at.G;
+    t.rows = (int)min(max(R - r0, (int64_t)0), (int64_t)height);
+    t.pa = t.sp.p0 + r0 / at.G;
+    t.pb = t.sp.p0 + (r0 + t.rows - 1) / at.G;
+    t.st = t.rows > 0 ? steps_of(t.pa, t.pb, at.window, at.sinks) : Steps{0, 0, 0};
+    return t;
+}
+
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks)
+{
+    return j <= p && (window == 0 || p - j < window || j < sinks);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
+
+// Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float max_over_rows(float v)
+{
+    float a = v, b = v;
+    swap32(a, b);
+    a = fmaxf(a, b);
+    b = a;
+    swap16(a, b);
+    return fmaxf(a, b);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const half2_t h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+// v_mfma_f32_16x16x32_f16 (see mfma16).
+__device__ __forceinline__ float4_t mfma(half8_t a, u32x4 b, float4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
+}
+
+// Four results of a row: its sum over its denominator; 0 for a row that saw nothing (its sum is 0, too).
+template <int FMT>
+__device__ __forceinline__ void store_row(uint16_t *y, const float4_t &v, float den)
+{
+    const float n = den == 0.f ? 0.f : kCodeUnit<FMT> / den;
+    *reinterpret_cast<uint2 *>(y) = make_uint2(pack2(v[0] * n, v[1] * n), pack2(v[2] * n, v[3] * n));
+}
+
+// Few rows: 16 CT query rows of one key/value head, a split's steps dealt out to the NW waves.  splits > 1: unnormalised
+// sums, their maximum and denominator go to the workspace (part: row, split, D + 4), to be joined by k_join.
+template <int D, int FMT, int CT, int NW>
+__device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__ part, int splits, int chunk, int split, int h,
+                                           int r0, int b)
+{
+    constexpr int KL = D / 64, DT = D / 16, CS = D + 4;   // 16-byte loads of a token and lane; tiles of 16 values; LDS stride
+    __shared__ alignas(16) float so[NW][16][CS];
+    __shared__ float sm[NW][16 * CT], sl[NW][16 * CT];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, j = lane & 15;
+    const tri_cache &c = at.c;
+    const Tile t = tile_of(at, b, r0, 16 * CT);
+    if (t.rows == 0) return;
+    const int steps = t.st.count(), i0 = split * chunk, i1 = split == splits - 1 ? steps : min(steps, i0 + chunk);
+    if (split > 0 && i0 >= steps) return;        // (split 0 writes the zeros of rows that see nothing)
+
+    const int P = c.page, lp = 31 - __builtin_clz(P);
+    const int64_t head_bytes = (int64_t)P * D;
+    const float ck = at.scale * 1.44269504088896f * kCodeUnit<FMT>;
+
+    // queries: lane (g, j) holds row j's values D/4 g .. D/4 (g + 1) - 1, eight for every 32 of a product
+    u32x4 q[CT][D / 32];
+    int pos[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int r = r0 + 16 * ct + j, i = r / at.G;
+        const bool live = 16 * ct + j < t.rows;
+        pos[ct] = live ? t.sp.p0 + i : -1;
+        const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? i : 0)) * at.q_stride + (h * at.G + (live ? r % at.G : 0)) * D + (D / 4) * g;
+#pragma unroll
+        for (int s = 0; s < D / 32; ++s) q[ct][s] = *reinterpret_cast<const u32x4 *>(x + 8 * s);
+    }
+
+    float m[CT], l[CT];
+    float4_t o[CT][DT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        m[ct] = kNone;
+        l[ct] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[ct][d] = float4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // pages of step i: of this lane's rows of A in the first product (tokens 16 (j / 4) ..), and of its tokens in the second
+    // (16 g ..)
+    const int32_t *table = at.sq.table + (int64_t)b * at.sq.width;
+    auto pages = [&](int i, int &pk, int &pv) {
+        pk = pv = -1;
+        if (i >= i1) return;
+        const int64_t t0 = (int64_t)t.st.at(i) * kStep;
+        const int64_t a = (t0 + 16 * (j >> 2)) >> lp, e = (t0 + 16 * g) >> lp;
+        if (a < at.sq.width) pk = table[a];
+        if (e < at.sq.width) pv = table[e];
+        if (pk < 0 || pk >= (int)c.pages) pk = -1;
+        if (pv < 0 || pv >= (int)c.pages) pv = -1;
+    };
+    u32x4 kr[4][KL], vr[DT];
+    float sk, sv;
+    auto load_keys = [&](int i, int pk, int pv) {
+        const int t0 = t.st.at(i) * kStep;
+        const uint8_t *x = c.K + ((int64_t)max(pk, 0) * c.heads + h) * head_bytes + (D / 4) * g;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+            const int row = (t0 + 16 * (j >> 2) + 4 * tt + (j & 3)) & (P - 1);
+#pragma unroll
+            for (int k = 0; k < KL; ++k) kr[tt][k] = *reinterpret_cast<const u32x4 *>(x + row * D + 16 * k);
+        }
+        const int64_t s = (int64_t)max(pv, 0) * c.heads + h;
+        sk = c.K_scale[s];
+        sv = c.V_scale[s];
+    };
+    auto load_values = [&](int i, int pv) {
+        const int t0 = t.st.at(i) * kStep;
+        const uint8_t *x = c.V + ((int64_t)max(pv, 0) * c.heads + h) * head_bytes + ((t0 + 16 * g) & (P - 1));
+#pragma unroll
+        for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const u32x4 *>(x + (16 * d + j) * P);
+    };
+
+    int i = i0 + wv, pk, pv, nk, nv;
+    pages(i, pk, pv);
+    pages(i + NW, nk, nv);
+    if (i < i1) {
+        load_keys(i, pk, pv);
+        load_values(i, pv);
+    }
+    for (; i < i1; i += NW) {
+        const int t0 = t.st.at(i) * kStep;
+        const bool more = i + NW < i1;
+        float4_t s[CT][4];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) s[ct][tt] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const half8_t a = decode8<FMT>(kr[tt][k / 2][2 * (k % 2)], kr[tt][k / 2][2 * (k % 2) + 1]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    s[ct][tt] = mfma(a, q[ct][k], s[ct][tt]);
+            }
+        }
+        const bool here = pv >= 0;
+        const float a = ck * sk, u = here ? sv : 1.f, lu = log2_(u), iu = 1.f / u;
+        const int pv0 = pv;
+        pk = nk;
+        pv = nv;
+        if (more) load_keys(i + NW, pk, pv);
+        // every row sees all of the step, unless it reaches past the first row's position, before the last one's window
+        // (and behind the first tokens), or onto a page that is not there
+        const bool whole = t0 + kStep - 1 <= t.pa &&
+                           (at.window == 0 || t.pb - t0 < at.window || t0 + kStep <= at.sinks) && __all(pv0 >= 0);
+        u32x4 w[CT][2];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            float y[16], mx = kNone;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = fmaf(s[ct][e / 4][e % 4], a, lu);
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (!here || !sees(pos[ct], t0 + 16 * g + e, at.window, at.sinks)) y[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, y[e]);
+            mx = max_over_rows(mx);
+            if (__any(mx > m[ct])) {
+                const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
+                m[ct] = mn;
+                l[ct] *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[ct][d] *= f;
+            }
+            const float shift = kLift - m[ct];
+            float sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                y[e] = exp2_(y[e] + shift);
+                sum += y[e];
+            }
+            l[ct] = sum == 0.f ? l[ct] : fmaf(sum, iu, l[ct]);     // (a scale that no visible token has may be anything)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[ct][e / 4][e % 4] = pack2(y[2 * e], y[2 * e + 1]);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const half8_t lo = decode8<FMT>(vr[d][0], vr[d][1]), hi = decode8<FMT>(vr[d][2], vr[d][3]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) o[ct][d] = mfma(hi, w[ct][1], mfma(lo, w[ct][0], o[ct][d]));
+        }
+        if (more) load_values(i + NW, pv);
+        pages(i + 2 * NW, nk, nv);
+    }
+
+    // the waves' sums, in the waves' order
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        l[ct] = sum_over_rows(l[ct]);
+        if (g == 0) {
+            sm[wv][16 * ct + j] = m[ct];
+            sl[wv][16 * ct + j] = l[ct];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        float top = kNone;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) top = fmaxf(top, sm[k][16 * ct + j]);
+        const float f = exp2_(m[ct] - top);
+        if (ct > 0) __syncthreads();             // (the last tile's sums have been read)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) *reinterpret_cast<float4_t *>(&so[wv][j][16 * d + 4 * g]) = o[ct][d] * f;
+        __syncthreads();
+        for (int e = threadIdx.x; e < 16 * (D / 4); e += 64 * NW) {
+            const int col = e / (D / 4), d = 4 * (e % (D / 4)), r = r0 + 16 * ct + col;
+            if (16 * ct + col >= t.rows) continue;
+            float tp = kNone, den = 0.f;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) tp = fmaxf(tp, sm[k][16 * ct + col]);
+            float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                v += *reinterpret_cast<const float4_t *>(&so[k][col][d]);
+                den = fmaf(sl[k][16 * ct + col], exp2_(sm[k][16 * ct + col] - tp), den);
+            }
+            const int64_t row = (int64_t)(t.sp.r0 + r / at.G);
+            const int head = h * at.G + r % at.G;
+            if (splits == 1) {
+                store_row<FMT>(at.O + row * at.o_stride + head * D + d, v, den);
+            } else {
+                float *y = part + ((row * at.H + head) * splits + split) * (D + 4);
+                *reinterpret_cast<float4_t *>(y + d) = v;
+                if (d == 0) {
+                    y[D] = tp;
+                    y[D + 1] = den;
+                }
+            }
+        }
+    }
+}
+
+// Jobs: split (fastest), key/value head, row tile, sequence.
+template <int D, int FMT, int CT, int NW>
+__global__ __launch_bounds__(64 * NW) void k_attend_few(const Attend at, float *__restrict__ part, int splits, int chunk, int tiles,
+                                                        int64_t jobs)
+{
+    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
+        const int64_t k = job / splits, n = k / at.c.heads;
+        if (job != blockIdx.x) __syncthreads();  // (the last job's sums have been read)
+        attend_few<D, FMT, CT, NW>(at, part, splits, chunk, (int)(job % splits), (int)(k % at.c.heads), (int)(n % tiles) * 16 * CT,
+                                   (int)(n / tiles));
+    }
+}
+
+// A row's splits joined: a workgroup per row, D/4 threads for each of several splits at a time, joined in LDS in order.
+template <int D, int FMT>
+__global__ __launch_bounds__(256) void k_join(const Attend at, const float *__restrict__ part, int splits, int chunk, int height)
+{
+    constexpr int GR = 256 / (D / 4);
+    __shared__ float4_t so[GR][D / 4];
+    __shared__ float sm[GR], sl[GR];
+    const int64_t rows = (int64_t)at.T * at.H;
+    const int grp = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4);
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const int tok = (int)(row / at.H), head = (int)(row % at.H), b = owner(at.sq, tok);
+        const Span sp = span_of(at.sq, at.T, b);
+        const int i = tok - sp.r0;
+        if (i < 0 || i >= sp.n) continue;        // (the same for the whole workgroup)
+        const int r = i * at.G + head % at.G;
+        const Tile t = tile_of(at, b, r - r % height, height);
+        const int n = min(splits, max(1, (t.st.count() + chunk - 1) / chunk));
+        const float *x = part + row * splits * (D + 4);
+        float m = kNone, den = 0.f;
+        float4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int k = grp; k < n; k += GR) {
+            const float *y = x + (int64_t)k * (D + 4);
+            const float4_t w = *reinterpret_cast<const float4_t *>(y + 4 * d);
+            const float ym = y[D], mn = fmaxf(m, ym), f = exp2_(m - mn), e = exp2_(ym - mn);
+            m = mn;
+            den = den * f + y[D + 1] * e;
+            v = v * f + w * e;
+        }
+        __syncthreads();                         // (the last row's sums have been read)
+        so[grp][d] = v;
+        if (d == 0) sm[grp] = m, sl[grp] = den;
+        __syncthreads();
+        if (grp == 0) {
+#pragma unroll
+            for (int k = 1; k < GR; ++k) {
+                const float mn = fmaxf(m, sm[k]), f = exp2_(m - mn), e = exp2_(sm[k] - mn);
+                m = mn;
+                den = den * f + sl[k] * e;
+                v = v * f + so[k][d] * e;
+            }
+            store_row<FMT>(at.O + (int64_t)tok * at.o_stride + head * D + 4 * d, v, den);
+        }
+    }
+}
+
+// How a call is cut: row tiles of a sequence at most, and a tile's steps (at most) into splits of chunk steps.
+struct Plan {
+    int ct, tiles, splits, chunk;
+};
+constexpr int kWaves = 4;
+Plan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
+{
+    Plan p;
+    const int64_t G = H / c.heads, most = sq.max_new < T ? sq.max_new : T, rows = most * G;
+    p.ct = rows <= 16 || c.dim == 256 ? 1 : 2;
+    p.tiles = (int)((rows + 16 * p.ct - 1) / (16 * p.ct));
+    int64_t steps = (sq.max_len + kStep - 1) / kStep;
+    if (window > 0) {
+        const int64_t seen = (window + 16 * p.ct + kStep - 2) / kStep + 1 + ((sinks < sq.max_len ? sinks : sq.max_len) + kStep - 1) / kStep;
+        steps = steps < seen ? steps : seen;
+    }
+    const int64_t groups = sq.B * c.heads * p.tiles, want = (2 * (int64_t)cu_count() + groups - 1) / groups;
+    int64_t chunk = (steps + want - 1) / want;
+    chunk = chunk < kWaves ? kWaves : chunk;
+    p.chunk = (int)chunk;
+    p.splits = (int)((steps + chunk - 1) / chunk);
+    return p;
+}
+
+// Grids stay far below 2^32 threads; workgroups take further jobs in a loop.
+constexpr int64_t kMostGroups = 1 << 20;
+
+template <int D, int FMT>
+void attend_dim(const Attend &at, const Plan &p, float *part, hipStream_t s)
+{
+    const int64_t jobs = (int64_t)p.splits * at.c.heads * p.tiles * at.sq.B;
+    const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
+    if (p.ct == 1) k_attend_few<D, FMT, 1, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+    else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+    if (p.splits > 1) {
+        const int64_t rows = (int64_t)at.T * at.H;
+        k_join<D, FMT><<<dim3((uint32_t)(rows < kMostGroups ? rows : kMostGroups)), 256, 0, s>>>(at, part, p.splits, p.chunk, 16 * p.ct);
+    }
+}
+
+}  // namespace
+
+int64_t attend_workspace_bytes(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
+{
+    const Plan p = plan_of(c, sq, T, H, window, sinks);
+    return p.splits > 1 ? (int64_t)T * H * p.splits * (c.dim + 4) * 4 : 0;
+}
+
+int launch_attend(const Attend &at, void *workspace, hipStream_t s)
+{
+    const Plan p = plan_of(at.c, at.sq, at.T, at.H, at.window, at.sinks);
+    float *part = static_cast<float *>(workspace);
+    auto dims = [&](auto fmt) {
+        constexpr int F = decltype(fmt)::value;
+        if (at.c.dim == 64) attend_dim<64, F>(at, p, part, s);
+        else if (at.c.dim == 128) attend_dim<128, F>(at, p, part, s);
+        else attend_dim<256, F>(at, p, part, s);
+    };
+    if (at.c.fmt == TRI_KV_INT8) dims(std::integral_constant<int, TRI_KV_INT8>{});
+    else dims(std::integral_constant<int, TRI_KV_E4M3>{});
+    return hipGetLastError() == hipSuccess ? TRI_OK : TRI_EHIP;
+}
+
+}  // namespace tri

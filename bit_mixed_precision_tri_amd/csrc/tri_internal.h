@@ -205,6 +205,22 @@ bool experts_gemm_fits(const Experts &ex, int fmt);
 int launch_experts_gemm(const Experts &ex, int fmt, hipStream_t s);
 int launch_combine(const uint16_t *Z, int64_t R, const int32_t *pos, const float *weights, const uint16_t *res, int T,
                    int topk, int N, uint16_t *Y, hipStream_t s);
+// Heads and the 8-bit cache (tri_heads.hip, tri_attend.hip).
+int launch_rotate(const tri_heads *heads, int G, int T, int dim, const tri_rotary &rot, const int32_t *positions, hipStream_t s);
+int launch_append(const tri_cache &c, const tri_sequences &sq, int T, const uint16_t *K, int64_t ks, const uint16_t *V,
+                  int64_t vs, const tri_rotary *rot, const uint16_t *gain, const tri_heads *queries, hipStream_t s);
+struct Attend {
+    tri_cache c;
+    tri_sequences sq;
+    const uint16_t *Q;
+    uint16_t *O;
+    int64_t q_stride, o_stride;
+    int T, H, G;                                 // G: query heads of a key/value head
+    float scale;
+    int window, sinks;
+};
+int64_t attend_workspace_bytes(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks);
+int launch_attend(const Attend &at, void *workspace, hipStream_t s);
 int launch_probe_read(const void *src, int64_t bytes, uint32_t *sink, hipStream_t s);
 int launch_probe_copy(const void *src, void *dst, int64_t bytes, hipStream_t s);
 int launch_probe_empty(int64_t workgroups, int threads, uint32_t *sink, hipStream_t s);

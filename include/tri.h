@@ -318,6 +318,117 @@ int tri_experts_pair(const _Float16 *X, int64_t T, const int32_t *offsets, const
 int tri_experts_combine(const _Float16 *Z, int64_t R, const int32_t *pos, const float *weights,
                         const _Float16 *residual, int64_t T, int topk, int64_t N, _Float16 *Y, hipStream_t stream);
 
+/* ---- Heads, and an 8-bit cache of keys and values ---------------------------
+ * What a decoder block computes between its Q/K/V layers and its O layer: every head of the
+ * queries and keys normalised and rotated by its token's position (tri_heads_rotate), the new keys
+ * and values rounded to 8 bits into the pages of a cache (tri_cache_append, which also does the
+ * first for a call's queries and keys), and causal attention over that cache
+ * (tri_cache_attend).  Sizes that change from step to step (how many tokens a sequence gets, how
+ * long it is, which pages it has) stay on the device: no call waits, allocates, or reads anything
+ * back, and a captured call follows them. */
+enum { TRI_KV_INT8 = 0, TRI_KV_E4M3 = 1 };
+
+/* T tokens of `heads` heads of dim values: value d of head h of token t is X[t*x_stride + h*dim + d]
+ * (fp16), and of the results Y[t*y_stride + h*dim + d].  Strides are multiples of 8 and at least
+ * heads*dim; X and Y are 16-byte aligned; Y may be X with the same stride, and overlap nothing else.
+ * gain: dim fp16, 16-byte aligned, or NULL (a gain of 1); used only with a norm.  heads <= 65535. */
+typedef struct tri_heads {
+    const _Float16 *X;
+    _Float16 *Y;
+    const _Float16 *gain;
+    int64_t x_stride, y_stride;
+    int heads;
+} tri_heads;
+
+/* Norm and rotation.  norm != 0: x' = x / sqrt(mean_d x^2 + eps) * gain, eps >= 0.  table: rows x
+ * dims/2 pairs (cos, sin) of fp32, 16-byte aligned: position p turns pair i of the first dims values,
+ * (a, b) -> (a c - b s, a s + b c) with (c, s) = table[p][i]; the pair is (x[i], x[i + dims/2]), or
+ * (x[2i], x[2i+1]) where interleaved != 0.  dims is a multiple of 16, at most dim; 0 (table is then
+ * not used, and any position will do): no rotation.  All in fp32, rounded once. */
+typedef struct tri_rotary {
+    const float *table;
+    int64_t rows;
+    int dims, interleaved, norm;
+    float eps;
+} tri_rotary;
+
+/* Y = the heads of X, normalised and rotated; G <= TRI_MAX_GROUPS sets of heads (queries and keys) of the
+ * same T tokens in one launch.  positions: T int32; the rows of a token whose position lies outside
+ * 0..rows-1 are not written.  dim: 64, 128 or 256.  T*heads < 2^31 for every set.
+ * Errors: TRI_EINVAL (T < 1, a size or stride out of range, null), TRI_EALIGN, TRI_EHIP. */
+int tri_heads_rotate(const tri_heads *heads, int G, int64_t T, int dim, const tri_rotary *rot,
+                     const int32_t *positions, hipStream_t stream);
+
+/* A cache of `pages` pages of `page` tokens, `heads` key/value heads of dim values each:
+ *   K        codes, (page, head, token, dim);
+ *   V        codes, (page, head, dim, token);
+ *   K_scale, V_scale   fp32, (page, head): a code stands for its value times its page's and head's scale.
+ * Codes are int8 (two's complement, -127..127; TRI_KV_INT8) or OCP e4m3 (TRI_KV_E4M3; the two codes
+ * that are no numbers are not written, and read as +-480).  page: 16, 32, 64 or 128; dim: 64, 128 or 256;
+ * heads <= 65535; pages < 2^31.  Codes 16-byte aligned, scales 4-byte.  Scales are expected positive
+ * and finite where a token is visible. */
+typedef struct tri_cache {
+    uint8_t *K, *V;
+    float *K_scale, *V_scale;
+    int64_t pages;
+    int heads, dim, page, fmt;
+} tri_cache;
+
+/* A batch of B sequences with new tokens.  offsets: B+1 int32 on the device, not decreasing (values are
+ * clamped to 0..T): rows offsets[b] .. offsets[b+1]-1 of a call's T rows are the new tokens of sequence
+ * b.  lens: B int32 (clamped to 0..2^31 - 256), a sequence's tokens with the new ones: they stand at its last positions, row t at
+ * lens[b] - offsets[b+1] + t.  table: B x width int32, row b the pages of sequence b in order; places past
+ * its tokens, and pages that a window has left behind, may hold anything.  max_new, max_len: what a
+ * sequence's new tokens and length are at most; grids are sized by them.  Only the first max_new new
+ * tokens of a sequence are taken; a longer one than max_len is taken whole, if more slowly.  B <= 65535,
+ * width, max_new, max_len < 2^31 - 128.  Pointers 4-byte aligned. */
+typedef struct tri_sequences {
+    const int32_t *offsets, *lens, *table;
+    int64_t B, width, max_new, max_len;
+} tri_sequences;
+
+/* Round the T new tokens' keys and values to 8 bits, each at its position's page and place.  K, V: rows of
+ * cache->heads heads, strides and alignment as in tri_heads.  rot: NULL, or the norm (with k_gain, dim
+ * fp16 or NULL) and rotation that the keys go through first, rounded to fp16 there.
+ * The scale of a page and head is a power of two: the least 2^e >= 2^-30 at which the largest of the
+ * page's new values is at most 127 (int8) or 448 (e4m3) times it.  A page that holds earlier
+ * tokens keeps its scale if that is as large; else it grows to the new one, and the earlier tokens'
+ * codes are rounded again.  A code is the value times fp32(1 / scale), rounded to nearest, ties to even;
+ * infinities count as +-65504, NaN as 0.  The places behind the new tokens stay as they are.
+ * A token's keys and values are left out where its position is negative, has no place in the table of
+ * pages or (rot->dims > 0) in the rotation's, or where its page is outside 0..pages-1.
+ * queries: NULL, or (only with rot) query heads of the same T tokens, which are normalised and
+ * rotated by the same launch, as tri_heads_rotate would at these positions; rows of no sequence, behind
+ * a sequence's first max_new, or at a position that is negative or outside the rotation's table are
+ * not written.
+ * A page that gets new tokens must belong to one sequence; calls that write the same pages must be
+ * ordered.  K, V and queries must not overlap the cache.
+ * Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
+int tri_cache_append(const tri_cache *cache, const tri_sequences *seqs, int64_t T, const _Float16 *K,
+                     int64_t k_stride, const _Float16 *V, int64_t v_stride, const tri_rotary *rot,
+                     const _Float16 *k_gain, const tri_heads *queries, hipStream_t stream);
+
+/* Workspace (device bytes, a multiple of 16, or 0) that tri_cache_attend needs for these arguments; it reads no
+ * device memory.  -1 for sizes that it does not take. */
+int64_t tri_cache_attend_workspace_bytes(const tri_cache *cache, const tri_sequences *seqs, int64_t T, int heads,
+                                         int64_t window, int64_t sinks);
+
+/* Causal attention of the T new tokens' queries over the cache, in which their own keys and values stand
+ * already:  O[t][h] = sum_j p_j v_j,  p = softmax_j(scale q . k_j) over the visible positions j of the
+ * token's sequence, k_j and v_j those of key/value head h / (heads / cache->heads).  Position p sees
+ * j <= p; with window > 0 only j > p - window and the first `sinks` ones (window = 0: sinks is not
+ * used).  A position whose page is outside 0..pages-1, or that has no place in the table, is not seen.
+ * A row that sees nothing is 0; rows of no sequence (before offsets[0] or behind offsets[B]) and
+ * rows behind a sequence's first max_new stay as they are.
+ * Scores, softmax and sums are fp32; the weights, relative to the largest, enter the second product as
+ * fp16.  Q, O: rows of `heads` heads, as X and Y of tri_heads (O must not overlap Q); heads is a multiple of cache->heads;
+ * scale is finite; T*heads < 2^31.  workspace: 16-byte aligned, of at least
+ * tri_cache_attend_workspace_bytes bytes, overwritten; NULL where that is 0.  Calls that share one must
+ * be ordered.  Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
+int tri_cache_attend(const tri_cache *cache, const tri_sequences *seqs, int64_t T, const _Float16 *Q, int64_t q_stride,
+                     int heads, float scale, int64_t window, int64_t sinks, _Float16 *O, int64_t o_stride,
+                     void *workspace, int64_t workspace_bytes, hipStream_t stream);
+
 /* The algorithm tri_linear would pick for (M, N, K, fmt); TRI_EINVAL if invalid.  Up to
  * M = 16 it is TRI_ALGO_SMALLM; above, whichever of TRI_ALGO_SMALLM and TRI_ALGO_GEMM a cost
  * model fitted to MI355X timings says is faster (the small-M kernels' time grows with the
