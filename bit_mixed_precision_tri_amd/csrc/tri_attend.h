@@ -1,0 +1,92 @@
+// tri_attend.h -- what the kernels of attention over the 8-bit cache share (tri_attend.hip says what they compute).
+#pragma once
+#include "tri_cache.h"
+
+namespace tri {
+
+constexpr int kStep = 64;                        // tokens of a step
+constexpr float kLift = 10.f;                    // weights are lifted by 2^10
+constexpr float kNone = -1e30f;                  // the running maximum of a row that has seen nothing
+
+// The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
+struct Steps {
+    int head, from, tail;
+    __device__ __forceinline__ int count() const { return head + tail; }
+    __device__ __forceinline__ int at(int i) const { return i < head ? i : from + (i - head); }
+};
+__device__ __forceinline__ Steps steps_of(int pa, int pb, int window, int sinks)
+{
+    if (pb < 0) return Steps{0, 0, 0};
+    const int last = pb / kStep + 1;
+    if (window == 0) return Steps{0, 0, last};
+    const int from = max((int)((int64_t)pa - window + 1 < 0 ? 0 : pa - window + 1), 0) / kStep;
+    const int head = min((int)(((int64_t)min(sinks, pb + 1) + kStep - 1) / kStep), from);
+    return Steps{head, from, last - from};
+}
+
+// A row tile's sequence, rows and steps.  Rows are a sequence's (new token, head of the group) pairs.
+struct Tile {
+    Span sp;
+    int rows, pa, pb;                            // rows of the tile that exist; positions of the first and the last
+    Steps st;
+};
+__device__ __forceinline__ Tile tile_of(const Attend &at, int b, int r0, int height)
+{
+    Tile t;
+    t.sp = span_of(at.sq, at.T, b);
+    const int64_t R = (int64_t)t.sp.n * at.G;
+    t.rows = (int)min(max(R - r0, (int64_t)0), (int64_t)height);
+    t.pa = t.sp.p0 + r0 / at.G;
+    t.pb = t.sp.p0 + (r0 + t.rows - 1) / at.G;
+    t.st = t.rows > 0 ? steps_of(t.pa, t.pb, at.window, at.sinks) : Steps{0, 0, 0};
+    return t;
+}
+
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks)
+{
+    return j <= p && (window == 0 || p - j < window || j < sinks);
+}
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
+
+// Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float max_over_rows(float v)
+{
+    float a = v, b = v;
+    swap32(a, b);
+    a = fmaxf(a, b);
+    b = a;
+    swap16(a, b);
+    return fmaxf(a, b);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    const half2_t h = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, h);
+}
+
+// Four results of a row: its sum over its denominator; 0 for a row that saw nothing (its sum is 0, too).
+template <int FMT>
+__device__ __forceinline__ void store_row(uint16_t *y, const float4_t &v, float den)
+{
+    const float n = den == 0.f ? 0.f : kCodeUnit<FMT> / den;
+    *reinterpret_cast<uint2 *>(y) = make_uint2(pack2(v[0] * n, v[1] * n), pack2(v[2] * n, v[3] * n));
+}
+
+// How a call is cut: row tiles of `height` rows, `tiles` of them for a sequence at most, and a tile's steps (at most) into
+// splits of chunk steps.  tall: k_attend_tall's tiles.
+struct AttendPlan {
+    int height, tiles, splits, chunk;
+    bool tall;
+};
+
+// Grids stay far below 2^32 threads; workgroups take further jobs in a loop.
+constexpr int64_t kMostGroups = 1 << 20;
+
+// tri_attend_tall.hip: rows of a tile, and the launch.
+int tall_height(int dim);
+void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipStream_t s);
+
+}  // namespace tri

@@ -11,87 +11,16 @@
 // S^T then holds weights of one query row, and they are its part of the second product's B operand as they lie: the
 // weights never leave their lanes.  Which token a row of A is can be chosen freely; rows are taken so that a lane's 16
 // weights are of 16 consecutive tokens, all in one page.
-#include "tri_cache.h"
+#include "tri_attend.h"
 
 namespace tri {
 
 namespace {
 
-constexpr int kStep = 64;                        // tokens of a step
-constexpr float kLift = 10.f;                    // weights are lifted by 2^10
-constexpr float kNone = -1e30f;                  // the running maximum of a row that has seen nothing
-
-// The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
-struct Steps {
-    int head, from, tail;
-    __device__ __forceinline__ int count() const { return head + tail; }
-    __device__ __forceinline__ int at(int i) const { return i < head ? i : from + (i - head); }
-};
-__device__ __forceinline__ Steps steps_of(int pa, int pb, int window, int sinks)
-{
-    if (pb < 0) return Steps{0, 0, 0};
-    const int last = pb / kStep + 1;
-    if (window == 0) return Steps{0, 0, last};
-    const int from = max((int)((int64_t)pa - window + 1 < 0 ? 0 : pa - window + 1), 0) / kStep;
-    const int head = min((int)(((int64_t)min(sinks, pb + 1) + kStep - 1) / kStep), from);
-    return Steps{head, from, last - from};
-}
-
-// A row tile's sequence, rows and steps.  Rows are a sequence's (new token, head of the group) pairs.
-struct Tile {
-    Span sp;
-    int rows, pa, pb;                            // rows of the tile that exist; positions of the first and the last
-    Steps st;
-};
-__device__ __forceinline__ Tile tile_of(const Attend &at, int b, int r0, int height)
-{
-    Tile t;
-    t.sp = span_of(at.sq, at.T, b);
-    const int64_t R = (int64_t)t.sp.n * at.G;
-    t.rows = (int)min(max(R - r0, (int64_t)0), (int64_t)height);
-    t.pa = t.sp.p0 + r0 / at.G;
-    t.pb = t.sp.p0 + (r0 + t.rows - 1) / at.G;
-    t.st = t.rows > 0 ? steps_of(t.pa, t.pb, at.window, at.sinks) : Steps{0, 0, 0};
-    return t;
-}
-
-__device__ __forceinline__ bool sees(int p, int j, int window, int sinks)
-{
-    return j <= p && (window == 0 || p - j < window || j < sinks);
-}
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
-
-// Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ float max_over_rows(float v)
-{
-    float a = v, b = v;
-    swap32(a, b);
-    a = fmaxf(a, b);
-    b = a;
-    swap16(a, b);
-    return fmaxf(a, b);
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b)
-{
-    const half2_t h = {(_Float16)a, (_Float16)b};
-    return __builtin_bit_cast(uint32_t, h);
-}
-
 // v_mfma_f32_16x16x32_f16 (see mfma16).
 __device__ __forceinline__ float4_t mfma(half8_t a, u32x4 b, float4_t c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, b), c, 0, 0, 0);
-}
-
-// Four results of a row: its sum over its denominator; 0 for a row that saw nothing (its sum is 0, too).
-template <int FMT>
-__device__ __forceinline__ void store_row(uint16_t *y, const float4_t &v, float den)
-{
-    const float n = den == 0.f ? 0.f : kCodeUnit<FMT> / den;
-    *reinterpret_cast<uint2 *>(y) = make_uint2(pack2(v[0] * n, v[1] * n), pack2(v[2] * n, v[3] * n));
 }
 
 // Few rows: 16 CT query rows of one key/value head, a split's steps dealt out to the NW waves.  splits > 1: unnormalised
@@ -354,20 +283,17 @@ __global__ __launch_bounds__(256) void k_join(const Attend at, const float *__re
     }
 }
 
-// How a call is cut: row tiles of a sequence at most, and a tile's steps (at most) into splits of chunk steps.
-struct Plan {
-    int ct, tiles, splits, chunk;
-};
 constexpr int kWaves = 4;
-Plan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
+AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
 {
-    Plan p;
+    AttendPlan p;
     const int64_t G = H / c.heads, most = sq.max_new < T ? sq.max_new : T, rows = most * G;
-    p.ct = rows <= 16 || c.dim == 256 ? 1 : 2;
-    p.tiles = (int)((rows + 16 * p.ct - 1) / (16 * p.ct));
+    p.tall = rows > 32;
+    p.height = p.tall ? tall_height(c.dim) : rows <= 16 || c.dim == 256 ? 16 : 32;
+    p.tiles = (int)((rows + p.height - 1) / p.height);
     int64_t steps = (sq.max_len + kStep - 1) / kStep;
     if (window > 0) {
-        const int64_t seen = (window + 16 * p.ct + kStep - 2) / kStep + 1 + ((sinks < sq.max_len ? sinks : sq.max_len) + kStep - 1) / kStep;
+        const int64_t seen = (window + p.height + kStep - 2) / kStep + 1 + ((sinks < sq.max_len ? sinks : sq.max_len) + kStep - 1) / kStep;
         steps = steps < seen ? steps : seen;
     }
     const int64_t groups = sq.B * c.heads * p.tiles, want = (2 * (int64_t)cu_count() + groups - 1) / groups;
@@ -378,19 +304,18 @@ Plan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t 
     return p;
 }
 
-// Grids stay far below 2^32 threads; workgroups take further jobs in a loop.
-constexpr int64_t kMostGroups = 1 << 20;
-
 template <int D, int FMT>
-void attend_dim(const Attend &at, const Plan &p, float *part, hipStream_t s)
+void attend_dim(const Attend &at, const AttendPlan &p, float *part, hipStream_t s)
 {
-    const int64_t jobs = (int64_t)p.splits * at.c.heads * p.tiles * at.sq.B;
-    const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
-    if (p.ct == 1) k_attend_few<D, FMT, 1, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
-    else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+    if (!p.tall) {
+        const int64_t jobs = (int64_t)p.splits * at.c.heads * p.tiles * at.sq.B;
+        const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
+        if (p.height == 16) k_attend_few<D, FMT, 1, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+        else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+    }
     if (p.splits > 1) {
         const int64_t rows = (int64_t)at.T * at.H;
-        k_join<D, FMT><<<dim3((uint32_t)(rows < kMostGroups ? rows : kMostGroups)), 256, 0, s>>>(at, part, p.splits, p.chunk, 16 * p.ct);
+        k_join<D, FMT><<<dim3((uint32_t)(rows < kMostGroups ? rows : kMostGroups)), 256, 0, s>>>(at, part, p.splits, p.chunk, p.height);
     }
 }
 
@@ -398,14 +323,15 @@ void attend_dim(const Attend &at, const Plan &p, float *part, hipStream_t s)
 
 int64_t attend_workspace_bytes(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
 {
-    const Plan p = plan_of(c, sq, T, H, window, sinks);
+    const AttendPlan p = plan_of(c, sq, T, H, window, sinks);
     return p.splits > 1 ? (int64_t)T * H * p.splits * (c.dim + 4) * 4 : 0;
 }
 
 int launch_attend(const Attend &at, void *workspace, hipStream_t s)
 {
-    const Plan p = plan_of(at.c, at.sq, at.T, at.H, at.window, at.sinks);
+    const AttendPlan p = plan_of(at.c, at.sq, at.T, at.H, at.window, at.sinks);
     float *part = static_cast<float *>(workspace);
+    if (p.tall) launch_attend_tall(at, p, part, s);
     auto dims = [&](auto fmt) {
         constexpr int F = decltype(fmt)::value;
         if (at.c.dim == 64) attend_dim<64, F>(at, p, part, s);
