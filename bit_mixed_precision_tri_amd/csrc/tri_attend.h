@@ -50,6 +50,10 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks)
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
+// A scale within the normal numbers: where no token is visible a page's may be anything, and nothing may come of it that is
+// no number (a visible token's is positive and finite; 0 times the call's scale counts as 10^-37).
+__device__ __forceinline__ float usable(float s) { return fminf(fmaxf(s, 1e-37f), 1e37f); }
+
 // Maximum over lanes l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ float max_over_rows(float v)
 {

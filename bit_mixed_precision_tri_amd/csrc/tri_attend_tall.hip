@@ -6,6 +6,7 @@
 // v_mfma_f32_32x32x16_f16: a lane holds 16 weights of one row for every 32 tokens, which are its B operand of the second
 // product as they lie; values are stored in LDS in the order of a lane's tokens, so that an A operand is one 16-byte read.
 #include "tri_attend.h"
+#include <cstdlib>
 
 namespace tri {
 
@@ -52,7 +53,8 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     if (split > 0 && i0 >= steps64) return;
     const int P = c.page, lp = 31 - __builtin_clz(P);
     const int64_t head_bytes = (int64_t)P * D;
-    const float ck = at.scale * 1.44269504088896f * kCodeUnit<FMT>;
+    const float ck = fabsf(at.scale) * 1.44269504088896f * kCodeUnit<FMT>;    // (the scale's sign goes into q)
+    const uint32_t flip = at.scale < 0.f ? 0x80008000u : 0u;
     const int n0 = i0 * F, n1 = i1 * F;
     auto token_of = [&](int n) { return t.st.at(n / F) * kStep + (n % F) * STEP; };
 
@@ -66,7 +68,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         pos[ct] = live ? t.sp.p0 + i : -1;
         const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? i : 0)) * at.q_stride + (h * at.G + (live ? r % at.G : 0)) * D + 8 * hf;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) q[ct][s] = *reinterpret_cast<const half8_t *>(x + 16 * s);
+        for (int s = 0; s < D / 16; ++s) q[ct][s] = __builtin_bit_cast(half8_t, *reinterpret_cast<const u32x4 *>(x + 16 * s) ^ flip);
     }
     {
         const int w0 = wv * QT * 32, w1 = min(w0 + QT * 32, t.rows) - 1;
@@ -76,35 +78,38 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         }
     }
 
-    // codes on their way to LDS
+    // codes on their way to LDS: pages of a thread's pieces a step ahead of the pieces themselves
     const int32_t *table = at.sq.table + (int64_t)b * at.sq.width;
+    const int last_page = (int)at.sq.width - 1;
     u32x4 kr[KU], vr[VU];
     float sk = 0.f, sv = 0.f;
     bool here = false;
-    auto page_of = [&](int64_t token) {
-        const int64_t a = token >> lp;
-        const int id = a < at.sq.width ? table[a] : -1;
-        return id >= 0 && id < (int)c.pages ? id : -1;
+    int kid[KU], vid;                                    // (a thread's pieces of V are of one block of 16 tokens)
+    static_assert(NT % BLK == 0, "");
+    auto look = [&](int n) {                             // (what the table holds: nothing here waits for it)
+        const int t0 = token_of(n);
+#pragma unroll
+        for (int k = 0; k < KU; ++k) kid[k] = table[min((t0 + (k * NT + tid) / (D / 16)) >> lp, last_page)];
+        vid = table[min((t0 + 16 * (tid % BLK)) >> lp, last_page)];
     };
     auto load = [&](int n) {
         const int t0 = token_of(n);
 #pragma unroll
         for (int k = 0; k < KU; ++k) {
             const int u = k * NT + tid, tok = u / (D / 16), piece = u % (D / 16);
-            const int id = max(page_of((int64_t)t0 + tok), 0);
-            kr[k] = *reinterpret_cast<const u32x4 *>(c.K + ((int64_t)id * c.heads + h) * head_bytes + ((t0 + tok) & (P - 1)) * D + 16 * piece);
+            const int id = (uint32_t)kid[k] < (uint32_t)c.pages ? kid[k] : 0;    // (a page that is not there: any one's codes)
+            kr[k] = *reinterpret_cast<const u32x4 *>(c.K + ((int64_t)id * c.heads + h) * head_bytes +
+                                                     (((t0 + tok) & (P - 1)) * D + 16 * piece));
         }
+        const bool ok = (uint32_t)vid < (uint32_t)c.pages;
+        const int64_t at_v = (int64_t)(ok ? vid : 0) * c.heads + h;
+        const uint8_t *v = c.V + at_v * head_bytes + ((t0 + 16 * (tid % BLK)) & (P - 1));
 #pragma unroll
-        for (int k = 0; k < VU; ++k) {
-            const int u = k * NT + tid, blk = u % BLK, d = u / BLK;
-            const int id = max(page_of((int64_t)t0 + 16 * blk), 0);
-            vr[k] = *reinterpret_cast<const u32x4 *>(c.V + ((int64_t)id * c.heads + h) * head_bytes + d * P + ((t0 + 16 * blk) & (P - 1)));
-        }
+        for (int k = 0; k < VU; ++k) vr[k] = *reinterpret_cast<const u32x4 *>(v + ((k * NT + tid) / BLK) * P);
         if (tid < BLK) {
-            const int id = page_of((int64_t)t0 + 16 * tid);
-            here = id >= 0;
-            sk = c.K_scale[(int64_t)max(id, 0) * c.heads + h];
-            sv = c.V_scale[(int64_t)max(id, 0) * c.heads + h];
+            here = ok && (t0 + 16 * tid) >> lp <= last_page;
+            sk = c.K_scale[at_v];
+            sv = c.V_scale[at_v];
         }
     };
     auto put = [&](int buf) {
@@ -122,8 +127,9 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             vb[chunk_at<VC>(d, 2 * blk + 1)] = __builtin_bit_cast(u32x4, decode8<FMT>(vr[k][1], vr[k][3]));
         }
         if (tid < BLK) {
-            const float u = here ? sv : 1.f;
-            meta_at[buf * BLK + tid] = u32x4{__float_as_uint(ck * sk), __float_as_uint(log2_(u)), __float_as_uint(1.f / u), here ? 1u : 0u};
+            const float u = usable(sv);
+            meta_at[buf * BLK + tid] = u32x4{__float_as_uint(usable(ck * sk)), __float_as_uint(log2_(u)), __float_as_uint(1.f / u),
+                                             here ? 1u : 0u};
         }
     };
 
@@ -139,33 +145,50 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             for (int e = 0; e < 16; ++e) o[ct][d][e] = 0.f;
     }
 
+    const int key0 = 16 * chunk_at<KC>(l, hf), val0 = 16 * (STEP * KC + chunk_at<VC>(l, hf));
     if (n0 < n1) {
+        look(n0);
         load(n0);
+        if (n0 + 1 < n1) look(n0 + 1);
         put(0);
         if (n0 + 1 < n1) load(n0 + 1);
+        if (n0 + 2 < n1) look(n0 + 2);
     }
     for (int n = n0; n < n1; ++n) {
         const int buf = (n - n0) & 1, t0 = token_of(n);
         __syncthreads();
         if (n + 1 < n1) put(buf ^ 1);
         if (n + 2 < n1) load(n + 2);
+        if (n + 3 < n1) look(n + 3);
         // nothing of the step for this wave: it lies behind its last row, or between the first tokens and its first row's window
         if (t0 > wb || (at.window > 0 && wa - (t0 + STEP - 1) >= at.window && t0 >= at.sinks)) continue;
-        const u32x4 *kb = lds + buf * BUF, *vb = kb + STEP * KC;
+        const char *const bytes = reinterpret_cast<const char *>(lds) + buf * (BUF * 16);
+        // A operands: chunk 2 k + hf of a row, where chunk_at puts it (its exclusive or with 2 k is one of the byte address, too)
+        auto key = [&](int tt, int k) { return *reinterpret_cast<const half8_t *>(bytes + (key0 ^ (32 * k)) + tt * (32 * KC * 16)); };
+        auto val = [&](int d, int k) { return *reinterpret_cast<const half8_t *>(bytes + (val0 ^ (32 * k)) + d * (32 * VC * 16)); };
         float16_t s[QT][TT];
+        half8_t ka[2][TT], va[2][DT];
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) {
+        for (int tt = 0; tt < TT; ++tt) ka[0][tt] = key(tt, 0);
 #pragma unroll
-            for (int ct = 0; ct < QT; ++ct)
+        for (int k = 0; k < D / 16; ++k) {
+            if (k + 1 < D / 16) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) s[ct][tt][e] = 0.f;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const half8_t a = __builtin_bit_cast(half8_t, kb[chunk_at<KC>(32 * tt + l, 2 * k + hf)]);
-#pragma unroll
-                for (int ct = 0; ct < QT; ++ct) s[ct][tt] = mfma32(a, q[ct][k], s[ct][tt]);
+                for (int tt = 0; tt < TT; ++tt) ka[(k + 1) & 1][tt] = key(tt, k + 1);
             }
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+                for (int ct = 0; ct < QT; ++ct) {
+                    if (k == 0) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) s[ct][tt][e] = 0.f;
+                    }
+                    s[ct][tt] = mfma32(ka[k & 1][tt], q[ct][k], s[ct][tt]);
+                }
         }
+#pragma unroll
+        for (int d = 0; d < DT; ++d) va[0][d] = val(d, 0);
         float a[BLK], lu[BLK], iu[BLK];
         uint32_t there = 1u;
 #pragma unroll
@@ -181,19 +204,24 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         half8_t w[QT][BLK];
 #pragma unroll
         for (int ct = 0; ct < QT; ++ct) {
+            if (!whole) {
+#pragma unroll
+                for (int k = 0; k < BLK; ++k) {
+                    const int p = meta_at[buf * BLK + k][3] != 0u ? pos[ct] : -1;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (!sees(p, t0 + 16 * k + 8 * (e / 4) + 4 * hf + e % 4, at.window, at.sinks)) s[ct][k / 2][8 * (k % 2) + e] = -INFINITY;
+                }
+            }
+            // the largest y of a block is its largest score's (a > 0)
             float mx = kNone;
 #pragma unroll
-            for (int k = 0; k < BLK; ++k)
+            for (int k = 0; k < BLK; ++k) {
+                float top = s[ct][k / 2][8 * (k % 2)];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float &x = reinterpret_cast<float *>(&s[ct][k / 2])[8 * (k % 2) + e];
-                    x = fmaf(x, a[k], lu[k]);
-                    if (!whole) {
-                        const int j = t0 + 16 * k + 8 * (e / 4) + 4 * hf + e % 4;
-                        if (meta_at[buf * BLK + k][3] == 0u || !sees(pos[ct], j, at.window, at.sinks)) x = -INFINITY;
-                    }
-                    mx = fmaxf(mx, x);
-                }
+                for (int e = 1; e < 8; ++e) top = fmaxf(top, s[ct][k / 2][8 * (k % 2) + e]);
+                mx = fmaxf(mx, fmaf(top, a[k], lu[k]));
+            }
             float other = mx;
             swap32(mx, other);
             mx = fmaxf(mx, other);
@@ -204,27 +232,30 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
-            const float shift = kLift - m[ct];
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
-                float y[8], add = 0.f;
+                const float shift = lu[k] + (kLift - m[ct]);
+                float y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    y[e] = exp2_(s[ct][k / 2][8 * (k % 2) + e] + shift);
-                    add += y[e];
-                }
-                sum[ct] = add == 0.f ? sum[ct] : fmaf(add, iu[k], sum[ct]);    // (a scale that no visible token has may be anything)
-                w[ct][k] = __builtin_bit_cast(half8_t, u32x4{pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])});
+                for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
+                const u32x4 pk = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+                // (the denominator takes the weights as they are: of values of small scale, nothing may be left of them in fp16)
+                const float add = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
+                sum[ct] = fmaf(add, iu[k], sum[ct]);
+                w[ct][k] = __builtin_bit_cast(half8_t, pk);
             }
         }
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
+        for (int k = 0; k < BLK; ++k) {
+            if (k + 1 < BLK) {
 #pragma unroll
-            for (int k = 0; k < BLK; ++k) {
-                const half8_t v = __builtin_bit_cast(half8_t, vb[chunk_at<VC>(32 * d + l, 2 * k + hf)]);
-#pragma unroll
-                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(v, w[ct][k], o[ct][d]);
+                for (int d = 0; d < DT; ++d) va[(k + 1) & 1][d] = val(d, k + 1);
             }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], w[ct][k], o[ct][d]);
+        }
     }
 
 #pragma unroll
@@ -258,7 +289,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 // row tile, the last one (which sees most) first.
 template <int D, int FMT, int QT, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, int splits, int chunk, int tiles,
-                                                            int64_t jobs)
+                                                            int64_t jobs, bool fold)
 {
     constexpr int STEP = kTallStep<D>;
     __shared__ u32x4 lds[2 * (STEP * (D / 8) + D * (STEP / 8)) + 2 * (STEP / 16)];
@@ -266,8 +297,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attend_tall(const
     for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
         const int64_t k = job % pairs, n = job / pairs;
         if (job != blockIdx.x) __syncthreads();  // (the last job's steps have been read)
-        attend_tall<D, FMT, QT, NW>(at, part, splits, chunk, (int)(n % splits), (int)(k % at.c.heads),
-                                    (tiles - 1 - (int)(n / splits)) * (32 * QT * NW), (int)(k / at.c.heads), lds);
+        const int y = (int)(n / splits), tile = fold && y >= (tiles + 1) / 2 ? y - (tiles + 1) / 2 : tiles - 1 - y;
+        attend_tall<D, FMT, QT, NW>(at, part, splits, chunk, (int)(n % splits), (int)(k % at.c.heads), tile * (32 * QT * NW),
+                                    (int)(k / at.c.heads), lds);
     }
 }
 
@@ -285,7 +317,7 @@ void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipS
     const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
     auto go = [&](auto dim, auto fmt) {
         constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
-        k_attend_tall<D, F, kTallCols<D>, kTallWaves<D>><<<grid, 64 * kTallWaves<D>, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
+        k_attend_tall<D, F, kTallCols<D>, kTallWaves<D>><<<grid, 64 * kTallWaves<D>, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs, getenv("FOLD") != nullptr);
     };
     auto dims = [&](auto fmt) {
         if (at.c.dim == 64) go(std::integral_constant<int, 64>{}, fmt);

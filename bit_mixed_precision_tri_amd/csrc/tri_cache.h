@@ -89,8 +89,10 @@ __device__ __forceinline__ uint2 decode4(uint32_t w)
         return make_uint2(__builtin_bit_cast(uint32_t, (half2_t)(as_h2(perm(0x64646464u, u, 0x04010400u)) - off)),
                           __builtin_bit_cast(uint32_t, (half2_t)(as_h2(perm(0x64646464u, u, 0x04030402u)) - off)));
     } else {
-        const uint32_t a = perm(0u, w, 0x010C000Cu), b = perm(0u, w, 0x030C020Cu);
-        return make_uint2(((a >> 1) & 0x3F803F80u) | (a & 0x80008000u), ((b >> 1) & 0x3F803F80u) | (b & 0x80008000u));
+        typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+        const i16x2 a = __builtin_bit_cast(i16x2, perm(0u, w, 0x010C000Cu)) >> (int16_t)1;    // sign, sign, exponent, fraction
+        const i16x2 b = __builtin_bit_cast(i16x2, perm(0u, w, 0x030C020Cu)) >> (int16_t)1;
+        return make_uint2(__builtin_bit_cast(uint32_t, a) & 0xBF80BF80u, __builtin_bit_cast(uint32_t, b) & 0xBF80BF80u);
     }
 }
 // Eight codes, an operand of a product.
