@@ -80,14 +80,32 @@ __device__ __forceinline__ void store_row(uint16_t *y, const float4_t &v, float 
 }
 
 // How a call is cut: row tiles of `height` rows, `tiles` of them for a sequence at most, and a tile's steps (at most) into
-// splits of chunk steps.  tall: k_attend_tall's tiles.
+// splits of chunk steps.  tall: k_attend_tall's tiles; pair: with two groups of waves each, which take the steps in turn.
 struct AttendPlan {
     int height, tiles, splits, chunk;
-    bool tall;
+    bool tall, pair;
 };
 
-// Grids stay far below 2^32 threads; workgroups take further jobs in a loop.
-constexpr int64_t kMostGroups = 1 << 20;
+// One launch's part of a call: seqs sequences from seq0 on, tiles row tiles of each from tile0 on.
+struct AttendGrid {
+    int seq0, seqs, tile0, tiles;
+};
+
+// A grid has fewer than 2^32 threads: as many launches as that takes (one, but for bounds of millions of tiles), each of at most
+// 2^22 workgroups of up to 512 threads.  (heads * splits is far below: a split has at least kLeastChunk steps.)
+template <typename Launch>
+void for_grids(const Attend &at, const AttendPlan &p, Launch launch)
+{
+    const int64_t most = 1 << 22, one = (int64_t)at.c.heads * p.splits;
+    const int64_t tiles = p.tiles * one <= most ? p.tiles : most / one > 0 ? most / one : 1;
+    const int64_t seqs = tiles * one * at.sq.B <= most ? at.sq.B : most / (tiles * one) > 0 ? most / (tiles * one) : 1;
+    for (int64_t b = 0; b < at.sq.B; b += seqs)
+        for (int64_t t = 0; t < p.tiles; t += tiles) {
+            const AttendGrid gd = {(int)b, (int)(seqs < at.sq.B - b ? seqs : at.sq.B - b), (int)t,
+                                   (int)(tiles < p.tiles - t ? tiles : p.tiles - t)};
+            launch(gd, (uint32_t)(gd.seqs * (int64_t)gd.tiles * one));
+        }
+}
 
 // tri_attend_tall.hip: rows of a tile, and the launch.
 int tall_height(int dim);

@@ -224,17 +224,13 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
     }
 }
 
-// Jobs: split (fastest), key/value head, row tile, sequence.
+// Workgroups: split (fastest), key/value head, row tile, sequence.
 template <int D, int FMT, int CT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attend_few(const Attend at, float *__restrict__ part, int splits, int chunk, int tiles,
-                                                        int64_t jobs)
+__global__ __launch_bounds__(64 * NW) void k_attend_few(const Attend at, float *__restrict__ part, const AttendPlan p, const AttendGrid gd)
 {
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int64_t k = job / splits, n = k / at.c.heads;
-        if (job != blockIdx.x) __syncthreads();  // (the last job's sums have been read)
-        attend_few<D, FMT, CT, NW>(at, part, splits, chunk, (int)(job % splits), (int)(k % at.c.heads), (int)(n % tiles) * 16 * CT,
-                                   (int)(n / tiles));
-    }
+    const uint32_t k = blockIdx.x / p.splits, n = k / at.c.heads;
+    attend_few<D, FMT, CT, NW>(at, part, p.splits, p.chunk, (int)(blockIdx.x % p.splits), (int)(k % at.c.heads),
+                               (gd.tile0 + (int)(n % gd.tiles)) * 16 * CT, gd.seq0 + (int)(n / gd.tiles));
 }
 
 // A row's splits joined: a workgroup per row, D/4 threads for each of several splits at a time, joined in LDS in order.
@@ -284,6 +280,9 @@ __global__ __launch_bounds__(256) void k_join(const Attend at, const float *__re
 }
 
 constexpr int kWaves = 4;
+// Workgroups of k_join: it takes further rows in a loop.
+constexpr int64_t kMostGroups = 1 << 20;
+
 AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
 {
     AttendPlan p;
@@ -296,9 +295,15 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
         const int64_t seen = (window + p.height + kStep - 2) / kStep + 1 + ((sinks < sq.max_len ? sinks : sq.max_len) + kStep - 1) / kStep;
         steps = steps < seen ? steps : seen;
     }
-    const int64_t groups = sq.B * c.heads * p.tiles, want = (2 * (int64_t)cu_count() + groups - 1) / groups;
+    const int64_t groups = sq.B * c.heads * p.tiles, cus = cu_count();
+    // Tall tiles: one pass over a tile's steps, unless the tiles leave half the CUs idle (what joins splits moves as much as many
+    // steps do).  Up to two tiles per CU, the longest tile's steps are what the call waits for: two groups of waves share them
+    // (2048 tokens of 32 heads, 512 tiles: 62 -> 57 us; 880 tiles of two chunks over a window: 97 us, 114 with pairs).
+    p.pair = p.tall && groups <= 2 * cus;
+    const int64_t want = p.tall ? (groups * 2 > cus ? 1 : cus / groups) : (2 * cus + groups - 1) / groups;
     int64_t chunk = (steps + want - 1) / want;
-    chunk = chunk < kWaves ? kWaves : chunk;
+    const int64_t least = p.tall ? 16 : kWaves;
+    chunk = chunk < least ? least : chunk;
     p.chunk = (int)chunk;
     p.splits = (int)((steps + chunk - 1) / chunk);
     return p;
@@ -307,12 +312,11 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
 template <int D, int FMT>
 void attend_dim(const Attend &at, const AttendPlan &p, float *part, hipStream_t s)
 {
-    if (!p.tall) {
-        const int64_t jobs = (int64_t)p.splits * at.c.heads * p.tiles * at.sq.B;
-        const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
-        if (p.height == 16) k_attend_few<D, FMT, 1, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
-        else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<grid, 64 * kWaves, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs);
-    }
+    if (!p.tall)
+        for_grids(at, p, [&](const AttendGrid &gd, uint32_t groups) {
+            if (p.height == 16) k_attend_few<D, FMT, 1, kWaves><<<groups, 64 * kWaves, 0, s>>>(at, part, p, gd);
+            else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<groups, 64 * kWaves, 0, s>>>(at, part, p, gd);
+        });
     if (p.splits > 1) {
         const int64_t rows = (int64_t)at.T * at.H;
         k_join<D, FMT><<<dim3((uint32_t)(rows < kMostGroups ? rows : kMostGroups)), 256, 0, s>>>(at, part, p.splits, p.chunk, p.height);

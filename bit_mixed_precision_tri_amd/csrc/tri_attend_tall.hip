@@ -6,7 +6,6 @@
 // v_mfma_f32_32x32x16_f16: a lane holds 16 weights of one row for every 32 tokens, which are its B operand of the second
 // product as they lie; values are stored in LDS in the order of a lane's tokens, so that an A operand is one 16-byte read.
 #include "tri_attend.h"
-#include <cstdlib>
 
 namespace tri {
 
@@ -21,9 +20,15 @@ __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
+// Weights are lifted by 2^6 and may grow to 2^14 before the maximum is moved: every row's maximum grows a few times, some row's
+// of a wave in most steps.
+constexpr float kTallLift = 6.f, kSlack = 8.f;
+
 template <int D> constexpr int kTallStep = D == 256 ? 32 : 64;   // tokens of a step here
-template <int D> constexpr int kTallWaves = 4;
-template <int D> constexpr int kTallCols = 1;
+template <int D> constexpr int kTallWaves = 4;                   // waves that share a step
+template <int D> constexpr int kTallCols = 1;                    // tiles of 32 rows of a wave
+// LDS of a group in 16-byte chunks: two buffers of keys, values and what belongs to 16 tokens.
+template <int D> constexpr int kTallLds = 4 * D * (kTallStep<D> / 8) + 2 * (kTallStep<D> / 16);
 
 // 16-byte chunk c of row r among rows of N chunks: placed so that 16 lanes that read one chunk of 16 rows meet all banks.
 template <int N>
@@ -33,7 +38,7 @@ __device__ __forceinline__ int chunk_at(int r, int c)
     return r * N + (c ^ ((r / per) & (N >= 16 ? 15 : N - 1)));
 }
 
-template <int D, int FMT, int QT, int NW>
+template <int D, int FMT, int QT, int NW, int NG>
 __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict__ part, int splits, int chunk, int split, int h, int r0,
                                             int b, u32x4 *lds)
 {
@@ -41,9 +46,11 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     constexpr int KC = D / 8, VC = STEP / 8;             // chunks of a key's and a value's row
     constexpr int KU = STEP * D / 16 / NT, VU = KU;      // 16-byte pieces of codes per thread
     constexpr int BLK = STEP / 16, TT = STEP / 32, DT = D / 32;
-    constexpr int BUF = STEP * KC + D * VC;              // chunks of a buffer
-    u32x4 *const meta_at = lds + 2 * BUF;                // (a, log2 u, 1 / u, whether the page is there) of 16 tokens
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), hf = lane >> 5, l = lane & 31;
+    const int gr = __builtin_amdgcn_readfirstlane(threadIdx.x / NT), tid = threadIdx.x % NT;
+    u32x4 *const all = lds;
+    lds += gr * kTallLds<D>;
+    u32x4 *const meta_at = lds + 4 * D * VC;             // (a, log2 u, 1 / u, whether the page is there) of 16 tokens
+    const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), hf = lane >> 5, l = lane & 31;
     const tri_cache &c = at.c;
     const Tile t = tile_of(at, b, r0, HEIGHT);
     if (t.rows == 0) return;
@@ -55,7 +62,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     const int64_t head_bytes = (int64_t)P * D;
     const float ck = fabsf(at.scale) * 1.44269504088896f * kCodeUnit<FMT>;    // (the scale's sign goes into q)
     const uint32_t flip = at.scale < 0.f ? 0x80008000u : 0u;
-    const int n0 = i0 * F, n1 = i1 * F;
+    const int n0 = i0 * F + gr, n1 = i1 * F, rounds = (n1 - i0 * F + NG - 1) / NG;    // (the same for all groups)
     auto token_of = [&](int n) { return t.st.at(n / F) * kStep + (n % F) * STEP; };
 
     // this wave's rows
@@ -78,53 +85,73 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         }
     }
 
-    // codes on their way to LDS: pages of a thread's pieces a step ahead of the pieces themselves
+    // Codes on their way to LDS; pages are looked up a step ahead of the codes.  A wave's piece of keys is of 16 tokens at most,
+    // so of one page (its number goes into scalar registers); its values are of one page where a page holds the step, else of
+    // a page per lane.
     const int32_t *table = at.sq.table + (int64_t)b * at.sq.width;
     const int last_page = (int)at.sq.width - 1;
+    const bool big = P >= STEP;
     u32x4 kr[KU], vr[VU];
     float sk = 0.f, sv = 0.f;
     bool here = false;
-    int kid[KU], vid;                                    // (a thread's pieces of V are of one block of 16 tokens)
-    static_assert(NT % BLK == 0, "");
+    int kid[KU], vid = 0;
+    static_assert(NT % BLK == 0 && 64 / (D / 16) <= 16, "");
+    const int koff = ((tid / (D / 16)) & (P - 1)) * D + 16 * (tid % (D / 16)), ktok = wv * 64 / (D / 16);
+    const int voff = (tid / BLK) * P + ((16 * (tid % BLK)) & (P - 1));
     auto look = [&](int n) {                             // (what the table holds: nothing here waits for it)
         const int t0 = token_of(n);
 #pragma unroll
-        for (int k = 0; k < KU; ++k) kid[k] = table[min((t0 + (k * NT + tid) / (D / 16)) >> lp, last_page)];
-        vid = table[min((t0 + 16 * (tid % BLK)) >> lp, last_page)];
+        for (int k = 0; k < KU; ++k)
+            if (k == 0 || !big) kid[k] = table[min((t0 + k * (NT / (D / 16)) + ktok) >> lp, last_page)];
+        if (!big) vid = table[min((t0 + 16 * (tid % BLK)) >> lp, last_page)];
     };
     auto load = [&](int n) {
-        const int t0 = token_of(n);
+        const int t0 = token_of(n), in = t0 & (P - 1);   // (0 where a page is smaller than a step)
+        const int first = __builtin_amdgcn_readfirstlane(kid[0]);
 #pragma unroll
         for (int k = 0; k < KU; ++k) {
-            const int u = k * NT + tid, tok = u / (D / 16), piece = u % (D / 16);
-            const int id = (uint32_t)kid[k] < (uint32_t)c.pages ? kid[k] : 0;    // (a page that is not there: any one's codes)
-            kr[k] = *reinterpret_cast<const u32x4 *>(c.K + ((int64_t)id * c.heads + h) * head_bytes +
-                                                     (((t0 + tok) & (P - 1)) * D + 16 * piece));
+            const int id = big ? first : __builtin_amdgcn_readfirstlane(kid[k]);
+            const uint8_t *x = c.K + ((int64_t)((uint32_t)id < (uint32_t)c.pages ? id : 0) * c.heads + h) * head_bytes;   // (none: any one's)
+            kr[k] = *reinterpret_cast<const u32x4 *>(x + (big ? (in + k * (NT / (D / 16))) * D : ((k * (NT / (D / 16))) & (P - 1)) * D) + koff);
         }
-        const bool ok = (uint32_t)vid < (uint32_t)c.pages;
-        const int64_t at_v = (int64_t)(ok ? vid : 0) * c.heads + h;
-        const uint8_t *v = c.V + at_v * head_bytes + ((t0 + 16 * (tid % BLK)) & (P - 1));
+        if (big) {
+            const bool ok = (uint32_t)first < (uint32_t)c.pages;
+            const int64_t pg = (int64_t)(ok ? first : 0) * c.heads + h;
+            const uint8_t *x = c.V + pg * head_bytes + in;
 #pragma unroll
-        for (int k = 0; k < VU; ++k) vr[k] = *reinterpret_cast<const u32x4 *>(v + ((k * NT + tid) / BLK) * P);
-        if (tid < BLK) {
-            here = ok && (t0 + 16 * tid) >> lp <= last_page;
-            sk = c.K_scale[at_v];
-            sv = c.V_scale[at_v];
+            for (int k = 0; k < VU; ++k) vr[k] = *reinterpret_cast<const u32x4 *>(x + (k * (NT / BLK) * P + voff));
+            here = ok && (t0 >> lp) <= last_page;
+            sk = c.K_scale[pg];
+            sv = c.V_scale[pg];
+        } else {
+            const bool ok = (uint32_t)vid < (uint32_t)c.pages;
+            const int64_t pg = (int64_t)(ok ? vid : 0) * c.heads + h;
+            const uint8_t *x = c.V + pg * head_bytes;
+#pragma unroll
+            for (int k = 0; k < VU; ++k) vr[k] = *reinterpret_cast<const u32x4 *>(x + (k * (NT / BLK) * P + voff));
+            if (tid < BLK) {
+                here = ok && (t0 + 16 * tid) >> lp <= last_page;
+                sk = c.K_scale[pg];
+                sv = c.V_scale[pg];
+            }
         }
     };
+    // where they go: rows k * NT / .. further lie that much further on (chunk_at's pattern repeats within them)
+    const int kput = 16 * chunk_at<KC>(tid / (D / 16), 2 * (tid % (D / 16)));
+    const int vput = 16 * (STEP * KC + chunk_at<VC>(tid / BLK, 2 * (tid % BLK)));
+    static_assert(NT / (D / 16) % 16 == 0 && NT / BLK % 16 == 0, "");
     auto put = [&](int buf) {
-        u32x4 *kb = lds + buf * BUF, *vb = kb + STEP * KC;
+        char *const x = reinterpret_cast<char *>(lds) + buf * (2 * D * VC * 16);
 #pragma unroll
         for (int k = 0; k < KU; ++k) {
-            const int u = k * NT + tid, tok = u / (D / 16), piece = u % (D / 16);
-            kb[chunk_at<KC>(tok, 2 * piece)] = __builtin_bit_cast(u32x4, decode8<FMT>(kr[k][0], kr[k][1]));
-            kb[chunk_at<KC>(tok, 2 * piece + 1)] = __builtin_bit_cast(u32x4, decode8<FMT>(kr[k][2], kr[k][3]));
+            *reinterpret_cast<half8_t *>(x + kput + k * (NT / (D / 16) * KC * 16)) = decode8<FMT>(kr[k][0], kr[k][1]);
+            *reinterpret_cast<half8_t *>(x + (kput ^ 16) + k * (NT / (D / 16) * KC * 16)) = decode8<FMT>(kr[k][2], kr[k][3]);
         }
 #pragma unroll
         for (int k = 0; k < VU; ++k) {
-            const int u = k * NT + tid, blk = u % BLK, d = u / BLK;
-            vb[chunk_at<VC>(d, 2 * blk)] = __builtin_bit_cast(u32x4, decode8<FMT>(vr[k][0], vr[k][2]));
-            vb[chunk_at<VC>(d, 2 * blk + 1)] = __builtin_bit_cast(u32x4, decode8<FMT>(vr[k][1], vr[k][3]));
+            char *const v = x + k * (NT / BLK * VC * 16);
+            *reinterpret_cast<half8_t *>(v + vput) = decode8<FMT>(vr[k][0], vr[k][2]);
+            *reinterpret_cast<half8_t *>(v + (vput ^ 16)) = decode8<FMT>(vr[k][1], vr[k][3]);
         }
         if (tid < BLK) {
             const float u = usable(sv);
@@ -145,36 +172,51 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             for (int e = 0; e < 16; ++e) o[ct][d][e] = 0.f;
     }
 
+    // A operands: chunk 2 k + hf of a row, where chunk_at puts it (its exclusive or with 2 k is one of the byte address, too)
+    const char *const bytes = reinterpret_cast<const char *>(lds);
     const int key0 = 16 * chunk_at<KC>(l, hf), val0 = 16 * (STEP * KC + chunk_at<VC>(l, hf));
-    if (n0 < n1) {
-        look(n0);
-        load(n0);
-        if (n0 + 1 < n1) look(n0 + 1);
-        put(0);
-        if (n0 + 1 < n1) load(n0 + 1);
-        if (n0 + 2 < n1) look(n0 + 2);
-    }
-    for (int n = n0; n < n1; ++n) {
-        const int buf = (n - n0) & 1, t0 = token_of(n);
-        __syncthreads();
-        if (n + 1 < n1) put(buf ^ 1);
-        if (n + 2 < n1) load(n + 2);
-        if (n + 3 < n1) look(n + 3);
-        // nothing of the step for this wave: it lies behind its last row, or between the first tokens and its first row's window
-        if (t0 > wb || (at.window > 0 && wa - (t0 + STEP - 1) >= at.window && t0 >= at.sinks)) continue;
-        const char *const bytes = reinterpret_cast<const char *>(lds) + buf * (BUF * 16);
-        // A operands: chunk 2 k + hf of a row, where chunk_at puts it (its exclusive or with 2 k is one of the byte address, too)
-        auto key = [&](int tt, int k) { return *reinterpret_cast<const half8_t *>(bytes + (key0 ^ (32 * k)) + tt * (32 * KC * 16)); };
-        auto val = [&](int d, int k) { return *reinterpret_cast<const half8_t *>(bytes + (val0 ^ (32 * k)) + d * (32 * VC * 16)); };
-        float16_t s[QT][TT];
-        half8_t ka[2][TT], va[2][DT];
+    auto key = [&](int buf, int tt, int k) {
+        return *reinterpret_cast<const half8_t *>(bytes + buf * (2 * D * VC * 16) + (key0 ^ (32 * k)) + tt * (32 * KC * 16));
+    };
+    auto val = [&](int buf, int d, int k) {
+        return *reinterpret_cast<const half8_t *>(bytes + buf * (2 * D * VC * 16) + (val0 ^ (32 * k)) + d * (32 * VC * 16));
+    };
+    float16_t s[QT][TT];
+    half8_t w[QT][BLK];
+    // Operands are read two products (of every accumulator) ahead: the groups of the schedule keep the compiler to that.
+    auto values = [&](int buf) {
+        half8_t va[2][DT];
 #pragma unroll
-        for (int tt = 0; tt < TT; ++tt) ka[0][tt] = key(tt, 0);
+        for (int d = 0; d < DT; ++d) va[0][d] = val(buf, d, 0);
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) {
+            if (k + 1 < BLK) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) va[(k + 1) & 1][d] = val(buf, d, k + 1);
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], w[ct][k], o[ct][d]);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x100, DT + 1, 0);
+#pragma unroll
+        for (int i = 0; i < BLK * DT; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, QT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+    };
+    auto scores = [&](int buf) {
+        half8_t ka[3][TT];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int tt = 0; tt < TT; ++tt) ka[k][tt] = key(buf, tt, k);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            if (k + 1 < D / 16) {
+            if (k + 2 < D / 16) {
 #pragma unroll
-                for (int tt = 0; tt < TT; ++tt) ka[(k + 1) & 1][tt] = key(tt, k + 1);
+                for (int tt = 0; tt < TT; ++tt) ka[(k + 2) % 3][tt] = key(buf, tt, k + 2);
             }
 #pragma unroll
             for (int tt = 0; tt < TT; ++tt)
@@ -184,11 +226,18 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                         for (int e = 0; e < 16; ++e) s[ct][tt][e] = 0.f;
                     }
-                    s[ct][tt] = mfma32(ka[k & 1][tt], q[ct][k], s[ct][tt]);
+                    s[ct][tt] = mfma32(ka[k % 3][tt], q[ct][k], s[ct][tt]);
                 }
         }
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * TT + 1, 1);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) va[0][d] = val(d, 0);
+        for (int i = 0; i < TT * D / 16; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x8, QT, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        }
+    };
+    // the scores' weights
+    auto weigh = [&](int buf, int t0) {
         float a[BLK], lu[BLK], iu[BLK];
         uint32_t there = 1u;
 #pragma unroll
@@ -201,17 +250,23 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         }
         const bool whole = t0 + STEP - 1 <= wa && (at.window == 0 || wb - t0 < at.window || t0 + STEP <= at.sinks) &&
                            __builtin_amdgcn_readfirstlane(there) != 0;
-        half8_t w[QT][BLK];
 #pragma unroll
         for (int ct = 0; ct < QT; ++ct) {
             if (!whole) {
+                // bit off stands for token t0 + 4 hf + off
+                auto upto = [](int x) { return x < 0 ? 0ull : x >= 63 ? ~0ull : (2ull << x) - 1; };
+                const int reach = pos[ct] - t0 - 4 * hf;
+                unsigned long long seen = pos[ct] < 0 ? 0ull : upto(reach);
+                if (at.window > 0) seen &= ~upto(max(reach, -1) - at.window) | upto(at.sinks - t0 - 4 * hf - 1);
+                uint32_t part_of[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-                for (int k = 0; k < BLK; ++k) {
-                    const int p = meta_at[buf * BLK + k][3] != 0u ? pos[ct] : -1;
+                for (int k = 0; k < BLK; ++k)
+                    if (meta_at[buf * BLK + k][3] == 0u) part_of[k / 2] &= k % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+                for (int k = 0; k < BLK; ++k)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (!sees(p, t0 + 16 * k + 8 * (e / 4) + 4 * hf + e % 4, at.window, at.sinks)) s[ct][k / 2][8 * (k % 2) + e] = -INFINITY;
-                }
+                        if ((part_of[k / 2] >> (16 * (k % 2) + 8 * (e / 4) + e % 4) & 1u) == 0u) s[ct][k / 2][8 * (k % 2) + e] = -INFINITY;
             }
             // the largest y of a block is its largest score's (a > 0)
             float mx = kNone;
@@ -225,7 +280,8 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             float other = mx;
             swap32(mx, other);
             mx = fmaxf(mx, other);
-            if (__any(mx > m[ct])) {
+            // m need not be the maximum: within 2^kSlack of it, weights still are fp16 numbers and o stays as it is
+            if (__any(mx > m[ct] + kSlack)) {
                 const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
                 m[ct] = mn;
                 sum[ct] *= f;
@@ -234,7 +290,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             }
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
-                const float shift = lu[k] + (kLift - m[ct]);
+                const float shift = lu[k] + (kTallLift - m[ct]);
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
@@ -245,19 +301,74 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
                 w[ct][k] = __builtin_bit_cast(half8_t, pk);
             }
         }
-#pragma unroll
-        for (int k = 0; k < BLK; ++k) {
-            if (k + 1 < BLK) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d) va[(k + 1) & 1][d] = val(d, k + 1);
-            }
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], w[ct][k], o[ct][d]);
+    };
+
+    if (n0 < n1) {
+        look(n0);
+        load(n0);
+        if (n0 + NG < n1) look(n0 + NG);
+        put(0);
+        if (n0 + NG < n1) load(n0 + NG);
+        if (n0 + 2 * NG < n1) look(n0 + 2 * NG);
+    }
+    // The second group decodes the next step's codes at the end of a round, the first at its start: so one's waves feed the
+    // matrix cores while the other's, on the same SIMDs, use the vector ALU.
+    for (int it = 0; it < rounds; ++it) {
+        const int n = n0 + it * NG, buf = it & 1, t0 = token_of(n < n1 ? n : n0);
+        // nothing of the step for this wave: there is none, it lies behind its last row, or between the first tokens and its first
+        // row's window
+        const bool idle = n >= n1 || t0 > wb || (at.window > 0 && wa - (t0 + STEP - 1) >= at.window && t0 >= at.sinks);
+        auto next = [&]() {
+            if (n + NG < n1) put(buf ^ 1);
+            if (n + 2 * NG < n1) load(n + 2 * NG);
+            if (n + 3 * NG < n1) look(n + 3 * NG);
+        };
+        __syncthreads();
+        if (gr == 0) next();
+        if (!idle) {
+            scores(buf);
+            weigh(buf, t0);
+            values(buf);
         }
+        if (gr != 0) next();
     }
 
+    // the groups' sums, one after the other through LDS
+#pragma unroll
+    for (int from = 1; from < NG; ++from) {
+        __syncthreads();
+        if (gr == from) {
+#pragma unroll
+            for (int ct = 0; ct < QT; ++ct) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<float4_t *>(all)[((ct * DT + d) * 4 + e) * NT + tid] =
+                            float4_t{o[ct][d][4 * e], o[ct][d][4 * e + 1], o[ct][d][4 * e + 2], o[ct][d][4 * e + 3]};
+                reinterpret_cast<float2 *>(all + QT * DT * 4 * NT)[ct * NT + tid] = make_float2(m[ct], sum[ct]);
+            }
+        }
+        __syncthreads();
+        if (gr == 0) {
+#pragma unroll
+            for (int ct = 0; ct < QT; ++ct) {
+                const float2 x = reinterpret_cast<const float2 *>(all + QT * DT * 4 * NT)[ct * NT + tid];
+                const float mn = fmaxf(m[ct], x.x), f = exp2_(m[ct] - mn), g = exp2_(x.x - mn);
+                m[ct] = mn;
+                sum[ct] = sum[ct] * f + x.y * g;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float4_t v = reinterpret_cast<const float4_t *>(all)[((ct * DT + d) * 4 + e) * NT + tid];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[ct][d][4 * e + i] = o[ct][d][4 * e + i] * f + v[i] * g;
+                    }
+            }
+        }
+    }
+    if (gr != 0) return;
 #pragma unroll
     for (int ct = 0; ct < QT; ++ct) {
         float other = sum[ct], den = sum[ct];
@@ -285,22 +396,18 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     }
 }
 
-// Jobs: key/value head and sequence (fastest: the tiles of one head go to one XCD where their number is a multiple of 8), split,
-// row tile, the last one (which sees most) first.
-template <int D, int FMT, int QT, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, int splits, int chunk, int tiles,
-                                                            int64_t jobs, bool fold)
+// Workgroups: key/value head and sequence (fastest: the tiles of one head go to one XCD where their number is a multiple of 8),
+// split, row tile, the last one (which sees most) first.
+template <int D, int FMT, int QT, int NW, int NG>
+__global__ __launch_bounds__(64 * NW * NG, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, const AttendPlan p,
+                                                                                const AttendGrid gd)
 {
-    constexpr int STEP = kTallStep<D>;
-    __shared__ u32x4 lds[2 * (STEP * (D / 8) + D * (STEP / 8)) + 2 * (STEP / 16)];
-    const int64_t pairs = at.sq.B * at.c.heads;
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        const int64_t k = job % pairs, n = job / pairs;
-        if (job != blockIdx.x) __syncthreads();  // (the last job's steps have been read)
-        const int y = (int)(n / splits), tile = fold && y >= (tiles + 1) / 2 ? y - (tiles + 1) / 2 : tiles - 1 - y;
-        attend_tall<D, FMT, QT, NW>(at, part, splits, chunk, (int)(n % splits), (int)(k % at.c.heads), tile * (32 * QT * NW),
-                                    (int)(k / at.c.heads), lds);
-    }
+    __shared__ u32x4 lds[NG * kTallLds<D>];
+    static_assert(NG <= 2 && (NG == 1 || NG * kTallLds<D> >= QT * (D / 32) * 4 * 64 * NW + QT * 32 * NW), "the groups' sums");
+    const uint32_t pairs = gd.seqs * at.c.heads, k = blockIdx.x % pairs, n = blockIdx.x / pairs;
+    const int tile = gd.tile0 + gd.tiles - 1 - (int)(n / p.splits);
+    attend_tall<D, FMT, QT, NW, NG>(at, part, p.splits, p.chunk, (int)(n % p.splits), (int)(k % at.c.heads), tile * (32 * QT * NW),
+                                    gd.seq0 + (int)(k / at.c.heads), lds);
 }
 
 }  // namespace
@@ -313,11 +420,17 @@ int tall_height(int dim)
 
 void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipStream_t s)
 {
-    const int64_t jobs = (int64_t)p.splits * at.c.heads * p.tiles * at.sq.B;
-    const dim3 grid((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups));
     auto go = [&](auto dim, auto fmt) {
-        constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
-        k_attend_tall<D, F, kTallCols<D>, kTallWaves<D>><<<grid, 64 * kTallWaves<D>, 0, s>>>(at, part, p.splits, p.chunk, p.tiles, jobs, getenv("FOLD") != nullptr);
+        constexpr int D = decltype(dim)::value, F = decltype(fmt)::value, NW = kTallWaves<D>;
+        for_grids(at, p, [&](const AttendGrid &gd, uint32_t groups) {
+            if constexpr (D < 256) {
+                if (p.pair) {
+                    k_attend_tall<D, F, kTallCols<D>, NW, 2><<<groups, 128 * NW, 0, s>>>(at, part, p, gd);
+                    return;
+                }
+            }
+            k_attend_tall<D, F, kTallCols<D>, NW, 1><<<groups, 64 * NW, 0, s>>>(at, part, p, gd);
+        });
     };
     auto dims = [&](auto fmt) {
         if (at.c.dim == 64) go(std::integral_constant<int, 64>{}, fmt);
