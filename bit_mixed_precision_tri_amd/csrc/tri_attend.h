@@ -5,7 +5,9 @@
 namespace tri {
 
 constexpr int kStep = 64;                        // tokens of a step
-constexpr float kLift = 10.f;                    // weights are lifted by 2^10
+// Weights are lifted by 2^10; the running maximum follows only when it is 2^5 behind: a weight stays below 2^15, and the sums
+// need no scaling in most steps.
+constexpr float kLift = 10.f, kSlack = 5.f;
 constexpr float kNone = -1e30f;                  // the running maximum of a row that has seen nothing
 
 // The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
@@ -42,9 +44,14 @@ __device__ __forceinline__ Tile tile_of(const Attend &at, int b, int r0, int hei
     return t;
 }
 
-__device__ __forceinline__ bool sees(int p, int j, int window, int sinks)
+// Which of the tokens j0 .. j0 + 63 position p sees, a bit each (p < 0: none).
+__device__ __forceinline__ unsigned long long seen_of(int p, int j0, int window, int sinks)
 {
-    return j <= p && (window == 0 || p - j < window || j < sinks);
+    auto upto = [](int x) { return x < 0 ? 0ull : x >= 63 ? ~0ull : (2ull << x) - 1; };
+    const int reach = p - j0;                    // (p < 0 comes with j0 >= 0)
+    unsigned long long seen = p < 0 ? 0ull : upto(reach);
+    if (window > 0) seen &= ~upto(max(reach, -1) - window) | upto(sinks - j0 - 1);
+    return seen;
 }
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -29,31 +29,59 @@ template <int D, int FMT, int CT, int NW>
 __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__ part, int splits, int chunk, int split, int h,
                                            int r0, int b)
 {
-    constexpr int KL = D / 64, DT = D / 16, CS = D + 4;   // 16-byte loads of a token and lane; tiles of 16 values; LDS stride
+    constexpr int KL = D / 16, DT = D / 16, CS = D + 4;  // 16-byte loads of keys of a step and lane; tiles of 16 values; LDS stride
     __shared__ alignas(16) float so[NW][16][CS];
     __shared__ float sm[NW][16 * CT], sl[NW][16 * CT];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, j = lane & 15;
     const tri_cache &c = at.c;
+    const int P = c.page, lp = 31 - __builtin_clz(P), i0 = split * chunk;
+    const int64_t head_bytes = (int64_t)P * D;
+
+    // Pages of the step of token t0: of this lane's rows of A in the first product (tokens 16 (j / 4) ..), and of its tokens in
+    // the second (16 g ..); as the table holds them, looked up a step before they are used.
+    const int32_t *table = at.sq.table + (int64_t)b * at.sq.width;
+    const int64_t last_page = at.sq.width - 1;
+    auto look = [&](int64_t t0, int &pk, int &pv) {
+        pk = table[min((t0 + 16 * (j >> 2)) >> lp, last_page)];
+        pv = table[min((t0 + 16 * g) >> lp, last_page)];
+    };
+    int i = i0 + wv, pk, pv, nk, nv;
+    if (at.window == 0) {                        // (steps are in order from 0 on: no need to know the sequence's length first)
+        look((int64_t)i * kStep, pk, pv);
+        look((int64_t)(i + NW) * kStep, nk, nv);
+    }
+
     const Tile t = tile_of(at, b, r0, 16 * CT);
     if (t.rows == 0) return;
-    const int steps = t.st.count(), i0 = split * chunk, i1 = split == splits - 1 ? steps : min(steps, i0 + chunk);
+    const int steps = t.st.count(), i1 = split == splits - 1 ? steps : min(steps, i0 + chunk);
     if (split > 0 && i0 >= steps) return;        // (split 0 writes the zeros of rows that see nothing)
+    if (at.window > 0) {
+        look((int64_t)t.st.at(i) * kStep, pk, pv);
+        look((int64_t)t.st.at(i + NW) * kStep, nk, nv);
+    }
 
-    const int P = c.page, lp = 31 - __builtin_clz(P);
-    const int64_t head_bytes = (int64_t)P * D;
-    const float ck = at.scale * 1.44269504088896f * kCodeUnit<FMT>;
-
-    // queries: lane (g, j) holds row j's values D/4 g .. D/4 (g + 1) - 1, eight for every 32 of a product
+    // Keys.  A load is of whole 128-byte lines: for dim 64 rows of A are tokens (16 (j / 4) + 4 n + j % 4 of the step in load n:
+    // four in a row); for more, rows 2 x and 2 x + 1 are the halves of a line of token 16 (x / 2) + 2 n + x % 2, each multiplied by
+    // both halves of the queries, and the scores are the sums of what belongs together (the matrix cores have time for
+    // twice the products here; half lines read 5.4 TB/s instead of 6.2).
+    constexpr bool kHalves = D >= 128;
+    constexpr int LINES = kHalves ? D / 128 : 1;
+    auto q_at = [&](int n) {                     // operand n: of line n / 4, half n / 2 % 2, eight values each
+        return kHalves ? 128 * (n / 4) + 64 * (n / 2 % 2) + 16 * g + 8 * (n % 2) : 16 * g + 8 * n;
+    };
+    const int krow = kHalves ? 16 * (j >> 2) + (j >> 1 & 1) : 16 * (j >> 2) + (j & 3), kbyte = kHalves ? 16 * (g + 4 * (j & 1)) : 16 * g;
+    const uint32_t flip = at.scale < 0.f ? 0x80008000u : 0u;     // (the scale's sign goes into the queries)
+    const float ck = fabsf(at.scale) * 1.44269504088896f * kCodeUnit<FMT>;
     u32x4 q[CT][D / 32];
     int pos[CT];
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
-        const int r = r0 + 16 * ct + j, i = r / at.G;
+        const int r = r0 + 16 * ct + j, n = r / at.G;
         const bool live = 16 * ct + j < t.rows;
-        pos[ct] = live ? t.sp.p0 + i : -1;
-        const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? i : 0)) * at.q_stride + (h * at.G + (live ? r % at.G : 0)) * D + (D / 4) * g;
+        pos[ct] = live ? t.sp.p0 + n : -1;
+        const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? n : 0)) * at.q_stride + (h * at.G + (live ? r % at.G : 0)) * D;
 #pragma unroll
-        for (int s = 0; s < D / 32; ++s) q[ct][s] = *reinterpret_cast<const u32x4 *>(x + 8 * s);
+        for (int s = 0; s < D / 32; ++s) q[ct][s] = *reinterpret_cast<const u32x4 *>(x + q_at(s)) ^ flip;
     }
 
     float m[CT], l[CT];
@@ -66,105 +94,120 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
         for (int d = 0; d < DT; ++d) o[ct][d] = float4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    // pages of step i: of this lane's rows of A in the first product (tokens 16 (j / 4) ..), and of its tokens in the second
-    // (16 g ..)
-    const int32_t *table = at.sq.table + (int64_t)b * at.sq.width;
-    auto pages = [&](int i, int &pk, int &pv) {
-        pk = pv = -1;
-        if (i >= i1) return;
-        const int64_t t0 = (int64_t)t.st.at(i) * kStep;
-        const int64_t a = (t0 + 16 * (j >> 2)) >> lp, e = (t0 + 16 * g) >> lp;
-        if (a < at.sq.width) pk = table[a];
-        if (e < at.sq.width) pv = table[e];
-        if (pk < 0 || pk >= (int)c.pages) pk = -1;
-        if (pv < 0 || pv >= (int)c.pages) pv = -1;
-    };
-    u32x4 kr[4][KL], vr[DT];
+    auto streamed = [](const uint8_t *x) { return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(x)); };
+    u32x4 kr[KL], vr[DT];
     float sk, sv;
-    auto load_keys = [&](int i, int pk, int pv) {
-        const int t0 = t.st.at(i) * kStep;
-        const uint8_t *x = c.K + ((int64_t)max(pk, 0) * c.heads + h) * head_bytes + (D / 4) * g;
+    bool here;                                   // whether this lane's tokens (16 g .. of the step) have a page
+    auto load_keys = [&](int64_t t0) {           // (a page that is not there: any one's codes)
+        const uint8_t *x = c.K + ((int64_t)((uint32_t)pk < (uint32_t)c.pages ? pk : 0) * c.heads + h) * head_bytes + kbyte;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            const int row = (t0 + 16 * (j >> 2) + 4 * tt + (j & 3)) & (P - 1);
-#pragma unroll
-            for (int k = 0; k < KL; ++k) kr[tt][k] = *reinterpret_cast<const u32x4 *>(x + row * D + 16 * k);
+        for (int n = 0; n < KL; ++n) {
+            const int row = (int)(t0 + krow + (kHalves ? 2 * (n / LINES) : 4 * n)) & (P - 1);
+            kr[n] = streamed(x + row * D + (kHalves ? 128 * (n % LINES) : 0));
         }
-        const int64_t s = (int64_t)max(pv, 0) * c.heads + h;
+        const bool ok = (uint32_t)pv < (uint32_t)c.pages;
+        const int64_t s = (int64_t)(ok ? pv : 0) * c.heads + h;
         sk = c.K_scale[s];
         sv = c.V_scale[s];
+        here = ok && (t0 + 16 * g) >> lp <= last_page;
     };
-    auto load_values = [&](int i, int pv) {
-        const int t0 = t.st.at(i) * kStep;
-        const uint8_t *x = c.V + ((int64_t)max(pv, 0) * c.heads + h) * head_bytes + ((t0 + 16 * g) & (P - 1));
+    // Values: rows of a page's tokens, so of whole lines but for pages of 128 tokens, whose lines another wave reads the rest of.
+    auto load_values = [&](int64_t t0) {
+        const uint8_t *x = c.V + ((int64_t)((uint32_t)pv < (uint32_t)c.pages ? pv : 0) * c.heads + h) * head_bytes + ((int)(t0 + 16 * g) & (P - 1));
+        if (P <= 64) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const u32x4 *>(x + (16 * d + j) * P);
+            for (int d = 0; d < DT; ++d) vr[d] = streamed(x + (16 * d + j) * P);
+        } else {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) vr[d] = *reinterpret_cast<const u32x4 *>(x + (16 * d + j) * P);
+        }
     };
 
-    int i = i0 + wv, pk, pv, nk, nv;
-    pages(i, pk, pv);
-    pages(i + NW, nk, nv);
     if (i < i1) {
-        load_keys(i, pk, pv);
-        load_values(i, pv);
+        const int64_t t0 = (int64_t)t.st.at(i) * kStep;
+        load_keys(t0);
+        load_values(t0);
     }
     for (; i < i1; i += NW) {
         const int t0 = t.st.at(i) * kStep;
         const bool more = i + NW < i1;
-        float4_t s[CT][4];
+        const int64_t t1 = (int64_t)t.st.at(i + NW) * kStep;
+        float s[CT][16];                         // the lane's tokens' scores
+        if constexpr (kHalves) {
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) s[ct][tt] = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                const half8_t a = decode8<FMT>(kr[tt][k / 2][2 * (k % 2)], kr[tt][k / 2][2 * (k % 2) + 1]);
+            for (int n = 0; n < 8; ++n) {
+                float4_t x[CT][2];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct)
-                    s[ct][tt] = mfma(a, q[ct][k], s[ct][tt]);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) x[ct][half] = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 2 * LINES; ++k) {
+                    const u32x4 w = kr[n * LINES + k / 2];
+                    const half8_t a = decode8<FMT>(w[2 * (k % 2)], w[2 * (k % 2) + 1]);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) x[ct][half] = mfma(a, q[ct][4 * (k / 2) + 2 * half + k % 2], x[ct][half]);
+                }
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    s[ct][2 * n] = x[ct][0][0] + x[ct][1][1];
+                    s[ct][2 * n + 1] = x[ct][0][2] + x[ct][1][3];
+                }
+            }
+        } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const half8_t lo = decode8<FMT>(kr[n][0], kr[n][1]), hi = decode8<FMT>(kr[n][2], kr[n][3]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const float4_t x = mfma(hi, q[ct][1], mfma(lo, q[ct][0], float4_t{0.f, 0.f, 0.f, 0.f}));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[ct][4 * n + e] = x[e];
+                }
             }
         }
-        const bool here = pv >= 0;
-        const float a = ck * sk, u = here ? sv : 1.f, lu = log2_(u), iu = 1.f / u;
-        const int pv0 = pv;
-        pk = nk;
-        pv = nv;
-        if (more) load_keys(i + NW, pk, pv);
+        const float u = usable(sv), a = usable(ck * sk), lu = log2_(u), iu = 1.f / u;
+        const bool there = here;
         // every row sees all of the step, unless it reaches past the first row's position, before the last one's window
         // (and behind the first tokens), or onto a page that is not there
-        const bool whole = t0 + kStep - 1 <= t.pa &&
-                           (at.window == 0 || t.pb - t0 < at.window || t0 + kStep <= at.sinks) && __all(pv0 >= 0);
+        const bool whole = t0 + kStep - 1 <= t.pa && (at.window == 0 || t.pb - t0 < at.window || t0 + kStep <= at.sinks) && __all(there);
+        pk = nk;
+        pv = nv;
+        if (more) {
+            load_keys(t1);
+            look((int64_t)t.st.at(i + 2 * NW) * kStep, nk, nv);
+        }
         u32x4 w[CT][2];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            float y[16], mx = kNone;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = fmaf(s[ct][e / 4][e % 4], a, lu);
             if (!whole) {
+                const uint32_t seen = there ? (uint32_t)seen_of(pos[ct], t0 + 16 * g, at.window, at.sinks) : 0u;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (!here || !sees(pos[ct], t0 + 16 * g + e, at.window, at.sinks)) y[e] = -INFINITY;
+                    if ((seen >> e & 1u) == 0u) s[ct][e] = -INFINITY;
             }
+            float top = s[ct][0];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, y[e]);
-            mx = max_over_rows(mx);
-            if (__any(mx > m[ct])) {
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, s[ct][e]);
+            const float mx = max_over_rows(fmaxf(kNone, fmaf(top, a, lu)));    // (a > 0)
+            if (__any(mx > m[ct] + kSlack)) {
                 const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
                 m[ct] = mn;
                 l[ct] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
-            const float shift = kLift - m[ct];
+            const float shift = lu + (kLift - m[ct]);
             float sum = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                y[e] = exp2_(y[e] + shift);
-                sum += y[e];
+            for (int e = 0; e < 8; ++e) {
+                const float y0 = exp2_(fmaf(s[ct][2 * e], a, shift)), y1 = exp2_(fmaf(s[ct][2 * e + 1], a, shift));
+                sum += y0 + y1;
+                w[ct][e / 4][e % 4] = pack2(y0, y1);
             }
-            l[ct] = sum == 0.f ? l[ct] : fmaf(sum, iu, l[ct]);     // (a scale that no visible token has may be anything)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[ct][e / 4][e % 4] = pack2(y[2 * e], y[2 * e + 1]);
+            l[ct] = fmaf(sum, iu, l[ct]);
         }
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -172,8 +215,7 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) o[ct][d] = mfma(hi, w[ct][1], mfma(lo, w[ct][0], o[ct][d]));
         }
-        if (more) load_values(i + NW, pv);
-        pages(i + 2 * NW, nk, nv);
+        if (more) load_values(t1);
     }
 
     // the waves' sums, in the waves' order
@@ -279,7 +321,8 @@ __global__ __launch_bounds__(256) void k_join(const Attend at, const float *__re
     }
 }
 
-constexpr int kWaves = 4;
+// Waves of k_attend_few: eight where 256 registers hold what one works on, else four.
+constexpr int few_waves(int dim, int ct) { return dim == 256 || (dim == 128 && ct == 2) ? 4 : 8; }
 // Workgroups of k_join: it takes further rows in a loop.
 constexpr int64_t kMostGroups = 1 << 20;
 
@@ -300,9 +343,9 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
     // steps do).  Up to two tiles per CU, the longest tile's steps are what the call waits for: two groups of waves share them
     // (2048 tokens of 32 heads, 512 tiles: 62 -> 57 us; 880 tiles of two chunks over a window: 97 us, 114 with pairs).
     p.pair = p.tall && groups <= 2 * cus;
-    const int64_t want = p.tall ? (groups * 2 > cus ? 1 : cus / groups) : (2 * cus + groups - 1) / groups;
+    const int64_t want = p.tall ? (groups * 2 > cus ? 1 : cus / groups) : (cus + groups - 1) / groups;
     int64_t chunk = (steps + want - 1) / want;
-    const int64_t least = p.tall ? 16 : kWaves;
+    const int64_t least = p.tall ? 16 : few_waves(c.dim, p.height / 16);
     chunk = chunk < least ? least : chunk;
     p.chunk = (int)chunk;
     p.splits = (int)((steps + chunk - 1) / chunk);
@@ -314,8 +357,8 @@ void attend_dim(const Attend &at, const AttendPlan &p, float *part, hipStream_t 
 {
     if (!p.tall)
         for_grids(at, p, [&](const AttendGrid &gd, uint32_t groups) {
-            if (p.height == 16) k_attend_few<D, FMT, 1, kWaves><<<groups, 64 * kWaves, 0, s>>>(at, part, p, gd);
-            else if constexpr (D < 256) k_attend_few<D, FMT, 2, kWaves><<<groups, 64 * kWaves, 0, s>>>(at, part, p, gd);
+            if (p.height == 16) k_attend_few<D, FMT, 1, few_waves(D, 1)><<<groups, 64 * few_waves(D, 1), 0, s>>>(at, part, p, gd);
+            else if constexpr (D < 256) k_attend_few<D, FMT, 2, few_waves(D, 2)><<<groups, 64 * few_waves(D, 2), 0, s>>>(at, part, p, gd);
         });
     if (p.splits > 1) {
         const int64_t rows = (int64_t)at.T * at.H;

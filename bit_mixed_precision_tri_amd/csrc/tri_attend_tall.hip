@@ -20,10 +20,6 @@ __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c)
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// Weights are lifted by 2^6 and may grow to 2^14 before the maximum is moved: every row's maximum grows a few times, some row's
-// of a wave in most steps.
-constexpr float kTallLift = 6.f, kSlack = 8.f;
-
 template <int D> constexpr int kTallStep = D == 256 ? 32 : 64;   // tokens of a step here
 template <int D> constexpr int kTallWaves = 4;                   // waves that share a step
 template <int D> constexpr int kTallCols = 1;                    // tiles of 32 rows of a wave
@@ -253,11 +249,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
         for (int ct = 0; ct < QT; ++ct) {
             if (!whole) {
-                // bit off stands for token t0 + 4 hf + off
-                auto upto = [](int x) { return x < 0 ? 0ull : x >= 63 ? ~0ull : (2ull << x) - 1; };
-                const int reach = pos[ct] - t0 - 4 * hf;
-                unsigned long long seen = pos[ct] < 0 ? 0ull : upto(reach);
-                if (at.window > 0) seen &= ~upto(max(reach, -1) - at.window) | upto(at.sinks - t0 - 4 * hf - 1);
+                const unsigned long long seen = seen_of(pos[ct], t0 + 4 * hf, at.window, at.sinks);
                 uint32_t part_of[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
                 for (int k = 0; k < BLK; ++k)
@@ -290,7 +282,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             }
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
-                const float shift = lu[k] + (kTallLift - m[ct]);
+                const float shift = lu[k] + (kLift - m[ct]);
                 float y[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
