@@ -285,6 +285,17 @@ __global__ __launch_bounds__(256) void k_join(const Attend at, const float *__re
     const int64_t rows = (int64_t)at.T * at.H;
     const int grp = threadIdx.x / (D / 4), d = threadIdx.x % (D / 4);
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float *x = part + row * splits * (D + 4);
+        // the first splits' sums are on their way before it is known how many there are
+        constexpr int AHEAD = 4;
+        float4_t w[AHEAD];
+        float2 md[AHEAD];
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q) {
+            const float *y = x + (int64_t)min(grp + q * GR, splits - 1) * (D + 4);
+            w[q] = *reinterpret_cast<const float4_t *>(y + 4 * d);
+            md[q] = *reinterpret_cast<const float2 *>(y + D);
+        }
         const int tok = (int)(row / at.H), head = (int)(row % at.H), b = owner(at.sq, tok);
         const Span sp = span_of(at.sq, at.T, b);
         const int i = tok - sp.r0;
@@ -292,17 +303,20 @@ __global__ __launch_bounds__(256) void k_join(const Attend at, const float *__re
         const int r = i * at.G + head % at.G;
         const Tile t = tile_of(at, b, r - r % height, height);
         const int n = min(splits, max(1, (t.st.count() + chunk - 1) / chunk));
-        const float *x = part + row * splits * (D + 4);
         float m = kNone, den = 0.f;
         float4_t v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int k = grp; k < n; k += GR) {
-            const float *y = x + (int64_t)k * (D + 4);
-            const float4_t w = *reinterpret_cast<const float4_t *>(y + 4 * d);
-            const float ym = y[D], mn = fmaxf(m, ym), f = exp2_(m - mn), e = exp2_(ym - mn);
+        auto add = [&](const float4_t &w, const float2 &md) {
+            const float mn = fmaxf(m, md.x), f = exp2_(m - mn), e = exp2_(md.x - mn);
             m = mn;
-            den = den * f + y[D + 1] * e;
+            den = den * f + md.y * e;
             v = v * f + w * e;
+        };
+#pragma unroll
+        for (int q = 0; q < AHEAD; ++q)
+            if (grp + q * GR < n) add(w[q], md[q]);
+        for (int k = grp + AHEAD * GR; k < n; k += GR) {
+            const float *y = x + (int64_t)k * (D + 4);
+            add(*reinterpret_cast<const float4_t *>(y + 4 * d), *reinterpret_cast<const float2 *>(y + D));
         }
         __syncthreads();                         // (the last row's sums have been read)
         so[grp][d] = v;
