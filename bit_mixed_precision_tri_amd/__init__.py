@@ -12,6 +12,7 @@ import collections
 import ctypes
 import functools
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libtri.so")
@@ -691,23 +692,23 @@ class Rotary:
         for g in self.gains or ():
             _need(g is None or (g.is_cuda and g.dtype is torch.float16 and g.dim() == 1 and g.is_contiguous()),
                   "gains must be contiguous (dim) float16 tensors on the GPU")
+        self._device = None if table is None else table.get_device()
+        self._gains = [(0, 0, 0) if g is None else (g.data_ptr(), g.shape[0], g.get_device()) for g in self.gains or ()]
         rows, half = (0, 0) if table is None else table.shape[:2]
         self.struct = TriRotary(None if table is None else table.data_ptr(), rows, 2 * half, 1 if interleaved else 0,
                                 1 if norm else 0, eps)
         self._ref = ctypes.addressof(self.struct)
 
     def _gain(self, i, n, dim, device):
-        """The gain of set i of n as an address, checked."""
-        if self.table is not None and self.table.get_device() != device:
+        """The gain of set i of n as an address (0: none), checked."""
+        if self._device != device and self._device is not None:
             raise ValueError("the rotation's table must be on the heads' device")
         if self.gains is None:
-            return None
-        _need(len(self.gains) == n, "gains must be one for each set of heads")
-        g = self.gains[i]
-        if g is None:
-            return None
-        _need(g.shape[0] == dim and g.get_device() == device, "gains must be (dim) tensors on the heads' device")
-        return g.data_ptr()
+            return 0
+        _need(len(self._gains) == n, "gains must be one for each set of heads")
+        ptr, size, dev = self._gains[i]
+        _need(ptr == 0 or (size == dim and dev == device), "gains must be (dim) tensors on the heads' device")
+        return ptr
 
 
 class KVCache:
@@ -765,15 +766,17 @@ class Sequences:
         return self._ref
 
 
-def _heads_of(x, what, dim, device, T=None, heads=None):
-    """Address, token stride and heads of a (T, heads, dim) float16 tensor whose tokens may lie apart."""
-    shape = x.shape
-    if not (len(shape) == 3 and x.dtype is _torch.float16 and x.get_device() == device and shape[2] == dim and
-            x.stride(2) == 1 and (shape[1] == 1 or x.stride(1) == dim) and (T is None or shape[0] == T) and
-            (heads is None or shape[1] == heads) and shape[0] > 0 and shape[1] > 0):
+_pack_heads = struct.Struct("PPPqqi4x").pack     # tri_heads
+
+
+def _heads_of(x, what, dim, device, T, heads):
+    """Address and token stride of a (T, heads, dim) float16 tensor whose tokens may lie apart."""
+    shape, stride = x.shape, x.stride()
+    if not (shape == (T, heads, dim) and x.dtype is _torch.float16 and x.get_device() == device and stride[2] == 1 and
+            (stride[1] == dim or heads == 1) and heads > 0):
         raise ValueError("%s must be a (T, heads, dim) float16 tensor on device %d whose heads lie one after another" %
                          (what, device))
-    return x.data_ptr(), x.stride(0) if shape[0] > 1 else shape[1] * dim, shape[1]
+    return x.data_ptr(), stride[0] if T > 1 else heads * dim
 
 
 def heads_rotate(xs, rotary, positions, out=None, stream=None):
@@ -787,13 +790,14 @@ def heads_rotate(xs, rotary, positions, out=None, stream=None):
     if out is None:
         out = tuple(_new(tuple(x.shape), torch.float16, x.device, stream) for x in xs)
     _need(len(out) == len(xs), "out must have a tensor for each of xs")
-    hs = (TriHeads * len(xs))()
-    for i, (x, y) in enumerate(zip(xs, out)):
-        h = hs[i]
-        h.X, h.x_stride, h.heads = _heads_of(x, "xs", dim, dev, T)
-        h.Y, h.y_stride, _ = _heads_of(y, "out", dim, dev, T, h.heads)
-        h.gain = rotary._gain(i, len(xs), dim, dev)
-    _launch("tri_heads_rotate", dev, stream, ctypes.addressof(hs), len(xs), T, dim, rotary._ref, positions.data_ptr())
+    hs = b""
+    for i, x in enumerate(xs):
+        _need(x.dim() == 3, "xs must be 1 to 4 (T, heads, dim) tensors on the GPU")
+        H = x.shape[1]
+        xp, xst = _heads_of(x, "xs", dim, dev, T, H)
+        yp, yst = _heads_of(out[i], "out", dim, dev, T, H)
+        hs += _pack_heads(xp, yp, rotary._gain(i, len(xs), dim, dev), xst, yst, H)
+    _launch("tri_heads_rotate", dev, stream, hs, len(xs), T, dim, rotary._ref, positions.data_ptr())
     return tuple(out)
 
 
@@ -803,24 +807,23 @@ def cache_append(cache, seqs, K, V, rotary=None, Q=None, out=None, stream=None):
     in a new tensor or in `out`, which may be Q itself."""
     torch = _torch or _load_torch()
     dim, dev = cache.dim, cache.device
-    kp, ks, _ = _heads_of(K, "K", dim, dev, None, cache.heads)
     T = K.shape[0]
-    vp, vs, _ = _heads_of(V, "V", dim, dev, T, cache.heads)
+    kp, ks = _heads_of(K, "K", dim, dev, T, cache.heads)
+    vp, vs = _heads_of(V, "V", dim, dev, T, cache.heads)
     rot = gain = q = None
     if rotary is not None:
         rot, gain = rotary._ref, rotary._gain(1, 2, dim, dev)
     if Q is not None:
-        _need(rotary is not None, "queries are taken with a rotation only")
+        _need(rotary is not None and Q.dim() == 3, "queries are (T, heads, dim), and taken with a rotation only")
+        H = Q.shape[1]
         if out is None:
             out = _new(tuple(Q.shape), torch.float16, Q.device, stream)
-        h = TriHeads()
-        h.X, h.x_stride, h.heads = _heads_of(Q, "Q", dim, dev, T)
-        h.Y, h.y_stride, _ = _heads_of(out, "out", dim, dev, T, h.heads)
-        h.gain = rotary._gain(0, 2, dim, dev)
-        q = ctypes.addressof(h)
+        qp, qs = _heads_of(Q, "Q", dim, dev, T, H)
+        op, os_ = _heads_of(out, "out", dim, dev, T, H)
+        q = _pack_heads(qp, op, rotary._gain(0, 2, dim, dev), qs, os_, H)
     else:
         _need(out is None, "out is for queries")
-    _launch("tri_cache_append", dev, stream, cache._ref, seqs._fit(cache), T, kp, ks, vp, vs, rot, gain, q)
+    _launch("tri_cache_append", dev, stream, cache._ref, seqs._fit(cache), T, kp, ks, vp, vs, rot, gain or None, q)
     return out
 
 
@@ -839,10 +842,11 @@ def cache_attend(cache, seqs, Q, scale=None, window=0, sinks=0, workspace=None, 
     `out`.  `workspace`: a uint8 tensor of at least cache_attend_workspace_bytes; allocated where it is None and needed."""
     torch = _torch or _load_torch()
     dim, dev = cache.dim, cache.device
-    qp, qs, H = _heads_of(Q, "Q", dim, dev)
-    T = Q.shape[0]
+    _need(Q.dim() == 3 and Q.shape[0] > 0, "Q must be a (T, heads, dim) tensor")
+    T, H, _ = Q.shape
+    qp, qs = _heads_of(Q, "Q", dim, dev, T, H)
     O = _new(tuple(Q.shape), torch.float16, Q.device, stream) if out is None else out
-    op, os_, _ = _heads_of(O, "out", dim, dev, T, H)
+    op, os_ = _heads_of(O, "out", dim, dev, T, H)
     sref = seqs._fit(cache)
     ws, nbytes = None, 0
     if workspace is None:
