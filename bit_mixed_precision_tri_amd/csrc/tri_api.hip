@@ -429,7 +429,12 @@ int tri_heads_rotate(const tri_heads *heads, int G, int64_t T, int dim, const tr
 {
     if (!heads || G < 1 || G > TRI_MAX_GROUPS || T < 1 || T >= kMaxDim || !known_dim(dim) || !positions) return TRI_EINVAL;
     int rc = check_rotary(rot, dim);
-    for (int g = 0; g < G && rc == TRI_OK; ++g) rc = check_heads(heads[g], T, dim);
+    int64_t all = 0;
+    for (int g = 0; g < G && rc == TRI_OK; ++g) {
+        rc = check_heads(heads[g], T, dim);
+        all += heads[g].heads;
+    }
+    if (rc == TRI_OK && T * all >= kMaxDim) rc = TRI_EINVAL;
     if (rc == TRI_OK && misaligned_to(positions, 4)) rc = TRI_EALIGN;
     return rc != TRI_OK ? rc : launch_rotate(heads, G, (int)T, dim, *rot, positions, stream);
 }

@@ -93,27 +93,6 @@ struct AttendPlan {
     bool tall, pair;
 };
 
-// One launch's part of a call: seqs sequences from seq0 on, tiles row tiles of each from tile0 on.
-struct AttendGrid {
-    int seq0, seqs, tile0, tiles;
-};
-
-// A grid has fewer than 2^32 threads: as many launches as that takes (one, but for bounds of millions of tiles), each of at most
-// 2^22 workgroups of up to 512 threads.  (heads * splits is far below: a split has at least kLeastChunk steps.)
-template <typename Launch>
-void for_grids(const Attend &at, const AttendPlan &p, Launch launch)
-{
-    const int64_t most = 1 << 22, one = (int64_t)at.c.heads * p.splits;
-    const int64_t tiles = p.tiles * one <= most ? p.tiles : most / one > 0 ? most / one : 1;
-    const int64_t seqs = tiles * one * at.sq.B <= most ? at.sq.B : most / (tiles * one) > 0 ? most / (tiles * one) : 1;
-    for (int64_t b = 0; b < at.sq.B; b += seqs)
-        for (int64_t t = 0; t < p.tiles; t += tiles) {
-            const AttendGrid gd = {(int)b, (int)(seqs < at.sq.B - b ? seqs : at.sq.B - b), (int)t,
-                                   (int)(tiles < p.tiles - t ? tiles : p.tiles - t)};
-            launch(gd, (uint32_t)(gd.seqs * (int64_t)gd.tiles * one));
-        }
-}
-
 // tri_attend_tall.hip: rows of a tile, and the launch.
 int tall_height(int dim);
 void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipStream_t s);

@@ -268,7 +268,7 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
 
 // Workgroups: split (fastest), key/value head, row tile, sequence.
 template <int D, int FMT, int CT, int NW>
-__global__ __launch_bounds__(64 * NW) void k_attend_few(const Attend at, float *__restrict__ part, const AttendPlan p, const AttendGrid gd)
+__global__ __launch_bounds__(64 * NW) void k_attend_few(const Attend at, float *__restrict__ part, const AttendPlan p, const Grid gd)
 {
     const uint32_t k = blockIdx.x / p.splits, n = k / at.c.heads;
     attend_few<D, FMT, CT, NW>(at, part, p.splits, p.chunk, (int)(blockIdx.x % p.splits), (int)(k % at.c.heads),
@@ -370,7 +370,7 @@ template <int D, int FMT>
 void attend_dim(const Attend &at, const AttendPlan &p, float *part, hipStream_t s)
 {
     if (!p.tall)
-        for_grids(at, p, [&](const AttendGrid &gd, uint32_t groups) {
+        for_grids(at.sq.B, p.tiles, (int64_t)at.c.heads * p.splits, [&](const Grid &gd, uint32_t groups) {
             if (p.height == 16) k_attend_few<D, FMT, 1, few_waves(D, 1)><<<groups, 64 * few_waves(D, 1), 0, s>>>(at, part, p, gd);
             else if constexpr (D < 256) k_attend_few<D, FMT, 2, few_waves(D, 2)><<<groups, 64 * few_waves(D, 2), 0, s>>>(at, part, p, gd);
         });

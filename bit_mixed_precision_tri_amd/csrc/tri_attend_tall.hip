@@ -392,7 +392,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 // split, row tile, the last one (which sees most) first.
 template <int D, int FMT, int QT, int NW, int NG>
 __global__ __launch_bounds__(64 * NW * NG, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, const AttendPlan p,
-                                                                                const AttendGrid gd)
+                                                                                const Grid gd)
 {
     __shared__ u32x4 lds[NG * kTallLds<D>];
     static_assert(NG <= 2 && (NG == 1 || NG * kTallLds<D> >= QT * (D / 32) * 4 * 64 * NW + QT * 32 * NW), "the groups' sums");
@@ -414,7 +414,7 @@ void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipS
 {
     auto go = [&](auto dim, auto fmt) {
         constexpr int D = decltype(dim)::value, F = decltype(fmt)::value, NW = kTallWaves<D>;
-        for_grids(at, p, [&](const AttendGrid &gd, uint32_t groups) {
+        for_grids(at.sq.B, p.tiles, (int64_t)at.c.heads * p.splits, [&](const Grid &gd, uint32_t groups) {
             if constexpr (D < 256) {
                 if (p.pair) {
                     k_attend_tall<D, F, kTallCols<D>, NW, 2><<<groups, 128 * NW, 0, s>>>(at, part, p, gd);

@@ -39,6 +39,28 @@ __device__ __forceinline__ int page_at(const tri_sequences &sq, const tri_cache 
     return id >= 0 && id < (int)c.pages ? id : -1;
 }
 
+// One launch's part of a call: seqs sequences from seq0 on, tiles pieces (row tiles, page slots) of each from tile0 on.
+struct Grid {
+    int seq0, seqs, tile0, tiles;
+};
+
+// A grid has fewer than 2^32 threads: as many launches as that takes (one, but for bounds of millions of pieces), each of at
+// most 2^21 workgroups of up to 1024 threads; `one` workgroups (far fewer than that) are for one piece of a sequence.
+template <typename Launch>
+void for_grids(int64_t B, int64_t pieces, int64_t one, Launch launch)
+{
+    const int64_t most = 1 << 21;
+    int64_t tiles = most / one, seqs;
+    tiles = tiles < 1 ? 1 : tiles < pieces ? tiles : pieces;
+    seqs = most / (tiles * one);
+    seqs = seqs < 1 ? 1 : seqs < B ? seqs : B;
+    for (int64_t b = 0; b < B; b += seqs)
+        for (int64_t t = 0; t < pieces; t += tiles) {
+            const Grid gd = {(int)b, (int)(seqs < B - b ? seqs : B - b), (int)t, (int)(tiles < pieces - t ? tiles : pieces - t)};
+            launch(gd, (uint32_t)(gd.seqs * (int64_t)gd.tiles * one));
+        }
+}
+
 // Largest code's value, as the exponent e and the fraction f (of 2^23) of f 2^e: 127 = 1.984375 * 2^6, 448 = 1.75 * 2^8.
 template <int FMT> constexpr int kTopExp = FMT == TRI_KV_INT8 ? 6 : 8;
 template <int FMT> constexpr uint32_t kTopFrac = FMT == TRI_KV_INT8 ? 0x7E0000u : 0x600000u;

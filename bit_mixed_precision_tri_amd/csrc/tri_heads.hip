@@ -38,12 +38,35 @@ __device__ __forceinline__ void pieces_of(int i, int dims, int &ca, int &cb)
     cb = i < nr ? i + nr : 2 * i + 1;
 }
 
-// Norm and rotation of a lane's values, in fp32, rounded to fp16 at the end.  turn: the table's row of the token's position.
-template <int D>
-__device__ __forceinline__ void turn_row(Piece2 &v, const tri_rotary &rot, const uint16_t *gain, const float *turn, int i)
+// What a lane's values are turned with: the gains of its pieces and the (cos, sin) of its eight pairs.
+struct Turn {
+    Piece2 gain;
+    float4_t cs[4];
+};
+__device__ __forceinline__ void load_gain(Turn &tn, const tri_rotary &rot, const uint16_t *gain, int i)
 {
     int ca, cb;
     pieces_of(i, rot.dims, ca, cb);
+    const u32x4 one = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+    tn.gain = Piece2{one, one};
+    if (rot.norm && gain)
+        tn.gain = Piece2{*reinterpret_cast<const u32x4 *>(gain + 8 * ca), *reinterpret_cast<const u32x4 *>(gain + 8 * cb)};
+}
+// (p: a position that the table has)
+__device__ __forceinline__ void load_angles(Turn &tn, const tri_rotary &rot, int p, int i)
+{
+    if (i >= rot.dims / 16) return;
+    int ca, cb;
+    pieces_of(i, rot.dims, ca, cb);
+    const float4_t *t = reinterpret_cast<const float4_t *>(rot.table + (int64_t)p * rot.dims);
+    const int a = rot.interleaved ? 2 * ca : 4 * i, b = rot.interleaved ? 2 * cb : 4 * i + 2;
+    tn.cs[0] = t[a], tn.cs[1] = t[a + 1], tn.cs[2] = t[b], tn.cs[3] = t[b + 1];
+}
+
+// Norm and rotation of a lane's values, in fp32, rounded to fp16 at the end.
+template <int D>
+__device__ __forceinline__ void turn_row(Piece2 &v, const tri_rotary &rot, const Turn &tn, int i)
+{
     float x[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -55,34 +78,24 @@ __device__ __forceinline__ void turn_row(Piece2 &v, const tri_rotary &rot, const
 #pragma unroll
         for (int e = 0; e < 16; ++e) s = fmaf(x[e], x[e], s);
         const float r = 1.f / sqrtf(row_sum<D>(s) * (1.f / D) + rot.eps);
-        u32x4 ga = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u}, gb = ga;
-        if (gain) {
-            ga = *reinterpret_cast<const u32x4 *>(gain + 8 * ca);
-            gb = *reinterpret_cast<const u32x4 *>(gain + 8 * cb);
-        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            x[e] *= r * h2f((uint16_t)(ga[e / 2] >> (16 * (e % 2))));
-            x[8 + e] *= r * h2f((uint16_t)(gb[e / 2] >> (16 * (e % 2))));
+            x[e] *= r * h2f((uint16_t)(tn.gain.a[e / 2] >> (16 * (e % 2))));
+            x[8 + e] *= r * h2f((uint16_t)(tn.gain.b[e / 2] >> (16 * (e % 2))));
         }
     }
     if (i < rot.dims / 16) {
-        float4_t cs[4];                          // (cos, sin) of eight pairs
-        const float4_t *t = reinterpret_cast<const float4_t *>(turn);
         if (rot.interleaved) {
-            cs[0] = t[2 * ca], cs[1] = t[2 * ca + 1], cs[2] = t[2 * cb], cs[3] = t[2 * cb + 1];
 #pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const float c = cs[p / 2][2 * (p % 2)], s = cs[p / 2][2 * (p % 2) + 1], a = x[2 * p], b = x[2 * p + 1];
+                const float c = tn.cs[p / 2][2 * (p % 2)], s = tn.cs[p / 2][2 * (p % 2) + 1], a = x[2 * p], b = x[2 * p + 1];
                 x[2 * p] = a * c - b * s;
                 x[2 * p + 1] = a * s + b * c;
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) cs[q] = t[4 * i + q];
-#pragma unroll
             for (int p = 0; p < 8; ++p) {
-                const float c = cs[p / 2][2 * (p % 2)], s = cs[p / 2][2 * (p % 2) + 1], a = x[p], b = x[8 + p];
+                const float c = tn.cs[p / 2][2 * (p % 2)], s = tn.cs[p / 2][2 * (p % 2) + 1], a = x[p], b = x[8 + p];
                 x[p] = a * c - b * s;
                 x[8 + p] = a * s + b * c;
             }
@@ -96,38 +109,55 @@ __device__ __forceinline__ void turn_row(Piece2 &v, const tri_rotary &rot, const
     }
 }
 
-// The heads of wave `w` (of a token's waves) of token t, at position p.
-template <int D>
-__device__ __forceinline__ void rotate_wave(const Sets &sets, const tri_rotary &rot, int t, int w, int p)
+// The heads of N units (of a token's) from `w` on of token t, at position p; a unit is as many heads as a wave has rows of lanes.
+template <int D, int N>
+__device__ __forceinline__ void rotate_units(const Sets &sets, const tri_rotary &rot, int t, int w, int p)
 {
-    const int lane = threadIdx.x & 63, i = lane % (D / 16);
-    tri_heads hs = sets.set[0];
-    int first = 0;
-#pragma unroll
-    for (int q = 1; q < TRI_MAX_GROUPS; ++q)
-        if (q < sets.G && w >= sets.first[q]) hs = sets.set[q], first = sets.first[q];
-    const int h = (w - first) * (1024 / D) + lane / (D / 16);
-    if (h >= hs.heads) return;                   // (whole rows of lanes)
+    const int lane = threadIdx.x & 63, i = lane % (D / 16), per = sets.first[sets.G];
     int ca, cb;
     pieces_of(i, rot.dims, ca, cb);
-    const uint16_t *x = reinterpret_cast<const uint16_t *>(hs.X) + (int64_t)t * hs.x_stride + h * D;
-    uint16_t *y = reinterpret_cast<uint16_t *>(hs.Y) + (int64_t)t * hs.y_stride + h * D;
-    Piece2 v = {*reinterpret_cast<const u32x4 *>(x + 8 * ca), *reinterpret_cast<const u32x4 *>(x + 8 * cb)};
-    turn_row<D>(v, rot, reinterpret_cast<const uint16_t *>(hs.gain), rot.table + (int64_t)p * rot.dims, i);
-    *reinterpret_cast<u32x4 *>(y + 8 * ca) = v.a;
-    *reinterpret_cast<u32x4 *>(y + 8 * cb) = v.b;
+    uint16_t *y[N];
+    Piece2 v[N];
+    Turn tn[N];                                  // (all of them have the token's angles)
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        tri_heads hs = sets.set[0];
+        int first = 0;
+#pragma unroll
+        for (int q = 1; q < TRI_MAX_GROUPS; ++q)
+            if (q < sets.G && w + n >= sets.first[q]) hs = sets.set[q], first = sets.first[q];
+        const int h = (w + n - first) * (1024 / D) + lane / (D / 16);
+        y[n] = nullptr;
+        load_gain(tn[n], rot, reinterpret_cast<const uint16_t *>(hs.gain), i);
+        if (w + n < per && h < hs.heads) {       // (whole rows of lanes)
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(hs.X) + (int64_t)t * hs.x_stride + h * D;
+            y[n] = reinterpret_cast<uint16_t *>(hs.Y) + (int64_t)t * hs.y_stride + h * D;
+            v[n] = Piece2{*reinterpret_cast<const u32x4 *>(x + 8 * ca), *reinterpret_cast<const u32x4 *>(x + 8 * cb)};
+        }
+    }
+    load_angles(tn[0], rot, p, i);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (y[n]) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tn[n].cs[q] = tn[0].cs[q];
+            turn_row<D>(v[n], rot, tn[n], i);
+            *reinterpret_cast<u32x4 *>(y[n] + 8 * ca) = v[n].a;
+            *reinterpret_cast<u32x4 *>(y[n] + 8 * cb) = v[n].b;
+        }
 }
 
 // A position's place in the rotation's table, or none.
 __device__ __forceinline__ bool turns(const tri_rotary &rot, int p) { return rot.dims == 0 || (p >= 0 && p < (int)rot.rows); }
 
-template <int D>
-__global__ __launch_bounds__(256) void k_rotate(const Sets sets, const tri_rotary rot, const int32_t *__restrict__ positions, int64_t waves)
+// A wave takes N units of a token's heads.
+template <int D, int N>
+__global__ __launch_bounds__(256) void k_rotate(const Sets sets, const tri_rotary rot, const int32_t *__restrict__ positions, uint32_t waves)
 {
-    const int per = sets.first[sets.G];
-    for (int64_t u = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < waves; u += (int64_t)gridDim.x * 4) {
-        const int t = (int)(u / per), w = (int)(u % per), p = positions[t];
-        if (turns(rot, p)) rotate_wave<D>(sets, rot, t, w, p);
+    const uint32_t per = (sets.first[sets.G] + N - 1) / N;
+    for (uint32_t u = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < waves; u += gridDim.x * 4) {
+        const int t = (int)(u / per), p = positions[t];
+        if (turns(rot, p)) rotate_units<D, N>(sets, rot, t, (int)(u % per) * N, p);
     }
 }
 
@@ -154,17 +184,19 @@ __device__ __forceinline__ bool find_part(const Append &ap, int which, int b, in
 {
     const tri_cache &c = ap.c;
     const Span sp = span_of(ap.sq, ap.T, b);
-    const int64_t P = c.page, from = max(sp.p0, 0), end = (int64_t)sp.p0 + sp.n;
-    const int64_t to = ap.rot.dims > 0 ? min(end, ap.rot.rows) : end;
-    const int64_t pi = from / P + slot, lo = max(from, pi * P), hi = min(to, (pi + 1) * P);
-    if (lo >= hi) return false;
+    // (positions are below 2^31 - 256, and so are the ends of the pages that hold them)
+    const int P = c.page, lp = 31 - __builtin_clz(P), from = max(sp.p0, 0), end = sp.p0 + sp.n;
+    const int to = ap.rot.dims > 0 ? (int)min((int64_t)end, ap.rot.rows) : end;
+    const int pi = (from >> lp) + slot;
+    if (pi > (to - 1) >> lp || from >= to) return false;
+    const int lo = max(from, pi << lp), hi = min(to, (pi + 1) << lp);
     const int id = page_at(ap.sq, c, b, pi);
     if (id < 0) return false;
     const int64_t at = (int64_t)id * c.heads + h;
-    pt.first = (int)(lo - pi * P);
-    pt.cnt = (int)(hi - lo);
-    pt.pos = (int)lo;
-    pt.x = ap.X[which] + (sp.r0 + (lo - sp.p0)) * ap.stride[which] + h * D;
+    pt.first = lo - (pi << lp);
+    pt.cnt = hi - lo;
+    pt.pos = lo;
+    pt.x = ap.X[which] + (int64_t)(sp.r0 + (lo - sp.p0)) * ap.stride[which] + h * D;
     pt.codes = (which ? c.V : c.K) + at * P * D;
     pt.scale = (which ? c.V_scale : c.K_scale) + at;
     pt.was = pt.first > 0 ? *pt.scale : 0.f;
@@ -228,12 +260,15 @@ __device__ __forceinline__ void append_keys(const Append &ap, const Part &pt, ui
     int ca, cb;
     pieces_of(i, ap.rot.dims, ca, cb);
     Piece2 v[PASSES];
+    Turn tn[PASSES];
     uint32_t most = 0;
+    load_gain(tn[0], ap.rot, ap.gain, i);
 #pragma unroll
     for (int s = 0; s < PASSES; ++s) {
         const int r = s * RPP + r0;
         v[s] = Piece2{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
         if (r < pt.cnt) {
+            load_angles(tn[s], ap.rot, pt.pos + r, i);
             const uint16_t *x = pt.x + r * ap.stride[0];
             v[s] = Piece2{*reinterpret_cast<const u32x4 *>(x + 8 * ca), *reinterpret_cast<const u32x4 *>(x + 8 * cb)};
         }
@@ -241,7 +276,8 @@ __device__ __forceinline__ void append_keys(const Append &ap, const Part &pt, ui
 #pragma unroll
     for (int s = 0; s < PASSES; ++s) {
         const int r = s * RPP + r0;
-        if (ap.turn && r < pt.cnt) turn_row<D>(v[s], ap.rot, ap.gain, ap.rot.table + (int64_t)(pt.pos + r) * ap.rot.dims, i);
+        tn[s].gain = tn[0].gain;
+        if (ap.turn && r < pt.cnt) turn_row<D>(v[s], ap.rot, tn[s], i);
         most = max(most, max(magnitude8(v[s].a), magnitude8(v[s].b)));
     }
     const float inv = settle_scale<D, FMT, NT>(pt, ap.c.page, 0, most_of_all<NT>(most, sm));
@@ -309,7 +345,12 @@ __device__ __forceinline__ void append_one(const Append &ap, const Part &pt, int
         int ca, cb;
         pieces_of(i, ap.rot.dims, ca, cb);
         Piece2 v = {*reinterpret_cast<const u32x4 *>(pt.x + 8 * ca), *reinterpret_cast<const u32x4 *>(pt.x + 8 * cb)};
-        if (ap.turn) turn_row<D>(v, ap.rot, ap.gain, ap.rot.table + (int64_t)pt.pos * ap.rot.dims, i);
+        if (ap.turn) {
+            Turn tn;
+            load_gain(tn, ap.rot, ap.gain, i);
+            load_angles(tn, ap.rot, pt.pos, i);
+            turn_row<D>(v, ap.rot, tn, i);
+        }
         const uint32_t most = most_of_all<64>(max(magnitude8(v.a), magnitude8(v.b)), nullptr);
         const float inv = settle_scale<D, FMT, 64>(pt, ap.c.page, 0, most);
         if (lane < D / 16) {
@@ -333,29 +374,27 @@ __device__ __forceinline__ void append_one(const Append &ap, const Part &pt, int
     }
 }
 
-// Jobs: every sequence's page slots times heads times (keys, values), then the query heads' waves.  PASSES 0: one token each.
-template <int D, int FMT, int NT, int PASSES>
-__global__ __launch_bounds__(NT) void k_append(const Append ap, const Sets sets, int64_t pages, int64_t jobs, int64_t waves)
+// Workgroups: `pages` of them for keys and values of a head in a page slot of a sequence (gd.tile0 ..: slots), then the query
+// heads' waves, of N units each.  PASSES 0: one token each.
+template <int D, int FMT, int NT, int PASSES, int N>
+__global__ __launch_bounds__(NT) void k_append(const Append ap, const Sets sets, const Grid gd, uint32_t pages, uint32_t waves)
 {
     __shared__ uint32_t sm[NT / 64];
-    const int per = sets.first[sets.G];
-    for (int64_t job = blockIdx.x; job < jobs; job += gridDim.x) {
-        if (job < pages) {
-            const int which = (int)(job & 1);
-            const int64_t k = job >> 1, r = k / ap.c.heads;
-            Part pt;                             // (the same in every thread of the workgroup)
-            if (!find_part<D>(ap, which, (int)(r / ap.slots), (int)(k % ap.c.heads), (int)(r % ap.slots), pt)) continue;
-            if constexpr (PASSES == 0) append_one<D, FMT>(ap, pt, which);
-            else if (which == 0) append_keys<D, FMT, NT, PASSES>(ap, pt, sm);
-            else append_values<D, FMT, NT, (PASSES + 1) / 2>(ap, pt, sm);
-        } else {
-            const int64_t u = (job - pages) * (NT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            if (u >= waves) continue;
-            const int t = (int)(u / per), b = owner(ap.sq, t);
-            const Span sp = span_of(ap.sq, ap.T, b);
-            const int i = t - sp.r0, p = sp.p0 + i;
-            if (i >= 0 && i < sp.n && p >= 0 && turns(ap.rot, p)) rotate_wave<D>(sets, ap.rot, t, (int)(u % per), p);
-        }
+    if (blockIdx.x < pages) {
+        const uint32_t which = blockIdx.x & 1, k = blockIdx.x >> 1, h = k % ap.c.heads, r = k / ap.c.heads;
+        Part pt;                                 // (the same in every thread of the workgroup)
+        if (!find_part<D>(ap, which, gd.seq0 + (int)(r / gd.tiles), (int)h, gd.tile0 + (int)(r % gd.tiles), pt)) return;
+        if constexpr (PASSES == 0) append_one<D, FMT>(ap, pt, which);
+        else if (which == 0) append_keys<D, FMT, NT, PASSES>(ap, pt, sm);
+        else append_values<D, FMT, NT, (PASSES + 1) / 2>(ap, pt, sm);
+        return;
+    }
+    const uint32_t per = (sets.first[sets.G] + N - 1) / N, step = (gridDim.x - pages) * (NT / 64);
+    for (uint32_t u = (blockIdx.x - pages) * (NT / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); u < waves; u += step) {
+        const int t = (int)(u / per), b = owner(ap.sq, t);
+        const Span sp = span_of(ap.sq, ap.T, b);
+        const int i = t - sp.r0, p = sp.p0 + i;
+        if (i >= 0 && i < sp.n && p >= 0 && turns(ap.rot, p)) rotate_units<D, N>(sets, ap.rot, t, (int)(u % per) * N, p);
     }
 }
 
@@ -371,24 +410,33 @@ Sets make_sets(const tri_heads *heads, int G, int dim)
     return s;
 }
 
-// Grids stay far below 2^32 threads; workgroups take further jobs in a loop.
+// Units of a wave: one while there are few, so that the chip fills, else two, whose loads are on their way together.
+constexpr int kUnits = 2;
+bool many_units(int64_t T, const Sets &s) { return T * s.first[s.G] >= 16 * (int64_t)cu_count(); }
+
+// Waves are taken in a loop past this many workgroups.
 constexpr int64_t kMostGroups = 1 << 20;
 
 template <int D, int FMT>
 void append_dim(const Append &ap, const Sets &sets, hipStream_t s)
 {
-    const int64_t pages = 2 * ap.sq.B * ap.c.heads * ap.slots, waves = (int64_t)ap.T * sets.first[sets.G];
-    auto go = [&](auto kernel, int nt) {
-        const int64_t jobs = pages + (waves + nt / 64 - 1) / (nt / 64);
-        kernel<<<dim3((uint32_t)(jobs < kMostGroups ? jobs : kMostGroups)), nt, 0, s>>>(ap, sets, pages, jobs, waves);
-    };
-    // one new token per sequence: a wave each; else a page's tokens are held by 256 to 1024 threads,
-    // at most 32 values each (64 and 128 values, 256 threads: up to 391 registers)
-    if (ap.sq.max_new == 1) go(k_append<D, FMT, 64, 0>, 64);
-    else if (ap.c.page * D <= 4096) go(k_append<D, FMT, 256, 1>, 256);
-    else if (ap.c.page * D <= 8192) go(k_append<D, FMT, 256, 2>, 256);
-    else if (ap.c.page * D <= 16384) go(k_append<D, FMT, 512, 2>, 512);
-    else go(k_append<D, FMT, 1024, 2>, 1024);
+    bool first = true;
+    for_grids(ap.sq.B, ap.slots, 2 * (int64_t)ap.c.heads, [&](const Grid &gd, uint32_t pages) {
+        auto go = [&](auto kernel, int nt, int units) {
+            const int64_t waves = first ? ap.T * (int64_t)((sets.first[sets.G] + units - 1) / units) : 0;
+            const int64_t more = (waves + nt / 64 - 1) / (nt / 64);
+            kernel<<<dim3(pages + (uint32_t)(more < kMostGroups ? more : kMostGroups)), nt, 0, s>>>(ap, sets, gd, pages, (uint32_t)waves);
+        };
+        const int size = ap.c.page * D;
+        // one new token per sequence: a wave each; else a page's tokens are held by 256 to 1024 threads, at most 32 values each (64
+        // and 128 values, 256 threads: up to 391 registers)
+        if (ap.sq.max_new == 1) go(k_append<D, FMT, 64, 0, 1>, 64, 1);
+        else if (size <= 4096) go(k_append<D, FMT, 256, 1, kUnits>, 256, kUnits);
+        else if (size <= 8192) go(k_append<D, FMT, 256, 2, kUnits>, 256, kUnits);
+        else if (size <= 16384) go(k_append<D, FMT, 512, 2, kUnits>, 512, kUnits);
+        else go(k_append<D, FMT, 1024, 2, kUnits>, 1024, kUnits);
+        first = false;
+    });
 }
 
 }  // namespace
@@ -396,11 +444,17 @@ void append_dim(const Append &ap, const Sets &sets, hipStream_t s)
 int launch_rotate(const tri_heads *heads, int G, int T, int dim, const tri_rotary &rot, const int32_t *positions, hipStream_t s)
 {
     const Sets sets = make_sets(heads, G, dim);
-    const int64_t waves = (int64_t)T * sets.first[G], wg = (waves + 3) / 4;
+    const bool many = many_units(T, sets);
+    const int units = many ? kUnits : 1;
+    const int64_t waves = T * (int64_t)((sets.first[G] + units - 1) / units), wg = (waves + 3) / 4;
     const dim3 grid((uint32_t)(wg < kMostGroups ? wg : kMostGroups));
-    if (dim == 64) k_rotate<64><<<grid, 256, 0, s>>>(sets, rot, positions, waves);
-    else if (dim == 128) k_rotate<128><<<grid, 256, 0, s>>>(sets, rot, positions, waves);
-    else k_rotate<256><<<grid, 256, 0, s>>>(sets, rot, positions, waves);
+    auto go = [&](auto one, auto more) {
+        if (many) more<<<grid, 256, 0, s>>>(sets, rot, positions, (uint32_t)waves);
+        else one<<<grid, 256, 0, s>>>(sets, rot, positions, (uint32_t)waves);
+    };
+    if (dim == 64) go(k_rotate<64, 1>, k_rotate<64, kUnits>);
+    else if (dim == 128) go(k_rotate<128, 1>, k_rotate<128, kUnits>);
+    else go(k_rotate<256, 1>, k_rotate<256, kUnits>);
     return hipGetLastError() == hipSuccess ? TRI_OK : TRI_EHIP;
 }
 

@@ -354,7 +354,7 @@ typedef struct tri_rotary {
 
 /* Y = the heads of X, normalised and rotated; G <= TRI_MAX_GROUPS sets of heads (queries and keys) of the
  * same T tokens in one launch.  positions: T int32; the rows of a token whose position lies outside
- * 0..rows-1 are not written.  dim: 64, 128 or 256.  T*heads < 2^31 for every set.
+ * 0..rows-1 are not written.  dim: 64, 128 or 256.  T times the sets' heads together < 2^31.
  * Errors: TRI_EINVAL (T < 1, a size or stride out of range, null), TRI_EALIGN, TRI_EHIP. */
 int tri_heads_rotate(const tri_heads *heads, int G, int64_t T, int dim, const tri_rotary *rot,
                      const int32_t *positions, hipStream_t stream);
