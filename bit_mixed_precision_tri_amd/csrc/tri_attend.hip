@@ -3,9 +3,11 @@
 // With q a row, k_j and v_j codes, s_j and u_j the scales of the keys' and values' pages, everything in base 2:
 //     x_j = scale log2(e) s_j (q . k_j),   y_j = x_j + log2 u_j,   m = max y_j,   w_j = 2^(y_j - m + 10),
 //     o = sum_j w_j v_j / sum_j (w_j / u_j).
-// The values' scales sit in the exponents, so that w_j (at most 2^10, rounded to fp16: normal numbers down to 2^-24 of the
-// largest) is the operand of the second product and the codes, exact in fp16, are the other; however small a scale is,
-// nothing underflows.  m, the two sums and o run on over the tokens (when m grows, the others shrink by 2^(m - m')).
+// The values' scales sit in the exponents, so that w_j (rounded to fp16: normal numbers down to 2^-24 of the largest) is the
+// operand of the second product and the codes, exact in fp16, are the other; however small a scale is, nothing underflows.
+// m, the two sums and o run on over the tokens (when m grows, the others shrink by 2^(m - m')).  With few rows the matrix cores
+// have time for a second product, of what the rounding of the weights left off: results are then as exact as fp32 weights'
+// (an error of 2.1e-4 of the results' size, all of it their own rounding to fp16; 2.9e-4 without, as for many rows).
 //
 // Both products are taken transposed: S^T = K Q^T (a row of A is a token, a column of B a query row), O^T = V^T W^T.  A lane of
 // S^T then holds weights of one query row, and they are its part of the second product's B operand as they lie: the
@@ -179,7 +181,7 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
             load_keys(t1);
             look((int64_t)t.st.at(i + 2 * NW) * kStep, nk, nv);
         }
-        u32x4 w[CT][2];
+        u32x4 w[CT][2], wl[CT][2];               // weights, and what their rounding to fp16 left off
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             if (!whole) {
@@ -205,7 +207,9 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
             for (int e = 0; e < 8; ++e) {
                 const float y0 = exp2_(fmaf(s[ct][2 * e], a, shift)), y1 = exp2_(fmaf(s[ct][2 * e + 1], a, shift));
                 sum += y0 + y1;
-                w[ct][e / 4][e % 4] = pack2(y0, y1);
+                const uint32_t x = pack2(y0, y1);
+                w[ct][e / 4][e % 4] = x;
+                wl[ct][e / 4][e % 4] = pack2(y0 - h2f((uint16_t)x), y1 - h2f((uint16_t)(x >> 16)));
             }
             l[ct] = fmaf(sum, iu, l[ct]);
         }
@@ -213,7 +217,8 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
         for (int d = 0; d < DT; ++d) {
             const half8_t lo = decode8<FMT>(vr[d][0], vr[d][1]), hi = decode8<FMT>(vr[d][2], vr[d][3]);
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) o[ct][d] = mfma(hi, w[ct][1], mfma(lo, w[ct][0], o[ct][d]));
+            for (int ct = 0; ct < CT; ++ct)
+                o[ct][d] = mfma(hi, w[ct][1], mfma(lo, w[ct][0], mfma(hi, wl[ct][1], mfma(lo, wl[ct][0], o[ct][d]))));
         }
         if (more) load_values(t1);
     }

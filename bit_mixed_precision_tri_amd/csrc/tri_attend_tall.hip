@@ -287,9 +287,11 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
                 const u32x4 pk = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
-                // (the denominator takes the weights as they are: of values of small scale, nothing may be left of them in fp16)
+                // the denominator takes the weights as they are rounded, so that what flat weights are off by together cancels; of
+                // small ones (values of a small scale are) it takes them as they are, since in fp16 nothing may be left of them
                 const float add = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-                sum[ct] = fmaf(add, iu[k], sum[ct]);
+                const float rounded = dot2(pk[3], 0x3C003C00u, dot2(pk[2], 0x3C003C00u, dot2(pk[1], 0x3C003C00u, dot2(pk[0], 0x3C003C00u, 0.f))));
+                sum[ct] = fmaf(rounded >= 1.f ? rounded : add, iu[k], sum[ct]);
                 w[ct][k] = __builtin_bit_cast(half8_t, pk);
             }
         }
