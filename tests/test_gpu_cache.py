@@ -429,6 +429,66 @@ def test_a_cache_past_four_gigabytes():
         near(got, want, tol, new)
 
 
+@pytest.mark.parametrize("D,fmt", [(64, E4M3), (128, INT8), (256, INT8)])
+def test_attend_many_rows_in_splits(D, fmt):
+    """Tiles of many rows whose steps are shared by workgroups and joined, with and without a window."""
+    rng = np.random.default_rng([41, D])
+    for new, lens, heads, G, window, sinks in [([40], [5000], 1, 1, 0, 0), ([50, 3], [3000, 2000], 1, 4, 0, 0), ([33], [6000], 1, 2, 2500, 70)]:
+        b = ref.Batch(rng, new, lens, heads, D, 64, fmt)
+        check_attend(b, heads * G, rng, window=window, sinks=sinks, what=(new, lens))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_many_rows_in_many_tiles(D):
+    """More tiles than the two per CU up to which two groups of waves share one."""
+    rng = np.random.default_rng([42, D])
+    B, heads = 70, 8
+    new = [int(x) for x in rng.integers(33, 50, B)]
+    lens = [n + int(x) for n, x in zip(new, rng.integers(0, 150, B))]
+    b = ref.Batch(rng, new, lens, heads, D, 16, INT8)
+    check_attend(b, heads, rng)
+
+
+def test_bounds_far_beyond_what_sequences_have():
+    """max_new of thousands for sequences of one token each: more workgroups than one launch takes.  A token that sees itself
+    alone gives its value."""
+    import torch
+    rng = np.random.default_rng(43)
+    B, heads, D, page = 3000, 32, 64, 16
+    K, V = (cuda(rng.standard_normal((B, heads, D)).astype(np.float16)) for _ in range(2))
+    cache = tri.KVCache.empty(B, heads, D, page, INT8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    seqs = tri.Sequences(torch.arange(B + 1, **i32), torch.ones(B, **i32), torch.randperm(B, device="cuda").to(torch.int32)[:, None].contiguous(),
+                         max_new=B)
+    tri.cache_append(cache, seqs, K, V)
+    one = tri.KVCache.empty(B, heads, D, page, INT8)
+    single = tri.Sequences(seqs.offsets, seqs.lens, seqs.table, max_new=1)
+    tri.cache_append(one, single, K, V)
+    for x, y in ((cache.K, one.K), (cache.V, one.V), (cache.K_scale, one.K_scale), (cache.V_scale, one.V_scale)):
+        assert torch.equal(x, y)
+    at = seqs.table[:, 0].long()
+    want = (cache.V.view(torch.int8)[at, :, :, 0].float() * cache.V_scale[at][..., None]).half()
+    Q = torch.randn((B, heads, D), device="cuda").half()
+    for sq in (seqs, single):
+        assert torch.equal(tri.cache_attend(cache, sq, Q), want)
+
+
+@pytest.mark.parametrize("n", [1, 20, 100])
+def test_flat_weights_and_equal_values(n):
+    """Equal scores and equal values: the mean of equal values is that value, whatever the number of tokens (roundings of equal
+    weights must cancel)."""
+    rng = np.random.default_rng([44, n])
+    for L in (n, n + 37, n + 1000):
+        for fmt, code in ((INT8, 77), (E4M3, 0x45)):
+            b = ref.Batch(rng, [n], [L], 1, 64, 16, fmt)
+            b.V[:], b.vs[:], b.ks[:] = code, 0.75, 0.01
+            cache, seqs = b.on_gpu()
+            Q = rng.standard_normal((n, 2, 64)).astype(np.float16)
+            got = host(tri.cache_attend(cache, seqs, cuda(Q), scale=0.0)).astype(np.float64)
+            v = ref.values_of(fmt)[code] * 0.75
+            assert np.all(np.abs(got - v) <= 2.0 ** -11 * v + (L + 64) * 2.0 ** -23 * v), (L, fmt)
+
+
 def test_long_contexts():
     """Splits of a long context, with and without a window, against sums taken in float64 on the GPU."""
     import torch
