@@ -13,6 +13,13 @@
 // S^T then holds weights of one query row, and they are its part of the second product's B operand as they lie: the
 // weights never leave their lanes.  Which token a row of A is can be chosen freely; rows are taken so that a lane's 16
 // weights are of 16 consecutive tokens, all in one page.
+//
+// Few rows are bound by reading the cache.  Each wave reads whole steps of 64 tokens by itself, straight from the pages into
+// its operands (no LDS, no barrier), the next step's codes while it works on this one's: 64 sequences of about 8192 tokens, 8
+// heads of 128 (810 MB), take 140 us, 5.8 TB/s (a plain read of as many bytes 122); 16 over windows of 4096, 32 heads (538 MB),
+// 98 - 101 us (82).  Vector instructions take a quarter of a wave's cycles there, waiting for loads and results 30%.  One
+// sequence alone is bound by latency: 333 tokens 6.7 us; 32768 tokens of 8 heads (67 MB, a read of which takes 11) 15 and the
+// join of their splits 4.
 #include "tri_attend.h"
 
 namespace tri {
@@ -360,7 +367,7 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
     const int64_t groups = sq.B * c.heads * p.tiles, cus = cu_count();
     // Tall tiles: one pass over a tile's steps, unless the tiles leave half the CUs idle (what joins splits moves as much as many
     // steps do).  Up to two tiles per CU, the longest tile's steps are what the call waits for: two groups of waves share them
-    // (2048 tokens of 32 heads, 512 tiles: 62 -> 57 us; 880 tiles of two chunks over a window: 97 us, 114 with pairs).
+    // (2048 tokens of 32 heads, 512 tiles: 62 us without, 57 with; 880 tiles over a window: 97 us without, 114 with).
     p.pair = p.tall && groups <= 2 * cus;
     const int64_t want = p.tall ? (groups * 2 > cus ? 1 : cus / groups) : (cus + groups - 1) / groups;
     int64_t chunk = (steps + want - 1) / want;

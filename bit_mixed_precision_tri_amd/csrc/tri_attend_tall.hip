@@ -5,6 +5,13 @@
 // into the other and those after are on their way).  Both products are transposed as in tri_attend.hip, on
 // v_mfma_f32_32x32x16_f16: a lane holds 16 weights of one row for every 32 tokens, which are its B operand of the second
 // product as they lie; values are stored in LDS in the order of a lane's tokens, so that an A operand is one 16-byte read.
+//
+// What bounds it is that the softmax and the decoding (vector ALU) and the products (matrix cores) overlap only across the two
+// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 59 us, 580 TFLOP/s; the last 2048 of
+// 16384 tokens of 8 heads (32 of queries) 610 us, 840; 1000 tokens over a window of 1024, 64 heads (59.6 GFLOP) 103, 580.
+// The products and their LDS reads alone take 30 us of the 59.  Measured and not taken:
+// eight waves on one step's codes (93 us for 97 over the window, but uneven for short prompts), the groups in strict turns
+// with two barriers a round (67 - 76 us for 57), one step's weights beside the last step's values in a wave (60).
 #include "tri_attend.h"
 
 namespace tri {

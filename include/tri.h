@@ -421,7 +421,7 @@ int64_t tri_cache_attend_workspace_bytes(const tri_cache *cache, const tri_seque
  * A row that sees nothing is 0; rows of no sequence (before offsets[0] or behind offsets[B]) and
  * rows behind a sequence's first max_new stay as they are.
  * Scores, softmax and sums are fp32; the weights, relative to the largest, enter the second product as
- * fp16.  Q, O: rows of `heads` heads, as X and Y of tri_heads (O must not overlap Q); heads is a multiple of cache->heads;
+ * fp16 (where a key/value head has at most 32 query rows, as the sum of two).  Q, O: rows of `heads` heads, as X and Y of tri_heads (O must not overlap Q); heads is a multiple of cache->heads;
  * scale is finite; T*heads < 2^31.  workspace: 16-byte aligned, of at least
  * tri_cache_attend_workspace_bytes bytes, overwritten; NULL where that is 0.  Calls that share one must
  * be ordered.  Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
