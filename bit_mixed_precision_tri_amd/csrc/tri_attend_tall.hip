@@ -7,9 +7,9 @@
 // product as they lie; values are stored in LDS in the order of a lane's tokens, so that an A operand is one 16-byte read.
 //
 // What bounds it is that the softmax and the decoding (vector ALU) and the products (matrix cores) overlap only across the two
-// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 59 us, 580 TFLOP/s; the last 2048 of
-// 16384 tokens of 8 heads (32 of queries) 610 us, 840; 1000 tokens over a window of 1024, 64 heads (59.6 GFLOP) 103, 580.
-// The products and their LDS reads alone take 30 us of the 59.  Measured and not taken:
+// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 58 us, 600 TFLOP/s; the last 2048 of
+// 16384 tokens of 8 heads (32 of queries) 610 us, 840; 1000 tokens over a window of 1024, 64 heads (59.6 GFLOP) 101, 590.
+// The products and their LDS reads alone take 30 us of the 58.  Measured and not taken:
 // eight waves on one step's codes (93 us for 97 over the window, but uneven for short prompts), the groups in strict turns
 // with two barriers a round (67 - 76 us for 57), one step's weights beside the last step's values in a wave (60).
 #include "tri_attend.h"
@@ -287,6 +287,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
+            float den[BLK], least = 1.f;
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
                 const float shift = lu[k] + (kLift - m[ct]);
@@ -294,13 +295,24 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                 for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
                 const u32x4 pk = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
-                // the denominator takes the weights as they are rounded, so that what flat weights are off by together cancels; of
-                // small ones (values of a small scale are) it takes them as they are, since in fp16 nothing may be left of them
-                const float add = ((y[0] + y[1]) + (y[2] + y[3])) + ((y[4] + y[5]) + (y[6] + y[7]));
-                const float rounded = dot2(pk[3], 0x3C003C00u, dot2(pk[2], 0x3C003C00u, dot2(pk[1], 0x3C003C00u, dot2(pk[0], 0x3C003C00u, 0.f))));
-                sum[ct] = fmaf(rounded >= 1.f ? rounded : add, iu[k], sum[ct]);
+                // the denominator takes the weights as they are rounded, so that what flat weights are off by together cancels
+                den[k] = dot2(pk[3], 0x3C003C00u, dot2(pk[2], 0x3C003C00u, dot2(pk[1], 0x3C003C00u, dot2(pk[0], 0x3C003C00u, 0.f))));
+                least = fminf(least, den[k]);
                 w[ct][k] = __builtin_bit_cast(half8_t, pk);
             }
+            // of small ones (values of a small scale are) it takes them as they are, since in fp16 nothing may be left of them
+            if (__any(least < 1.f)) {
+#pragma unroll
+                for (int k = 0; k < BLK; ++k) {
+                    const float shift = lu[k] + (kLift - m[ct]);
+                    float add = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) add += exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
+                    if (den[k] < 1.f) den[k] = add;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BLK; ++k) sum[ct] = fmaf(den[k], iu[k], sum[ct]);
         }
     };
 
