@@ -751,19 +751,17 @@ class Sequences:
         _need(offsets.shape == (B + 1,) and lens.shape == (B,), "offsets must be (B + 1), lens (B)")
         _need(max_new > 0 and (max_len is None or max_len > 0), "max_new and max_len must be at least 1")
         self.offsets, self.lens, self.table, self.device = offsets, lens, table, dev
-        most = min(128 * width, (1 << 31) - 129)
-        self.struct = TriSequences(offsets.data_ptr(), lens.data_ptr(), table.data_ptr(), B, width, max_new,
-                                   most if max_len is None else max_len)
-        self._whole = max_len is None
-        self._ref = ctypes.addressof(self.struct)
+        # a struct for every size of a page: calls of several threads on several caches may share the sequences
+        self.structs = {page: TriSequences(offsets.data_ptr(), lens.data_ptr(), table.data_ptr(), B, width, max_new,
+                                           min(page * width, (1 << 31) - 129) if max_len is None else max_len)
+                        for page in (16, 32, 64, 128)}
+        self._refs = {page: ctypes.addressof(s) for page, s in self.structs.items()}
 
     def _fit(self, cache):
         """The struct's address for a call on `cache`."""
         if self.device != cache.device:
             raise ValueError("the sequences must be on the cache's device")
-        if self._whole:
-            self.struct.max_len = min(self.struct.width * cache.page, (1 << 31) - 129)
-        return self._ref
+        return self._refs[cache.page]
 
 
 _pack_heads = struct.Struct("PPPqqi4x").pack     # tri_heads
@@ -830,7 +828,7 @@ def cache_append(cache, seqs, K, V, rotary=None, Q=None, out=None, stream=None):
 def cache_attend_workspace_bytes(cache, seqs, T, heads, window=0, sinks=0):
     """What cache_attend needs as workspace for T new tokens of `heads` query heads (0: none)."""
     seqs._fit(cache)
-    need = tri_cache_attend_workspace_bytes(cache.struct, seqs.struct, T, heads, window, sinks)
+    need = tri_cache_attend_workspace_bytes(cache.struct, seqs.structs[cache.page], T, heads, window, sinks)
     _need(need >= 0, "sizes that tri_cache_attend does not take")
     return need
 

@@ -134,6 +134,7 @@ int check_heads(const tri_heads &h, int64_t T, int dim)
 {
     if (!h.X || !h.Y || h.heads < 1 || h.heads > kMaxHeads || T * h.heads >= kMaxDim) return TRI_EINVAL;
     if (bad_stride(h.x_stride, (int64_t)h.heads * dim) || bad_stride(h.y_stride, (int64_t)h.heads * dim)) return TRI_EINVAL;
+    if (h.X == h.Y && h.x_stride != h.y_stride) return TRI_EINVAL;
     if (misaligned(h.X) || misaligned(h.Y) || misaligned(h.gain)) return TRI_EALIGN;
     return TRI_OK;
 }
@@ -472,7 +473,7 @@ int tri_cache_attend(const tri_cache *cache, const tri_sequences *seqs, int64_t 
     if (rc != TRI_OK) return rc;
     const int64_t row = (int64_t)heads * cache->dim;
     if (bad_attend(cache, T, heads, window, sinks) || !Q || !O || bad_stride(q_stride, row) || bad_stride(o_stride, row)) return TRI_EINVAL;
-    if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return TRI_EINVAL;           // (NaN fails)
+    if (Q == O || !(scale >= -3.4e38f && scale <= 3.4e38f)) return TRI_EINVAL;   // (NaN fails)
     const int64_t need = attend_workspace_bytes(*cache, *seqs, (int)T, heads, window, sinks);
     if (need > 0 && (!workspace || workspace_bytes < need)) return TRI_EINVAL;
     if (misaligned(Q) || misaligned(O) || misaligned(workspace)) return TRI_EALIGN;

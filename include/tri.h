@@ -401,8 +401,8 @@ typedef struct tri_sequences {
  * rotated by the same launch, as tri_heads_rotate would at these positions; rows of no sequence, behind
  * a sequence's first max_new, or at a position that is negative or outside the rotation's table are
  * not written.
- * A page that gets new tokens must belong to one sequence; calls that write the same pages must be
- * ordered.  K, V and queries must not overlap the cache.
+ * A page that gets new tokens must belong to one sequence and stand there once; calls that write the same
+ * pages must be ordered.  K, V and queries must not overlap the cache.
  * Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
 int tri_cache_append(const tri_cache *cache, const tri_sequences *seqs, int64_t T, const _Float16 *K,
                      int64_t k_stride, const _Float16 *V, int64_t v_stride, const tri_rotary *rot,

@@ -135,6 +135,18 @@ def test_attend_refusals_and_workspace():
         assert call(**kw) == EALIGN, kw
 
 
+def test_results_over_their_inputs_are_refused():
+    """Rows that would overlap others' inputs: attention in place, rotation in place with another stride."""
+    def rotate(h):
+        return raw("tri_heads_rotate", ctypes.addressof(h), 1, 5, 128, at(rotary()), ODD, None)
+
+    assert rotate(heads(Y=A, y_stride=520)) == EINVAL and rotate(heads(Y=A, x_stride=1024)) == EINVAL
+    assert rotate(heads(Y=A)) == EALIGN          # (in place with the same stride: refused for the positions' address only)
+    queries = heads(Y=A, y_stride=520)
+    assert raw("tri_cache_append", at(cache()), at(seqs()), 3, A, 512, B, 512, at(rotary()), None, at(queries), None) == EINVAL
+    assert raw("tri_cache_attend", at(cache()), at(seqs()), 3, A, 512, 4, 0.1, 0, 0, A, 512, None, 0, None) == EINVAL
+
+
 def test_binding_raises_on_error_status():
     with pytest.raises(tri.TriError):
         tri.tri_heads_rotate([heads(heads=0)], 1, 128, rotary(), D, stream=0)

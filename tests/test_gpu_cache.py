@@ -679,3 +679,24 @@ def test_helpers_refusals():
         tri.cache_attend(cache, seqs, torch.zeros((3, 5, 64), **f16), workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         tri.cache_attend_workspace_bytes(cache, seqs, 3, 5)
+
+
+def test_sequences_that_caches_of_other_pages_share():
+    """One Sequences without max_len for two caches: each call is sized by its own cache's pages, whichever came last."""
+    import torch
+    rng = np.random.default_rng(35)
+    D, width = 64, 40
+    K = rng.standard_normal((1, 2, D)).astype(np.float16)
+    q = cuda(rng.standard_normal((1, 8, D)).astype(np.float16))
+    seqs = tri.Sequences(cuda(np.array([0, 1], np.int32)), cuda(np.array([width * 16], np.int32)),
+                         cuda(rng.permutation(width).astype(np.int32)[None]), 1)
+    caches = [tri.KVCache.empty(width, 2, D, page, INT8) for page in (16, 128)]
+    need = [tri.cache_attend_workspace_bytes(c, seqs, 1, 8) for c in caches]
+    assert [tri.cache_attend_workspace_bytes(c, seqs, 1, 8) for c in caches[::-1]] == need[::-1] and need[0] < need[1]
+    for c in caches:                             # (scales of 1, large enough for the new token: all values are 3)
+        c.K.copy_(torch.randint(0, 256, c.K.shape, device="cuda"))
+        c.V.fill_(3)
+        tri.cache_append(c, seqs, cuda(K), cuda(np.full_like(K, 3)))
+    for c, n in list(zip(caches, need)) * 2:
+        o = tri.cache_attend(c, seqs, q, workspace=torch.empty(max(n, 16), dtype=torch.uint8, device="cuda"))
+        assert np.abs(host(o).astype(np.float64) - 3).max() <= 3 * 2.0 ** -11    # (one rounding to fp16)
