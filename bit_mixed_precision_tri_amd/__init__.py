@@ -769,6 +769,9 @@ _pack_heads = struct.Struct("PPPqqi4x").pack     # tri_heads
 
 def _heads_of(x, what, dim, device, T, heads):
     """Address and token stride of a (T, heads, dim) float16 tensor whose tokens may lie apart."""
+    if (x.is_contiguous() and x.dtype is _torch.float16 and x.get_device() == device and x.shape == (T, heads, dim) and
+            heads > 0):                          # (the usual case, in half the time)
+        return x.data_ptr(), heads * dim
     shape, stride = x.shape, x.stride()
     if not (shape == (T, heads, dim) and x.dtype is _torch.float16 and x.get_device() == device and stride[2] == 1 and
             (stride[1] == dim or heads == 1) and heads > 0):
