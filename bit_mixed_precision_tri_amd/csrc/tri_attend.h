@@ -78,6 +78,21 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return __builtin_bit_cast(uint32_t, h);
 }
 
+// Two weights, each as the sum of two fp16 numbers: x the nearest ones, y what these leave off.  (minus: -1, in a register that the
+// compiler cannot see through, so that a weight less its fp16 number is one fma that takes the half as it lies.)
+__device__ __forceinline__ float minus_one()
+{
+    float x = -1.f;
+    asm("" : "+v"(x));
+    return x;
+}
+__device__ __forceinline__ uint2 split2(float a, float b, float minus)
+{
+    uint32_t hi = pack2(a, b);
+    asm("" : "+v"(hi));
+    return make_uint2(hi, pack2(fmaf(h2f((uint16_t)hi), minus, a), fmaf(h2f((uint16_t)(hi >> 16)), minus, b)));
+}
+
 // Four results of a row: its sum over its denominator; 0 for a row that saw nothing (its sum is 0, too).
 template <int FMT>
 __device__ __forceinline__ void store_row(uint16_t *y, const float4_t &v, float den)

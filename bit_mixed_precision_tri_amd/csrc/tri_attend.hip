@@ -5,9 +5,9 @@
 //     o = sum_j w_j v_j / sum_j (w_j / u_j).
 // The values' scales sit in the exponents, so that w_j (rounded to fp16: normal numbers down to 2^-24 of the largest) is the
 // operand of the second product and the codes, exact in fp16, are the other; however small a scale is, nothing underflows.
-// m, the two sums and o run on over the tokens (when m grows, the others shrink by 2^(m - m')).  With few rows the matrix cores
-// have time for a second product, of what the rounding of the weights left off: results are then as exact as fp32 weights'
-// (an error of 2.1e-4 of the results' size, all of it their own rounding to fp16; 2.9e-4 without, as for many rows).
+// m, the two sums and o run on over the tokens (when m grows, the others shrink by 2^(m - m')).  What the rounding of a weight to
+// fp16 leaves off is an operand of its own, with the same codes: weights are exact to 2^-22, and results carry little more than their
+// own rounding to fp16 (an error of 2.1e-4 of their size, as with weights of fp32).
 //
 // Both products are taken transposed: S^T = K Q^T (a row of A is a token, a column of B a query row), O^T = V^T W^T.  A lane of
 // S^T then holds weights of one query row, and they are its part of the second product's B operand as they lie: the

@@ -6,12 +6,14 @@
 // v_mfma_f32_32x32x16_f16: a lane holds 16 weights of one row for every 32 tokens, which are its B operand of the second
 // product as they lie; values are stored in LDS in the order of a lane's tokens, so that an A operand is one 16-byte read.
 //
+// A weight is the sum of two fp16 numbers, each a product with the values' codes: as one alone it would be off by up to 2^-11,
+// more than the scores are, and than the rounding of a result where values cancel; a call's size would show in its results.  The
+// third product of a step costs 2048 tokens of 32 heads 57.5 -> 65 - 70 us, 1000 over a window of 1024 101 -> 114 - 119.
+//
 // What bounds it is that the softmax and the decoding (vector ALU) and the products (matrix cores) overlap only across the two
-// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 58 us, 600 TFLOP/s; the last 2048 of
-// 16384 tokens of 8 heads (32 of queries) 610 us, 840; 1000 tokens over a window of 1024, 64 heads (59.6 GFLOP) 101, 590.
-// The products and their LDS reads alone take 30 us of the 58.  Measured and not taken:
-// eight waves on one step's codes (93 us for 97 over the window, but uneven for short prompts), the groups in strict turns
-// with two barriers a round (67 - 76 us for 57), one step's weights beside the last step's values in a wave (60).
+// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 65 us, 525 TFLOP/s; 1000 tokens over a
+// window of 1024, 64 heads (59.6 GFLOP), 114, 521.  Measured and not taken, with one product of the weights (57.5 us): the groups in
+// strict turns with two barriers a round (67 - 76), one step's weights beside the last step's values in a wave (60).
 #include "tri_attend.h"
 
 namespace tri {
@@ -163,6 +165,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         }
     };
 
+    const float minus = minus_one();
     float m[QT], sum[QT];
     float16_t o[QT][DT];
 #pragma unroll
@@ -185,7 +188,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         return *reinterpret_cast<const half8_t *>(bytes + buf * (2 * D * VC * 16) + (val0 ^ (32 * k)) + d * (32 * VC * 16));
     };
     float16_t s[QT][TT];
-    half8_t w[QT][BLK];
+    half8_t w[QT][BLK], wl[QT][BLK];                     // weights, and what their rounding to fp16 left off
     // Operands are read two products (of every accumulator) ahead: the groups of the schedule keep the compiler to that.
     auto values = [&](int buf) {
         half8_t va[2][DT];
@@ -201,11 +204,15 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             for (int d = 0; d < DT; ++d)
 #pragma unroll
                 for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], w[ct][k], o[ct][d]);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], wl[ct][k], o[ct][d]);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, DT + 1, 0);
 #pragma unroll
         for (int i = 0; i < BLK * DT; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, QT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 2 * QT, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
     };
@@ -287,32 +294,24 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
-            float den[BLK], least = 1.f;
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
                 const float shift = lu[k] + (kLift - m[ct]);
-                float y[8];
+                float den = 0.f;
+                u32x4 hi, lo;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
-                const u32x4 pk = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
-                // the denominator takes the weights as they are rounded, so that what flat weights are off by together cancels
-                den[k] = dot2(pk[3], 0x3C003C00u, dot2(pk[2], 0x3C003C00u, dot2(pk[1], 0x3C003C00u, dot2(pk[0], 0x3C003C00u, 0.f))));
-                least = fminf(least, den[k]);
-                w[ct][k] = __builtin_bit_cast(half8_t, pk);
-            }
-            // of small ones (values of a small scale are) it takes them as they are, since in fp16 nothing may be left of them
-            if (__any(least < 1.f)) {
-#pragma unroll
-                for (int k = 0; k < BLK; ++k) {
-                    const float shift = lu[k] + (kLift - m[ct]);
-                    float add = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) add += exp2_(fmaf(s[ct][k / 2][8 * (k % 2) + e], a[k], shift));
-                    if (den[k] < 1.f) den[k] = add;
+                for (int e = 0; e < 4; ++e) {
+                    const int at = 8 * (k % 2) + 2 * e;
+                    const float y0 = exp2_(fmaf(s[ct][k / 2][at], a[k], shift)), y1 = exp2_(fmaf(s[ct][k / 2][at + 1], a[k], shift));
+                    den += y0 + y1;
+                    const uint2 x = split2(y0, y1, minus);
+                    hi[e] = x.x;
+                    lo[e] = x.y;
                 }
+                w[ct][k] = __builtin_bit_cast(half8_t, hi);
+                wl[ct][k] = __builtin_bit_cast(half8_t, lo);
+                sum[ct] = fmaf(den, iu[k], sum[ct]);
             }
-#pragma unroll
-            for (int k = 0; k < BLK; ++k) sum[ct] = fmaf(den[k], iu[k], sum[ct]);
         }
     };
 
