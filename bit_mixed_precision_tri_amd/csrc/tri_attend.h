@@ -8,7 +8,12 @@ constexpr int kStep = 64;                        // tokens of a step
 // Weights are lifted by 2^10; the running maximum follows only when it is 2^5 behind: a weight stays below 2^15, and the sums
 // need no scaling in most steps.
 constexpr float kLift = 10.f, kSlack = 5.f;
-constexpr float kNone = -1e30f;                  // the running maximum of a row that has seen nothing
+constexpr float kNone = -3.402823466e38f;        // the running maximum of a row that has seen nothing
+// A running maximum this far from 0 is off from its score's exponent, which is rounded once and elsewhere, by as much as a weight may
+// be off; much further, by more than fp16's exponents hold.  There exponents are differences of rounded numbers, at one operation
+// more per score, so that the largest is 0.
+constexpr float kFar = 1048576.f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m > kNone; }
 
 // The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
 struct Steps {

@@ -201,18 +201,23 @@ __device__ __forceinline__ void attend_few(const Attend &at, float *__restrict__
 #pragma unroll
             for (int e = 1; e < 16; ++e) top = fmaxf(top, s[ct][e]);
             const float mx = max_over_rows(fmaxf(kNone, fmaf(top, a, lu)));    // (a > 0)
-            if (__any(mx > m[ct] + kSlack)) {
+            if (__any(mx - m[ct] > kSlack)) {
                 const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
                 m[ct] = mn;
                 l[ct] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
-            const float shift = lu + (kLift - m[ct]);
-            float sum = 0.f;
+            float shift = lu + (kLift - m[ct]), f = a, sum = 0.f;
+            if (is_far(m[ct])) {                 // (by row: no row goes by what others hold)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[ct][e] = fmaf(s[ct][e], a, lu) - m[ct];
+                shift = kLift;
+                f = 1.f;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float y0 = exp2_(fmaf(s[ct][2 * e], a, shift)), y1 = exp2_(fmaf(s[ct][2 * e + 1], a, shift));
+                const float y0 = exp2_(fmaf(s[ct][2 * e], f, shift)), y1 = exp2_(fmaf(s[ct][2 * e + 1], f, shift));
                 sum += y0 + y1;
                 const uint32_t x = pack2(y0, y1);
                 w[ct][e / 4][e % 4] = x;

@@ -287,22 +287,39 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
             swap32(mx, other);
             mx = fmaxf(mx, other);
             // m need not be the maximum: within 2^kSlack of it, weights still are fp16 numbers and o stays as it is
-            if (__any(mx > m[ct] + kSlack)) {
+            if (__any(mx - m[ct] > kSlack)) {
                 const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
                 m[ct] = mn;
                 sum[ct] *= f;
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[ct][d] *= f;
             }
+            float f[BLK], shift[BLK];
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
-                const float shift = lu[k] + (kLift - m[ct]);
+                f[k] = a[k];
+                shift[k] = lu[k] + (kLift - m[ct]);
+            }
+            if (is_far(m[ct])) {                 // (by row: no row goes by what others hold)
+#pragma unroll
+                for (int k = 0; k < BLK; ++k) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int at = 8 * (k % 2) + e;
+                        s[ct][k / 2][at] = fmaf(s[ct][k / 2][at], a[k], lu[k]) - m[ct];
+                    }
+                    f[k] = 1.f;
+                    shift[k] = kLift;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BLK; ++k) {
                 float den = 0.f;
                 u32x4 hi, lo;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int at = 8 * (k % 2) + 2 * e;
-                    const float y0 = exp2_(fmaf(s[ct][k / 2][at], a[k], shift)), y1 = exp2_(fmaf(s[ct][k / 2][at + 1], a[k], shift));
+                    const float y0 = exp2_(fmaf(s[ct][k / 2][at], f[k], shift[k])), y1 = exp2_(fmaf(s[ct][k / 2][at + 1], f[k], shift[k]));
                     den += y0 + y1;
                     const uint2 x = split2(y0, y1, minus);
                     hi[e] = x.x;

@@ -420,8 +420,9 @@ int64_t tri_cache_attend_workspace_bytes(const tri_cache *cache, const tri_seque
  * used).  A position whose page is outside 0..pages-1, or that has no place in the table, is not seen.
  * A row that sees nothing is 0; rows of no sequence (before offsets[0] or behind offsets[B]) and
  * rows behind a sequence's first max_new stay as they are.
- * Scores, softmax and sums are fp32; a weight enters the second product as the sum of two fp16 numbers (off by
- * 2^-22 of itself, or 2^-35 of the largest product of a weight and its value's scale).  Q, O: rows of `heads` heads, as X and Y of tri_heads
+ * Scores, softmax and sums are fp32 (a score that, times log2(e), passes fp32's range spoils its row); a
+ * weight enters the second product as the sum of two fp16 numbers (off by 2^-22 of itself, or 2^-35 of
+ * the largest product of a weight and its value's scale).  Q, O: rows of `heads` heads, as X and Y of tri_heads
  * (O must not overlap Q); heads is a multiple of cache->heads; scale is finite; T*heads < 2^31.
  * workspace: 16-byte aligned, of at least tri_cache_attend_workspace_bytes bytes, overwritten; NULL where
  * that is 0.  Calls that share one must be ordered.  Errors: TRI_EINVAL, TRI_EALIGN, TRI_EHIP. */
