@@ -15,18 +15,19 @@ constexpr float kNone = -3.402823466e38f;        // the running maximum of a row
 constexpr float kFar = 1048576.f;
 __device__ __forceinline__ bool is_far(float m) { return fabsf(m) >= kFar && m > kNone; }
 
-// The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.
+// The steps that rows of positions pa .. pb (pa <= pb) see some token of: 0 .. head-1, then from .. from + tail - 1.  None of them
+// lies behind the `room` steps that the table of pages has places for, whatever a length says.
 struct Steps {
     int head, from, tail;
     __device__ __forceinline__ int count() const { return head + tail; }
     __device__ __forceinline__ int at(int i) const { return i < head ? i : from + (i - head); }
 };
-__device__ __forceinline__ Steps steps_of(int pa, int pb, int window, int sinks)
+__device__ __forceinline__ Steps steps_of(int pa, int pb, int window, int sinks, int room)
 {
     if (pb < 0) return Steps{0, 0, 0};
-    const int last = pb / kStep + 1;
+    const int last = min(pb / kStep + 1, room);
     if (window == 0) return Steps{0, 0, last};
-    const int from = max((int)((int64_t)pa - window + 1 < 0 ? 0 : pa - window + 1), 0) / kStep;
+    const int from = min(max((int)((int64_t)pa - window + 1 < 0 ? 0 : pa - window + 1), 0) / kStep, last);
     const int head = min((int)(((int64_t)min(sinks, pb + 1) + kStep - 1) / kStep), from);
     return Steps{head, from, last - from};
 }
@@ -45,7 +46,7 @@ __device__ __forceinline__ Tile tile_of(const Attend &at, int b, int r0, int hei
     t.rows = (int)min(max(R - r0, (int64_t)0), (int64_t)height);
     t.pa = t.sp.p0 + r0 / at.G;
     t.pb = t.sp.p0 + (r0 + t.rows - 1) / at.G;
-    t.st = t.rows > 0 ? steps_of(t.pa, t.pb, at.window, at.sinks) : Steps{0, 0, 0};
+    t.st = t.rows > 0 ? steps_of(t.pa, t.pb, at.window, at.sinks, at.room) : Steps{0, 0, 0};
     return t;
 }
 

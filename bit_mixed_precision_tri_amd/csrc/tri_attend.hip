@@ -21,6 +21,7 @@
 // sequence alone is bound by latency: 333 tokens 6.7 us; 32768 tokens of 8 heads (67 MB, a read of which takes 11) 15 and the
 // join of their splits 4.
 #include "tri_attend.h"
+#include <algorithm>
 
 namespace tri {
 
@@ -357,6 +358,12 @@ constexpr int few_waves(int dim, int ct) { return dim == 256 || (dim == 128 && c
 // Workgroups of k_join: it takes further rows in a loop.
 constexpr int64_t kMostGroups = 1 << 20;
 
+// (positions end before 2^31, and so do steps before 2^25)
+int room_of(const tri_cache &c, const tri_sequences &sq)
+{
+    return (int)std::min((sq.width * c.page + kStep - 1) / kStep, (int64_t)1 << 25);
+}
+
 AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks)
 {
     AttendPlan p;
@@ -364,7 +371,7 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
     p.tall = rows > 32;
     p.height = p.tall ? tall_height(c.dim) : rows <= 16 || c.dim == 256 ? 16 : 32;
     p.tiles = (int)((rows + p.height - 1) / p.height);
-    int64_t steps = (sq.max_len + kStep - 1) / kStep;
+    int64_t steps = std::min((sq.max_len + kStep - 1) / kStep, (int64_t)room_of(c, sq));
     if (window > 0) {
         const int64_t seen = (window + p.height + kStep - 2) / kStep + 1 + ((sinks < sq.max_len ? sinks : sq.max_len) + kStep - 1) / kStep;
         steps = steps < seen ? steps : seen;
@@ -405,8 +412,9 @@ int64_t attend_workspace_bytes(const tri_cache &c, const tri_sequences &sq, int 
     return p.splits > 1 ? (int64_t)T * H * p.splits * (c.dim + 4) * 4 : 0;
 }
 
-int launch_attend(const Attend &at, void *workspace, hipStream_t s)
+int launch_attend(Attend at, void *workspace, hipStream_t s)
 {
+    at.room = room_of(at.c, at.sq);
     const AttendPlan p = plan_of(at.c, at.sq, at.T, at.H, at.window, at.sinks);
     float *part = static_cast<float *>(workspace);
     if (p.tall) launch_attend_tall(at, p, part, s);

@@ -218,9 +218,10 @@ struct Attend {
     int T, H, G;                                 // G: query heads of a key/value head
     float scale;
     int window, sinks;
+    int room;                                    // steps of 64 tokens that the table of pages has places for
 };
 int64_t attend_workspace_bytes(const tri_cache &c, const tri_sequences &sq, int T, int H, int64_t window, int64_t sinks);
-int launch_attend(const Attend &at, void *workspace, hipStream_t s);
+int launch_attend(Attend at, void *workspace, hipStream_t s);
 int launch_probe_read(const void *src, int64_t bytes, uint32_t *sink, hipStream_t s);
 int launch_probe_copy(const void *src, void *dst, int64_t bytes, hipStream_t s);
 int launch_probe_empty(int64_t workgroups, int threads, uint32_t *sink, hipStream_t s);
