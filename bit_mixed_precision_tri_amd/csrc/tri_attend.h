@@ -115,7 +115,7 @@ struct AttendPlan {
 };
 
 // tri_attend_tall.hip: rows of a tile, and the launch.
-int tall_height(int dim);
+constexpr int kTallRows = 128;
 void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipStream_t s);
 
 }  // namespace tri

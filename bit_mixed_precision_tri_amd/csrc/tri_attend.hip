@@ -369,7 +369,7 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
     AttendPlan p;
     const int64_t G = H / c.heads, most = sq.max_new < T ? sq.max_new : T, rows = most * G;
     p.tall = rows > 32;
-    p.height = p.tall ? tall_height(c.dim) : rows <= 16 || c.dim == 256 ? 16 : 32;
+    p.height = p.tall ? kTallRows : rows <= 16 || c.dim == 256 ? 16 : 32;
     p.tiles = (int)((rows + p.height - 1) / p.height);
     int64_t steps = std::min((sq.max_len + kStep - 1) / kStep, (int64_t)room_of(c, sq));
     if (window > 0) {

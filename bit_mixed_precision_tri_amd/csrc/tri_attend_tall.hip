@@ -1,6 +1,6 @@
 // tri_attend_tall.hip -- attention over the 8-bit cache for many query rows of a key/value head (prefill).
 //
-// A workgroup takes NW * 32 * QT rows, 32 QT a wave, and walks the steps that they see.  A step's codes are read once,
+// A workgroup takes 128 rows, 32 a wave, and walks the steps that they see.  A step's codes are read once,
 // decoded to fp16 once, and lie in LDS for all waves (two buffers: while one is used, the next step's codes are written
 // into the other and those after are on their way).  Both products are transposed as in tri_attend.hip, on
 // v_mfma_f32_32x32x16_f16: a lane holds 16 weights of one row for every 32 tokens, which are its B operand of the second
@@ -30,8 +30,7 @@ __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c)
 }
 
 template <int D> constexpr int kTallStep = D == 256 ? 32 : 64;   // tokens of a step here
-template <int D> constexpr int kTallWaves = 4;                   // waves that share a step
-template <int D> constexpr int kTallCols = 1;                    // tiles of 32 rows of a wave
+constexpr int kWaves = kTallRows / 32;                           // waves that share a step, 32 rows each
 // LDS of a group in 16-byte chunks: two buffers of keys, values and what belongs to 16 tokens.
 template <int D> constexpr int kTallLds = 4 * D * (kTallStep<D> / 8) + 2 * (kTallStep<D> / 16);
 
@@ -43,11 +42,11 @@ __device__ __forceinline__ int chunk_at(int r, int c)
     return r * N + (c ^ ((r / per) & (N >= 16 ? 15 : N - 1)));
 }
 
-template <int D, int FMT, int QT, int NW, int NG>
+template <int D, int FMT, int NG>
 __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict__ part, int splits, int chunk, int split, int h, int r0,
                                             int b, u32x4 *lds)
 {
-    constexpr int STEP = kTallStep<D>, NT = 64 * NW, HEIGHT = 32 * QT * NW;
+    constexpr int STEP = kTallStep<D>, NT = 64 * kWaves;
     constexpr int KC = D / 8, VC = STEP / 8;             // chunks of a key's and a value's row
     constexpr int KU = STEP * D / 16 / NT, VU = KU;      // 16-byte pieces of codes per thread
     constexpr int BLK = STEP / 16, TT = STEP / 32, DT = D / 32;
@@ -57,7 +56,7 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     u32x4 *const meta_at = lds + 4 * D * VC;             // (a, log2 u, 1 / u, whether the page is there) of 16 tokens
     const int lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), hf = lane >> 5, l = lane & 31;
     const tri_cache &c = at.c;
-    const Tile t = tile_of(at, b, r0, HEIGHT);
+    const Tile t = tile_of(at, b, r0, kTallRows);
     if (t.rows == 0) return;
     // (the plan counts steps of 64 tokens; a split's share in steps of this kernel's)
     constexpr int F = kStep / STEP;
@@ -70,20 +69,17 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     const int n0 = i0 * F + gr, n1 = i1 * F, rounds = (n1 - i0 * F + NG - 1) / NG;    // (the same for all groups)
     auto token_of = [&](int n) { return t.st.at(n / F) * kStep + (n % F) * STEP; };
 
-    // this wave's rows
-    half8_t q[QT][D / 16];
-    int pos[QT], wa = 0x7fffffff, wb = -1;               // positions of the wave's first and last row that exist
-#pragma unroll
-    for (int ct = 0; ct < QT; ++ct) {
-        const int w = (wv * QT + ct) * 32 + l, r = r0 + w, i = r / at.G;
-        const bool live = w < t.rows;
-        pos[ct] = live ? t.sp.p0 + i : -1;
-        const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? i : 0)) * at.q_stride + (h * at.G + (live ? r % at.G : 0)) * D + 8 * hf;
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s) q[ct][s] = __builtin_bit_cast(half8_t, *reinterpret_cast<const u32x4 *>(x + 16 * s) ^ flip);
-    }
+    // this wave's rows, and this lane's: row `mine` of the tile, of new token tok and query head `head`
+    const int mine = wv * 32 + l, tok = (r0 + mine) / at.G, head = h * at.G + (r0 + mine) % at.G;
+    const bool live = mine < t.rows;
+    const int pos = live ? t.sp.p0 + tok : -1;
+    int wa = 0x7fffffff, wb = -1;                        // positions of the wave's first and last row that exist
+    half8_t q[D / 16];
     {
-        const int w0 = wv * QT * 32, w1 = min(w0 + QT * 32, t.rows) - 1;
+        const uint16_t *x = at.Q + (int64_t)(t.sp.r0 + (live ? tok : 0)) * at.q_stride + (live ? head : h * at.G) * D + 8 * hf;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) q[s] = __builtin_bit_cast(half8_t, *reinterpret_cast<const u32x4 *>(x + 16 * s) ^ flip);
+        const int w0 = wv * 32, w1 = min(w0 + 32, t.rows) - 1;
         if (w0 <= w1) {
             wa = t.sp.p0 + (r0 + w0) / at.G;
             wb = t.sp.p0 + (r0 + w1) / at.G;
@@ -166,17 +162,12 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     };
 
     const float minus = minus_one();
-    float m[QT], sum[QT];
-    float16_t o[QT][DT];
+    float m = kNone, sum = 0.f;
+    float16_t o[DT];
 #pragma unroll
-    for (int ct = 0; ct < QT; ++ct) {
-        m[ct] = kNone;
-        sum[ct] = 0.f;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[ct][d][e] = 0.f;
-    }
+        for (int e = 0; e < 16; ++e) o[d][e] = 0.f;
 
     // A operands: chunk 2 k + hf of a row, where chunk_at puts it (its exclusive or with 2 k is one of the byte address, too)
     const char *const bytes = reinterpret_cast<const char *>(lds);
@@ -187,9 +178,9 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
     auto val = [&](int buf, int d, int k) {
         return *reinterpret_cast<const half8_t *>(bytes + buf * (2 * D * VC * 16) + (val0 ^ (32 * k)) + d * (32 * VC * 16));
     };
-    float16_t s[QT][TT];
-    half8_t w[QT][BLK], wl[QT][BLK];                     // weights, and what their rounding to fp16 left off
-    // Operands are read two products (of every accumulator) ahead: the groups of the schedule keep the compiler to that.
+    float16_t s[TT];
+    half8_t w[BLK], wl[BLK];                             // weights, and what their rounding to fp16 left off
+    // Operands are read two products ahead: the groups of the schedule keep the compiler to that.
     auto values = [&](int buf) {
         half8_t va[2][DT];
 #pragma unroll
@@ -201,18 +192,14 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
                 for (int d = 0; d < DT; ++d) va[(k + 1) & 1][d] = val(buf, d, k + 1);
             }
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
+            for (int d = 0; d < DT; ++d) o[d] = mfma32(va[k & 1][d], w[k], o[d]);
 #pragma unroll
-                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], w[ct][k], o[ct][d]);
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-#pragma unroll
-                for (int ct = 0; ct < QT; ++ct) o[ct][d] = mfma32(va[k & 1][d], wl[ct][k], o[ct][d]);
+            for (int d = 0; d < DT; ++d) o[d] = mfma32(va[k & 1][d], wl[k], o[d]);
         }
         __builtin_amdgcn_sched_group_barrier(0x100, DT + 1, 0);
 #pragma unroll
         for (int i = 0; i < BLK * DT; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, 2 * QT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
     };
@@ -229,20 +216,18 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
                 for (int tt = 0; tt < TT; ++tt) ka[(k + 2) % 3][tt] = key(buf, tt, k + 2);
             }
 #pragma unroll
-            for (int tt = 0; tt < TT; ++tt)
+            for (int tt = 0; tt < TT; ++tt) {
+                if (k == 0) {
 #pragma unroll
-                for (int ct = 0; ct < QT; ++ct) {
-                    if (k == 0) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) s[ct][tt][e] = 0.f;
-                    }
-                    s[ct][tt] = mfma32(ka[k % 3][tt], q[ct][k], s[ct][tt]);
+                    for (int e = 0; e < 16; ++e) s[tt][e] = 0.f;
                 }
+                s[tt] = mfma32(ka[k % 3][tt], q[k], s[tt]);
+            }
         }
         __builtin_amdgcn_sched_group_barrier(0x100, 2 * TT + 1, 1);
 #pragma unroll
         for (int i = 0; i < TT * D / 16; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x8, QT, 1);
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 1);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
         }
     };
@@ -260,75 +245,72 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         }
         const bool whole = t0 + STEP - 1 <= wa && (at.window == 0 || wb - t0 < at.window || t0 + STEP <= at.sinks) &&
                            __builtin_amdgcn_readfirstlane(there) != 0;
+        if (!whole) {
+            const unsigned long long seen = seen_of(pos, t0 + 4 * hf, at.window, at.sinks);
+            uint32_t part_of[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-        for (int ct = 0; ct < QT; ++ct) {
-            if (!whole) {
-                const unsigned long long seen = seen_of(pos[ct], t0 + 4 * hf, at.window, at.sinks);
-                uint32_t part_of[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+            for (int k = 0; k < BLK; ++k)
+                if (meta_at[buf * BLK + k][3] == 0u) part_of[k / 2] &= k % 2 ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
-                for (int k = 0; k < BLK; ++k)
-                    if (meta_at[buf * BLK + k][3] == 0u) part_of[k / 2] &= k % 2 ? 0x0000FFFFu : 0xFFFF0000u;
+            for (int k = 0; k < BLK; ++k)
 #pragma unroll
-                for (int k = 0; k < BLK; ++k)
+                for (int e = 0; e < 8; ++e)
+                    if ((part_of[k / 2] >> (16 * (k % 2) + 8 * (e / 4) + e % 4) & 1u) == 0u) s[k / 2][8 * (k % 2) + e] = -INFINITY;
+        }
+        // the largest y of a block is its largest score's (a > 0)
+        float mx = kNone;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if ((part_of[k / 2] >> (16 * (k % 2) + 8 * (e / 4) + e % 4) & 1u) == 0u) s[ct][k / 2][8 * (k % 2) + e] = -INFINITY;
-            }
-            // the largest y of a block is its largest score's (a > 0)
-            float mx = kNone;
+        for (int k = 0; k < BLK; ++k) {
+            float top = s[k / 2][8 * (k % 2)];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, s[k / 2][8 * (k % 2) + e]);
+            mx = fmaxf(mx, fmaf(top, a[k], lu[k]));
+        }
+        float other = mx;
+        swap32(mx, other);
+        mx = fmaxf(mx, other);
+        // m need not be the maximum: within 2^kSlack of it, weights still are fp16 numbers and o stays as it is
+        if (__any(mx - m > kSlack)) {
+            const float mn = fmaxf(m, mx), f = exp2_(m - mn);
+            m = mn;
+            sum *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+        float f[BLK], shift[BLK];
+#pragma unroll
+        for (int k = 0; k < BLK; ++k) {
+            f[k] = a[k];
+            shift[k] = lu[k] + (kLift - m);
+        }
+        if (is_far(m)) {                         // (by row: no row goes by what others hold)
 #pragma unroll
             for (int k = 0; k < BLK; ++k) {
-                float top = s[ct][k / 2][8 * (k % 2)];
 #pragma unroll
-                for (int e = 1; e < 8; ++e) top = fmaxf(top, s[ct][k / 2][8 * (k % 2) + e]);
-                mx = fmaxf(mx, fmaf(top, a[k], lu[k]));
-            }
-            float other = mx;
-            swap32(mx, other);
-            mx = fmaxf(mx, other);
-            // m need not be the maximum: within 2^kSlack of it, weights still are fp16 numbers and o stays as it is
-            if (__any(mx - m[ct] > kSlack)) {
-                const float mn = fmaxf(m[ct], mx), f = exp2_(m[ct] - mn);
-                m[ct] = mn;
-                sum[ct] *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[ct][d] *= f;
-            }
-            float f[BLK], shift[BLK];
-#pragma unroll
-            for (int k = 0; k < BLK; ++k) {
-                f[k] = a[k];
-                shift[k] = lu[k] + (kLift - m[ct]);
-            }
-            if (is_far(m[ct])) {                 // (by row: no row goes by what others hold)
-#pragma unroll
-                for (int k = 0; k < BLK; ++k) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int at = 8 * (k % 2) + e;
-                        s[ct][k / 2][at] = fmaf(s[ct][k / 2][at], a[k], lu[k]) - m[ct];
-                    }
-                    f[k] = 1.f;
-                    shift[k] = kLift;
+                for (int e = 0; e < 8; ++e) {
+                    const int at = 8 * (k % 2) + e;
+                    s[k / 2][at] = fmaf(s[k / 2][at], a[k], lu[k]) - m;
                 }
+                f[k] = 1.f;
+                shift[k] = kLift;
             }
+        }
 #pragma unroll
-            for (int k = 0; k < BLK; ++k) {
-                float den = 0.f;
-                u32x4 hi, lo;
+        for (int k = 0; k < BLK; ++k) {
+            float den = 0.f;
+            u32x4 hi, lo;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int at = 8 * (k % 2) + 2 * e;
-                    const float y0 = exp2_(fmaf(s[ct][k / 2][at], f[k], shift[k])), y1 = exp2_(fmaf(s[ct][k / 2][at + 1], f[k], shift[k]));
-                    den += y0 + y1;
-                    const uint2 x = split2(y0, y1, minus);
-                    hi[e] = x.x;
-                    lo[e] = x.y;
-                }
-                w[ct][k] = __builtin_bit_cast(half8_t, hi);
-                wl[ct][k] = __builtin_bit_cast(half8_t, lo);
-                sum[ct] = fmaf(den, iu[k], sum[ct]);
+            for (int e = 0; e < 4; ++e) {
+                const int at = 8 * (k % 2) + 2 * e;
+                const float y0 = exp2_(fmaf(s[k / 2][at], f[k], shift[k])), y1 = exp2_(fmaf(s[k / 2][at + 1], f[k], shift[k]));
+                den += y0 + y1;
+                const uint2 x = split2(y0, y1, minus);
+                hi[e] = x.x;
+                lo[e] = x.y;
             }
+            w[k] = __builtin_bit_cast(half8_t, hi);
+            wl[k] = __builtin_bit_cast(half8_t, lo);
+            sum = fmaf(den, iu[k], sum);
         }
     };
 
@@ -368,97 +350,80 @@ __device__ __forceinline__ void attend_tall(const Attend &at, float *__restrict_
         __syncthreads();
         if (gr == from) {
 #pragma unroll
-            for (int ct = 0; ct < QT; ++ct) {
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        reinterpret_cast<float4_t *>(all)[((ct * DT + d) * 4 + e) * NT + tid] =
-                            float4_t{o[ct][d][4 * e], o[ct][d][4 * e + 1], o[ct][d][4 * e + 2], o[ct][d][4 * e + 3]};
-                reinterpret_cast<float2 *>(all + QT * DT * 4 * NT)[ct * NT + tid] = make_float2(m[ct], sum[ct]);
-            }
+                for (int e = 0; e < 4; ++e)
+                    reinterpret_cast<float4_t *>(all)[(d * 4 + e) * NT + tid] =
+                        float4_t{o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+            reinterpret_cast<float2 *>(all + DT * 4 * NT)[tid] = make_float2(m, sum);
         }
         __syncthreads();
         if (gr == 0) {
+            const float2 x = reinterpret_cast<const float2 *>(all + DT * 4 * NT)[tid];
+            const float mn = fmaxf(m, x.x), f = exp2_(m - mn), g = exp2_(x.x - mn);
+            m = mn;
+            sum = sum * f + x.y * g;
 #pragma unroll
-            for (int ct = 0; ct < QT; ++ct) {
-                const float2 x = reinterpret_cast<const float2 *>(all + QT * DT * 4 * NT)[ct * NT + tid];
-                const float mn = fmaxf(m[ct], x.x), f = exp2_(m[ct] - mn), g = exp2_(x.x - mn);
-                m[ct] = mn;
-                sum[ct] = sum[ct] * f + x.y * g;
+            for (int d = 0; d < DT; ++d)
 #pragma unroll
-                for (int d = 0; d < DT; ++d)
+                for (int e = 0; e < 4; ++e) {
+                    const float4_t v = reinterpret_cast<const float4_t *>(all)[(d * 4 + e) * NT + tid];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float4_t v = reinterpret_cast<const float4_t *>(all)[((ct * DT + d) * 4 + e) * NT + tid];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[ct][d][4 * e + i] = o[ct][d][4 * e + i] * f + v[i] * g;
-                    }
-            }
+                    for (int i = 0; i < 4; ++i) o[d][4 * e + i] = o[d][4 * e + i] * f + v[i] * g;
+                }
         }
     }
     if (gr != 0) return;
+    float other = sum, den = sum;
+    swap32(den, other);
+    den += other;
+    if (!live) return;
+    const int64_t row = (int64_t)(t.sp.r0 + tok);
+    uint16_t *y = at.O + row * at.o_stride + head * D;
+    float *p = part + ((row * at.H + head) * splits + split) * (D + 4);
 #pragma unroll
-    for (int ct = 0; ct < QT; ++ct) {
-        float other = sum[ct], den = sum[ct];
-        swap32(den, other);
-        den += other;
-        const int w = (wv * QT + ct) * 32 + l, r = r0 + w;
-        if (w >= t.rows) continue;
-        const int64_t row = (int64_t)(t.sp.r0 + r / at.G);
-        const int head = h * at.G + r % at.G;
-        uint16_t *y = at.O + row * at.o_stride + head * D;
-        float *p = part + ((row * at.H + head) * splits + split) * (D + 4);
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4_t v = {o[ct][d][4 * e], o[ct][d][4 * e + 1], o[ct][d][4 * e + 2], o[ct][d][4 * e + 3]};
-                const int at_d = 32 * d + 8 * e + 4 * hf;
-                if (splits == 1) store_row<FMT>(y + at_d, v, den);
-                else *reinterpret_cast<float4_t *>(p + at_d) = v;
-            }
-        if (splits > 1 && hf == 0) {
-            p[D] = m[ct];
-            p[D + 1] = den;
+        for (int e = 0; e < 4; ++e) {
+            const float4_t v = {o[d][4 * e], o[d][4 * e + 1], o[d][4 * e + 2], o[d][4 * e + 3]};
+            const int at_d = 32 * d + 8 * e + 4 * hf;
+            if (splits == 1) store_row<FMT>(y + at_d, v, den);
+            else *reinterpret_cast<float4_t *>(p + at_d) = v;
         }
+    if (splits > 1 && hf == 0) {
+        p[D] = m;
+        p[D + 1] = den;
     }
 }
 
 // Workgroups: key/value head and sequence (fastest: the tiles of one head go to one XCD where their number is a multiple of 8),
 // split, row tile, the last one (which sees most) first.
-template <int D, int FMT, int QT, int NW, int NG>
-__global__ __launch_bounds__(64 * NW * NG, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, const AttendPlan p,
-                                                                                const Grid gd)
+template <int D, int FMT, int NG>
+__global__ __launch_bounds__(64 * kWaves * NG, D == 256 ? 1 : 2) void k_attend_tall(const Attend at, float *__restrict__ part, const AttendPlan p,
+                                                                                    const Grid gd)
 {
     __shared__ u32x4 lds[NG * kTallLds<D>];
-    static_assert(NG <= 2 && (NG == 1 || NG * kTallLds<D> >= QT * (D / 32) * 4 * 64 * NW + QT * 32 * NW), "the groups' sums");
+    static_assert(NG <= 2 && (NG == 1 || NG * kTallLds<D> >= (D / 32) * 4 * 64 * kWaves + 32 * kWaves), "the groups' sums");
     const uint32_t pairs = gd.seqs * at.c.heads, k = blockIdx.x % pairs, n = blockIdx.x / pairs;
     const int tile = gd.tile0 + gd.tiles - 1 - (int)(n / p.splits);
-    attend_tall<D, FMT, QT, NW, NG>(at, part, p.splits, p.chunk, (int)(n % p.splits), (int)(k % at.c.heads), tile * (32 * QT * NW),
-                                    gd.seq0 + (int)(k / at.c.heads), lds);
+    attend_tall<D, FMT, NG>(at, part, p.splits, p.chunk, (int)(n % p.splits), (int)(k % at.c.heads), tile * kTallRows,
+                            gd.seq0 + (int)(k / at.c.heads), lds);
 }
 
 }  // namespace
 
-int tall_height(int dim)
-{
-    return dim == 64 ? 32 * kTallCols<64> * kTallWaves<64> : dim == 128 ? 32 * kTallCols<128> * kTallWaves<128>
-                                                                        : 32 * kTallCols<256> * kTallWaves<256>;
-}
-
 void launch_attend_tall(const Attend &at, const AttendPlan &p, float *part, hipStream_t s)
 {
     auto go = [&](auto dim, auto fmt) {
-        constexpr int D = decltype(dim)::value, F = decltype(fmt)::value, NW = kTallWaves<D>;
+        constexpr int D = decltype(dim)::value, F = decltype(fmt)::value;
         for_grids(at.sq.B, p.tiles, (int64_t)at.c.heads * p.splits, [&](const Grid &gd, uint32_t groups) {
             if constexpr (D < 256) {
                 if (p.pair) {
-                    k_attend_tall<D, F, kTallCols<D>, NW, 2><<<groups, 128 * NW, 0, s>>>(at, part, p, gd);
+                    k_attend_tall<D, F, 2><<<groups, 128 * kWaves, 0, s>>>(at, part, p, gd);
                     return;
                 }
             }
-            k_attend_tall<D, F, kTallCols<D>, NW, 1><<<groups, 64 * NW, 0, s>>>(at, part, p, gd);
+            k_attend_tall<D, F, 1><<<groups, 64 * kWaves, 0, s>>>(at, part, p, gd);
         });
     };
     auto dims = [&](auto fmt) {
