@@ -126,3 +126,23 @@ def test_any_far_scores(n):
                         best = v[np.argmax(x)]
                         near(got[t, h], best, 2.0 ** -11 * np.abs(best) + 2.0 ** -25, (fmt, D, t))
             assert sure > n
+
+
+@pytest.mark.parametrize("n", [2, 6, 40])
+def test_scores_past_fp32_spoil_only_their_rows(n):
+    """Every other row's query is 0 (all its scores are 0): the mean of what it sees, whatever becomes of the rows beside it."""
+    rng = np.random.default_rng([73, n])
+    for fmt in (ref.INT8, ref.E4M3):
+        for scale in (3e38, -3e38, 1e36):
+            L = 100
+            b = ref.Batch(rng, [n], [L], 1, 64, 16, fmt)
+            b.ks[:] = 512.0
+            Q = (rng.uniform(-1, 1, (n, 3, 64)) * 65504).astype(np.float16)
+            Q[:, 1] = 0
+            cache, seqs = b.on_gpu()
+            got, v = host(tri.cache_attend(cache, seqs, cuda(Q), scale=scale)), values(b, L)
+            for t in range(n):
+                x = v[:L - n + t + 1]
+                tol = 2.0 ** -11 * np.abs(x.mean(0)) + 2.0 ** -25 + (64 + L / 8) * 2.0 ** -23 * np.abs(x).mean(0)
+                tol = tol + 2.0 ** -21 * np.abs(x).mean(0) + 2.0 ** -35 * np.abs(x).sum(0)    # weights of two fp16 numbers
+                near(got[t, 1], x.mean(0), tol, (fmt, scale, t))
