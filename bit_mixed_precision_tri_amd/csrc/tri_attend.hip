@@ -379,7 +379,7 @@ AttendPlan plan_of(const tri_cache &c, const tri_sequences &sq, int T, int H, in
     const int64_t groups = sq.B * c.heads * p.tiles, cus = cu_count();
     // Tall tiles: one pass over a tile's steps, unless the tiles leave half the CUs idle (what joins splits moves as much as many
     // steps do).  Up to two tiles per CU, the longest tile's steps are what the call waits for: two groups of waves share them
-    // (2048 tokens of 32 heads, 512 tiles: 62 us without, 57 with; 880 tiles over a window: 97 us without, 114 with).
+    // (2048 tokens of 32 heads, 512 tiles: 75 us without, 68 with; 1008 tiles over a window: 119 us without, 137 with).
     p.pair = p.tall && groups <= 2 * cus;
     const int64_t want = p.tall ? (groups * 2 > cus ? 1 : cus / groups) : (cus + groups - 1) / groups;
     int64_t chunk = (steps + want - 1) / want;

@@ -8,12 +8,14 @@
 //
 // A weight is the sum of two fp16 numbers, each a product with the values' codes: as one alone it would be off by up to 2^-11,
 // more than the scores are, and than the rounding of a result where values cancel; a call's size would show in its results.  The
-// third product of a step costs 2048 tokens of 32 heads 57.5 -> 65 - 70 us, 1000 over a window of 1024 101 -> 114 - 119.
+// third product of a step costs 2048 tokens of 32 heads 57.5 -> 66 us, 1000 over a window of 1024 101 -> 115, long contexts, which the
+// matrix cores bound, up to 29% (2048 over 16384: 621 -> 800).  In which order the two products of the weights are issued changes nothing.
 //
-// What bounds it is that the softmax and the decoding (vector ALU) and the products (matrix cores) overlap only across the two
-// waves of a SIMD.  2048 tokens of 32 heads of 128 (34.4 GFLOP below the diagonal) take 65 us, 525 TFLOP/s; 1000 tokens over a
-// window of 1024, 64 heads (59.6 GFLOP), 114, 521.  Measured and not taken, with one product of the weights (57.5 us): the groups in
-// strict turns with two barriers a round (67 - 76), one step's weights beside the last step's values in a wave (60).
+// Otherwise the softmax and the decoding (vector ALU) and the products (matrix cores) overlap only across the two waves of a SIMD,
+// and waves wait a third of their cycles (barriers, the ends of tiles of uneven length).  2048 tokens of 32 heads of 128 (34.4 GFLOP
+// below the diagonal) take 64 - 69 us from card to card, 500 - 535 TFLOP/s; 1000 tokens over a window of 1024, 64 heads (59.6
+// GFLOP), 113 - 119, 500 - 530.  Measured and not taken, with one product of the weights (57.5 us): the groups in strict turns with
+// two barriers a round (67 - 76), one step's weights beside the last step's values in a wave (60).
 #include "tri_attend.h"
 
 namespace tri {
